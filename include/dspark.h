@@ -302,6 +302,93 @@ dspark_status dspark_markov_draft_noalloc(int B, int gamma, int V, int r, int d,
                                           void* stream);
 
 /*
+ * Log probabilities of given tokens on N rows of logits, with entropy, rank and the most likely
+ * alternatives: what a verified block (dspark_verify's out_tokens) is scored with, and the
+ * forward half of a likelihood or policy objective of the drafter.  For row i with logits z,
+ * m = max_v z_v and x = tokens[i]:
+ *   norm[i] = (m, ln sum_v exp((z_v - m) / T)),   ln p_v = (z_v - m) / T - norm[i][1],
+ *   logp[i] = ln p_x,   entropy[i] = -sum_v p_v ln p_v,   rank[i] = 1 + #{v : z_v > z_x},
+ *   top_ids[i][k], top_logp[i][k]: the k-th largest logit's entry and its ln p, the lower entry
+ *   first among equal logits.
+ * Arguments:
+ *   logits     rows of V elements of type zdt, `ld` elements apart (ld >= V: a padded vocabulary);
+ *              aligned to their type only (16-byte aligned rows are read fastest)
+ *   tokens     [N] int32, or NULL when neither logp nor rank is given.  -1: no token, logp and rank 0
+ *              (out_tokens pads with -1).  Another value outside [0, V): logp NaN, rank -1 and
+ *              DSPARK_ERR_INVALID in the workspace status; other rows are unaffected.
+ *   outputs    logp [N], norm [N][2], entropy [N] fp32, rank [N] int32, each optional; top_ids
+ *              [N][top] int32 and top_logp [N][top] fp32, 0 <= top <= min(32, V)
+ *   workspace  dspark_token_logprobs_workspace_bytes(N, V, top) bytes, 256-byte aligned, zeroed once
+ *              before the first call; every call leaves it ready for the next
+ * Masked entries are -inf (or the type's lowest number): p = 0.  They are never alternatives when
+ * -inf; positions past the last alternative hold -1 and -inf.  A row that is -inf everywhere has
+ * norm (-inf, 0), entropy 0 and logp -inf.  NaN or +inf logits make their row's norm[1], logp and
+ * entropy NaN; NaN entries are not alternatives and count in no rank.  N = 0 does nothing.  Sums run
+ * in a fixed order: the same inputs give the same bits.
+ */
+size_t dspark_token_logprobs_workspace_bytes(int N, int V, int top);
+dspark_status dspark_token_logprobs(int N, int V, float T, dspark_dtype zdt, const void* logits, int64_t ld,
+                                    const int32_t* tokens, int top, float* logp, float* norm,
+                                    float* entropy, int32_t* rank, int32_t* top_ids, float* top_logp,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of dspark_token_logprobs' logp and entropy with respect to the logits:
+ *   grad_logits[i][v] = (1 / T) (g ([v == x] - p_v) - h p_v (ln p_v + entropy[i])),
+ * g = grad_logp[i] (0 where tokens[i] = -1), h = grad_entropy[i].  norm and entropy are the forward
+ * call's.  At least one of grad_logp (with tokens) and grad_entropy (with entropy) is given, fp32 [N].
+ * grad_logits: rows of V elements of type zdt, grad_ld elements apart; it may be `logits` itself
+ * when grad_ld == ld.  A token outside [-1, V) makes its row's gradient NaN; a row that is -inf
+ * everywhere has a zero gradient but for the token's g / T.  One launch, no workspace.
+ */
+dspark_status dspark_token_logprobs_grad(int N, int V, float T, dspark_dtype zdt, const void* logits,
+                                         int64_t ld, const int32_t* tokens, const float* norm,
+                                         const float* entropy, const float* grad_logp,
+                                         const float* grad_entropy, void* grad_logits, int64_t grad_ld,
+                                         void* stream);
+
+/*
+ * Rows of a table for given tokens, scaled (Eq 5's W1[x_{k-1}], an input embedding):
+ *   out[i] = scale * W[tokens[i]],  zero for tokens[i] = -1 (padding), NaN for another token outside
+ *   [0, V) (no status word; no workspace needed).
+ * W [V][D] of type wdt, tokens [N] int32, out [N][D] of type odt (rounded once).  Any D >= 1; arrays
+ * aligned to their type (16-byte aligned rows move fastest).  N = 0 does nothing.  One launch.
+ */
+dspark_status dspark_embedding(int N, int V, int D, float scale, dspark_dtype wdt, const void* W,
+                               const int32_t* tokens, dspark_dtype odt, void* out, void* stream);
+
+/*
+ * The table's gradient for dspark_embedding:
+ *   grad_W[v] = scale * sum_{i : tokens[i] = v} grad[i],
+ * every sum in fp32 and in an order that depends on the tokens alone (the same inputs give the same
+ * bits; no floating-point atomics).  grad [N][D] of type gdt, grad_W [V][D] of type odt (rounded
+ * once).  accumulate = 0 writes every row (zero for tokens that do not occur); otherwise the sums are
+ * added to grad_W and other rows are neither read nor written.  tokens[i] = -1 adds nothing; another
+ * token outside [0, V) adds nothing and sets DSPARK_ERR_INVALID in the workspace status.
+ * workspace: dspark_embedding_grad_workspace_bytes(N, V, D) bytes, 256-byte aligned, zeroed once.
+ */
+size_t dspark_embedding_grad_workspace_bytes(int N, int V, int D);
+dspark_status dspark_embedding_grad(int N, int V, int D, float scale, dspark_dtype gdt, const void* grad,
+                                    const int32_t* tokens, dspark_dtype odt, void* grad_W, int accumulate,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of the low-rank bias product B = a W2 of Eq 5 (a = W1[x_{k-1}]) and Eq 6 (a = tanh(o)):
+ *   grad_a[n][j] = sum_v G[n][v] W2[v][j],   grad_W2[v][j] = sum_n G[n][v] a[n][j].
+ * G [N][V] of type gdt: gradients of the logits (dspark_draft_loss's grad_logits, or
+ * dspark_token_logprobs_grad's); a [N][r] and W2 ([V][r] or [r][V], w2_layout) of type wdt; grad_a
+ * [N][r] and grad_W2 (W2's layout) fp32, each optional (at least one).  accumulate != 0 adds to
+ * grad_W2 (not to grad_a) instead of writing it.  All arrays 16-byte aligned.  Sums in fp32 in a fixed
+ * order.  workspace: dspark_bias_grad_workspace_bytes(N, V, r, wdt) bytes, 256-byte aligned, zeroed
+ * once.  Limits: r a multiple of 8 in 8..512, 2 <= V <= 2^24, 0 <= N <= 2^24 (N = 0: zero gradients).
+ */
+size_t dspark_bias_grad_workspace_bytes(int N, int V, int r, dspark_dtype wdt);
+dspark_status dspark_bias_grad(int N, int V, int r, dspark_dtype gdt, const void* G, dspark_dtype wdt,
+                               const void* a, const void* W2, dspark_w2_layout w2_layout, float* grad_a,
+                               float* grad_W2, int accumulate, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/*
  * Synchronises `stream`, returns the device status word of `workspace` (the most severe error
  * any draft call recorded since the last read, DSPARK_OK if none) and resets the workspace so
  * the next call starts clean.  DSPARK_ERR_CUDA if the synchronisation itself fails.

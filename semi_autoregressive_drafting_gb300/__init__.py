@@ -13,6 +13,7 @@ h (hidden states [B][gamma][d]), x0 (anchors [B]).
 """
 from __future__ import annotations
 
+from contextlib import nullcontext
 from dataclasses import dataclass
 
 import torch
@@ -22,7 +23,11 @@ from . import _lib
 __all__ = ["Workspace", "markov_draft", "rnn_draft", "confidence", "tv_label",
            "prefix_schedule", "draft_path", "draft_launches", "draft_loss_launches",
            "DraftOutput", "DraftPlan",
-           "VerifyWorkspace", "verify", "LossWorkspace", "draft_loss", "sts", "CapacityRing"]
+           "VerifyWorkspace", "verify", "LossWorkspace", "draft_loss", "sts", "CapacityRing",
+           "LogprobWorkspace", "LogprobOutput", "LogprobPlan", "token_logprobs",
+           "LogprobGradPlan", "token_logprobs_grad", "EmbeddingPlan", "embedding",
+           "EmbeddingGradWorkspace", "EmbeddingGradPlan", "embedding_grad",
+           "BiasGradWorkspace", "BiasGradPlan", "bias_grad"]
 
 _F32, _BF16 = 0, 1
 _W2_LAYOUT = {"vr": 0, "rv": 1}
@@ -52,8 +57,8 @@ def _ptr(t):
     return t.data_ptr()
 
 
-def _stream(stream) -> int | None:
-    s = stream if stream is not None else torch.cuda.current_stream()
+def _stream(stream, device=None) -> int | None:
+    s = stream if stream is not None else torch.cuda.current_stream(device)
     return s.cuda_stream
 
 
@@ -326,6 +331,312 @@ def sts(conf_logits, accepted, grid, *, bins=15, stream=None):
                           _stream(stream))
     _lib.check(code, "dspark_sts")
     return tau, ece, eg, ws.status(stream)
+
+
+class _Plan:
+    """A call with its arguments checked and marshalled once: ``run()`` enqueues it again with the
+    same input and output buffers (one C call, no per-call allocation or checks) and returns
+    ``out``.  ``stream`` (a torch stream) overrides the one given at construction.
+
+    What a plan allocates (outputs, workspace) belongs to its stream: given ``stream``, it is
+    allocated and cleared there, and the inputs are recorded as in use on it."""
+
+    def _set(self, name, args, stream, out, keep, device):
+        if stream is not None:
+            for t in keep:
+                if isinstance(t, torch.Tensor):
+                    t.record_stream(stream)
+        self._fn = getattr(_lib.load(), name)
+        self._where = name
+        self._args = (*args, _stream(stream, device))
+        self.out = out
+        self._keep = keep   # every tensor whose address is baked into the arguments stays alive
+
+    def run(self, stream=None):
+        args = self._args if stream is None else self._args[:-1] + (stream.cuda_stream,)
+        code = self._fn(*args)
+        if code != 0:
+            _lib.check(code, self._where)
+        return self.out
+
+
+def _on(stream):
+    """The context in which a plan's own tensors are allocated."""
+    return torch.cuda.stream(stream) if stream is not None else nullcontext()
+
+
+def _same_device(*tensors):
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("libdspark takes device tensors")
+        if dev is not None and t.device != dev:
+            raise ValueError("all tensors are on one device")
+        dev = t.device
+    return dev
+
+
+def _ints(t, shape, name):
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} is int32")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    return _ptr(t)
+
+
+def _f32(t, shape, name):
+    if t is None:
+        return None
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} is float32")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    return _ptr(t)
+
+
+def _logit_rows(z, name):
+    """(leading shape, N, V, row stride, address) of logits [..., V]: the entries of a row are
+    consecutive, and the rows are one stride apart (a slice of a padded vocabulary is fine)."""
+    if z.dim() < 1 or z.shape[-1] < 2:
+        raise ValueError(f"{name} must be [..., V] with V >= 2")
+    if not z.is_cuda:
+        raise ValueError("libdspark takes device tensors")
+    lead, V = tuple(z.shape[:-1]), z.shape[-1]
+    N = 1
+    for n in lead:
+        N *= n
+    if N == 0:
+        return lead, 0, V, V, None
+    if z.stride(-1) != 1:
+        raise ValueError(f"the entries of a row of {name} are consecutive in memory")
+    ld = None   # the stride of the flattened leading dimensions
+    inner = 1
+    for n, st in zip(reversed(lead), reversed(z.stride()[:-1])):
+        if n == 1:
+            continue
+        if ld is None:
+            ld = st
+        elif st != ld * inner:
+            raise ValueError(f"the rows of {name} are not one stride apart: make it contiguous")
+        inner *= n
+    ld = V if ld is None else ld
+    if ld < V:
+        raise ValueError(f"the rows of {name} overlap")
+    return lead, N, V, ld, z.data_ptr()
+
+
+class LogprobWorkspace(Workspace):
+    """Zero-initialised device scratch for ``token_logprobs`` (shapes up to N rows, V, top)."""
+
+    def __init__(self, N: int, V: int, top: int = 0, device=None):
+        n = _lib.load().dspark_token_logprobs_workspace_bytes(N, V, top)
+        if n == 0:
+            raise ValueError("invalid token_logprobs shape for a workspace")
+        self.nbytes = int(n)
+        self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=device or "cuda")
+
+
+@dataclass
+class LogprobOutput:
+    logp: torch.Tensor            # [...] ln p of the given token
+    norm: torch.Tensor            # [..., 2] (largest logit, ln sum exp((z - largest) / T))
+    entropy: torch.Tensor         # [...]
+    rank: torch.Tensor            # [...] int32, 1 for the largest logit
+    top_ids: torch.Tensor | None  # [..., top] int32, -1 past the last alternative
+    top_logp: torch.Tensor | None  # [..., top]
+
+
+class LogprobPlan(_Plan):
+    """``token_logprobs`` with its arguments marshalled once (see ``_Plan``)."""
+
+    def __init__(self, logits, tokens, *, T=1.0, top=0, workspace=None, stream=None, out=None):
+        dev = _same_device(logits, tokens)
+        zdt = _dtype_code(logits)
+        lead, N, V, ld, zp = _logit_rows(logits, "logits")
+        if not 0 <= top <= min(32, V):
+            raise ValueError("top must be 0..min(32, V)")
+        tp = _ints(tokens, lead, "tokens")
+        with _on(stream):
+            ws = workspace or LogprobWorkspace(N, V, top, device=dev)
+            if out is None:
+                def new(*shape, dtype=torch.float32):
+                    return torch.empty(*lead, *shape, dtype=dtype, device=dev)
+                out = LogprobOutput(new(), new(2), new(), new(dtype=torch.int32),
+                                    new(top, dtype=torch.int32) if top else None, new(top) if top else None)
+        _same_device(logits, out.logp, out.norm, out.entropy, out.rank, out.top_ids, out.top_logp)
+        args = (N, V, float(T), zdt, zp, ld, tp, top, _f32(out.logp, lead, "logp"),
+                _f32(out.norm, (*lead, 2), "norm"), _f32(out.entropy, lead, "entropy"),
+                _ints(out.rank, lead, "rank"),
+                _ints(out.top_ids, (*lead, top), "top_ids") if top else None,
+                _f32(out.top_logp, (*lead, top), "top_logp") if top else None, ws.buf.data_ptr(), ws.nbytes)
+        self.workspace = ws
+        self._set("dspark_token_logprobs", args, stream, out, (logits, tokens, ws), dev)
+
+
+def token_logprobs(logits, tokens, *, T=1.0, top=0, workspace=None, stream=None,
+                   out=None) -> LogprobOutput:
+    """Log probabilities of given tokens under softmax(logits / T), with the entropy, the tokens'
+    ranks and the ``top`` (<= 32) most likely alternatives.  See ``dspark_token_logprobs``.
+
+    logits [..., V] fp32 or bf16 (rows one stride apart), tokens [...] int32, -1 for no token.
+    ``out``: an earlier call's LogprobOutput to write into."""
+    return LogprobPlan(logits, tokens, T=T, top=top, workspace=workspace, stream=stream, out=out).run()
+
+
+class LogprobGradPlan(_Plan):
+    """``token_logprobs_grad`` with its arguments marshalled once (see ``_Plan``)."""
+
+    def __init__(self, logits, tokens, norm, *, T=1.0, grad_logp=None, grad_entropy=None, entropy=None,
+                 stream=None, out=None):
+        if out is None:
+            with _on(stream):
+                out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        dev = _same_device(logits, tokens, norm, entropy, grad_logp, grad_entropy, out)
+        zdt = _dtype_code(logits)
+        lead, N, V, ld, zp = _logit_rows(logits, "logits")
+        if out.dtype != logits.dtype or out.shape != logits.shape:
+            raise ValueError("out has the logits' shape and dtype")
+        if grad_logp is None and grad_entropy is None:
+            raise ValueError("grad_logp or grad_entropy is required")
+        if grad_entropy is not None and entropy is None:
+            raise ValueError("grad_entropy needs the forward call's entropy")
+        _, _, _, gld, gp = _logit_rows(out, "out")
+        args = (N, V, float(T), zdt, zp, ld, _ints(tokens, lead, "tokens"), _f32(norm, (*lead, 2), "norm"),
+                _f32(entropy, lead, "entropy"), _f32(grad_logp, lead, "grad_logp"),
+                _f32(grad_entropy, lead, "grad_entropy"), gp, gld)
+        self._set("dspark_token_logprobs_grad", args, stream, out,
+                  (logits, tokens, norm, entropy, grad_logp, grad_entropy), dev)
+
+
+def token_logprobs_grad(logits, tokens, norm, *, T=1.0, grad_logp=None, grad_entropy=None,
+                        entropy=None, stream=None, out=None):
+    """Gradient of ``token_logprobs``' logp and entropy with respect to the logits, in their dtype.
+
+    ``norm`` and ``entropy`` are the forward call's; grad_logp, grad_entropy [...] fp32 (at least
+    one).  ``out`` may be the logits themselves.  See ``dspark_token_logprobs_grad``."""
+    return LogprobGradPlan(logits, tokens, norm, T=T, grad_logp=grad_logp, grad_entropy=grad_entropy,
+                           entropy=entropy, stream=stream, out=out).run()
+
+
+class EmbeddingPlan(_Plan):
+    """``embedding`` with its arguments marshalled once (see ``_Plan``)."""
+
+    def __init__(self, W, tokens, *, scale=1.0, dtype=None, stream=None, out=None):
+        dev = _same_device(W, tokens, out)
+        V, D = W.shape
+        lead = tuple(tokens.shape)
+        if out is None:
+            with _on(stream):
+                out = torch.empty(*lead, D, dtype=dtype or W.dtype, device=dev)
+        elif tuple(out.shape) != (*lead, D) or (dtype is not None and out.dtype != dtype):
+            raise ValueError("out must be [..., D] of the requested dtype")
+        args = (tokens.numel(), V, D, float(scale), _dtype_code(W), _ptr(W), _ints(tokens, lead, "tokens"),
+                _dtype_code(out), _ptr(out))
+        self._set("dspark_embedding", args, stream, out, (W, tokens), dev)
+
+
+def embedding(W, tokens, *, scale=1.0, dtype=None, stream=None, out=None):
+    """scale * W[tokens]: rows of W [V, D] for tokens [...] int32, zero rows for -1, in ``dtype``
+    (W's by default).  See ``dspark_embedding``."""
+    return EmbeddingPlan(W, tokens, scale=scale, dtype=dtype, stream=stream, out=out).run()
+
+
+class EmbeddingGradWorkspace(Workspace):
+    """Zero-initialised device scratch for ``embedding_grad`` (shapes up to N tokens, V, D)."""
+
+    def __init__(self, N: int, V: int, D: int, device=None):
+        n = _lib.load().dspark_embedding_grad_workspace_bytes(N, V, D)
+        if n == 0:
+            raise ValueError("invalid embedding_grad shape for a workspace")
+        self.nbytes = int(n)
+        self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=device or "cuda")
+
+
+class EmbeddingGradPlan(_Plan):
+    """``embedding_grad`` with its arguments marshalled once (see ``_Plan``)."""
+
+    def __init__(self, grad, tokens, V, *, scale=1.0, dtype=torch.float32, accumulate=False, out=None,
+                 workspace=None, stream=None):
+        dev = _same_device(grad, tokens, out)
+        lead, D = tuple(tokens.shape), grad.shape[-1]
+        if tuple(grad.shape) != (*lead, D):
+            raise ValueError("grad must be [..., D] for tokens [...]")
+        N = tokens.numel()
+        if out is None:
+            if accumulate:
+                raise ValueError("accumulate adds to out: give it")
+            with _on(stream):
+                out = torch.empty(V, D, dtype=dtype, device=dev)
+        elif tuple(out.shape) != (V, D):
+            raise ValueError("out must be [V, D]")
+        with _on(stream):
+            ws = workspace or EmbeddingGradWorkspace(N, V, D, device=dev)
+        args = (N, V, D, float(scale), _dtype_code(grad), _ptr(grad), _ints(tokens, lead, "tokens"),
+                _dtype_code(out), _ptr(out), int(accumulate), ws.buf.data_ptr(), ws.nbytes)
+        self.workspace = ws
+        self._set("dspark_embedding_grad", args, stream, out, (grad, tokens, ws), dev)
+
+
+def embedding_grad(grad, tokens, V, *, scale=1.0, dtype=torch.float32, accumulate=False, out=None,
+                   workspace=None, stream=None):
+    """The table gradient [V, D] of ``embedding``: every token's rows of grad [..., D] summed and
+    scaled; ``accumulate`` adds them to ``out``.  See ``dspark_embedding_grad``."""
+    return EmbeddingGradPlan(grad, tokens, V, scale=scale, dtype=dtype, accumulate=accumulate, out=out,
+                             workspace=workspace, stream=stream).run()
+
+
+class BiasGradWorkspace(Workspace):
+    """Zero-initialised device scratch for ``bias_grad`` (shapes up to N rows, V, r)."""
+
+    def __init__(self, N: int, V: int, r: int, bf16: bool = True, device=None):
+        n = _lib.load().dspark_bias_grad_workspace_bytes(N, V, r, _BF16 if bf16 else _F32)
+        if n == 0:
+            raise ValueError("invalid bias_grad shape for a workspace")
+        self.nbytes = int(n)
+        self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=device or "cuda")
+
+
+class BiasGradPlan(_Plan):
+    """``bias_grad`` with its arguments marshalled once (see ``_Plan``)."""
+
+    def __init__(self, grad_logits, a, W2, *, w2_layout="vr", accumulate=False, out=None, workspace=None,
+                 stream=None):
+        dev = _same_device(grad_logits, a, W2)
+        V, r = grad_logits.shape[-1], a.shape[-1]
+        lead = tuple(grad_logits.shape[:-1])
+        w2c = _w2_code(w2_layout)
+        if tuple(a.shape) != (*lead, r) or tuple(W2.shape) != ((r, V) if w2c == 1 else (V, r)):
+            raise ValueError("a must be [..., r] for grad_logits [..., V], and W2 [V][r] or [r][V] by w2_layout")
+        wdt = _dtype_code(a)
+        if _dtype_code(W2) != wdt:
+            raise TypeError("a and W2 share one dtype")
+        N = 1
+        for n in lead:
+            N *= n
+        if out is None:
+            if accumulate:
+                raise ValueError("accumulate adds to out: give it")
+            with _on(stream):
+                out = (torch.empty(*lead, r, dtype=torch.float32, device=dev),
+                       torch.empty(W2.shape, dtype=torch.float32, device=dev))
+        _same_device(grad_logits, *out)
+        with _on(stream):
+            ws = workspace or BiasGradWorkspace(N, V, r, wdt == _BF16, device=dev)
+        args = (N, V, r, _dtype_code(grad_logits), _ptr(grad_logits), wdt, _ptr(a), _ptr(W2), w2c,
+                _f32(out[0], (*lead, r), "grad_a"), _f32(out[1], W2.shape, "grad_W2"), int(accumulate),
+                ws.buf.data_ptr(), ws.nbytes)
+        self.workspace = ws
+        self._set("dspark_bias_grad", args, stream, tuple(out), (grad_logits, a, W2, ws), dev)
+
+
+def bias_grad(grad_logits, a, W2, *, w2_layout="vr", accumulate=False, out=None, workspace=None,
+              stream=None):
+    """Gradients of the bias product a W2 (Eqs 5, 6) for logit gradients [..., V]: (grad_a [..., r],
+    grad_W2 in W2's layout), fp32; ``accumulate`` adds to ``out[1]``.  See ``dspark_bias_grad``."""
+    return BiasGradPlan(grad_logits, a, W2, w2_layout=w2_layout, accumulate=accumulate, out=out,
+                        workspace=workspace, stream=stream).run()
 
 
 class CapacityRing:

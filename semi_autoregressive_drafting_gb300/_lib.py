@@ -15,6 +15,7 @@ I = ctypes.c_int
 F = ctypes.c_float
 SZ = ctypes.c_size_t
 U64 = ctypes.c_uint64
+I64 = ctypes.c_int64
 
 STATUS = {0: "DSPARK_OK", 1: "DSPARK_ERR_INVALID", 2: "DSPARK_ERR_WORKSPACE",
           3: "DSPARK_ERR_CUDA", 4: "DSPARK_ERR_TIMEOUT", 5: "DSPARK_ERR_UNSUPPORTED"}
@@ -37,6 +38,14 @@ SIGNATURES = {
     "dspark_sts_workspace_bytes": (SZ, [I, I, I, I]),
     "dspark_sts": (I, [I, I, P, P, I, P, I, P, P, P, P, SZ, P]),
     "dspark_draft_loss": (I, [I, I, I, F, P, P, P, P, F, F, F, P, P, P, P, P, SZ, P]),
+    "dspark_token_logprobs_workspace_bytes": (SZ, [I, I, I]),
+    "dspark_token_logprobs": (I, [I, I, F, I, P, I64, P, I, P, P, P, P, P, P, P, SZ, P]),
+    "dspark_token_logprobs_grad": (I, [I, I, F, I, P, I64, P, P, P, P, P, P, I64, P]),
+    "dspark_embedding": (I, [I, I, I, F, I, P, P, I, P, P]),
+    "dspark_embedding_grad_workspace_bytes": (SZ, [I, I, I]),
+    "dspark_embedding_grad": (I, [I, I, I, F, I, P, P, I, P, I, P, SZ, P]),
+    "dspark_bias_grad_workspace_bytes": (SZ, [I, I, I, I]),
+    "dspark_bias_grad": (I, [I, I, I, I, P, I, P, P, I, P, P, I, P, SZ, P]),
     "dspark_get_status": (I, [P, SZ, P]),
     "dspark_last_error": (ctypes.c_char_p, []),
     "dspark_draft_path": (I, [I, I, I, I, I]),

@@ -505,6 +505,139 @@ dspark_status dspark_sts(int N, int gamma, const float* conf_logits, const int32
   return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, "sts launch");
 }
 
+size_t dspark_token_logprobs_workspace_bytes(int N, int V, int top) {
+  if (N < 0 || V < 2 || V > (1 << 24) || top < 0 || top > 32 || top > V) return 0;
+  return logprobs_workspace_bytes(N, V, top);
+}
+
+dspark_status dspark_token_logprobs(int N, int V, float T, dspark_dtype zdt, const void* logits, int64_t ld,
+                                    const int32_t* tokens, int top, float* logp, float* norm,
+                                    float* entropy, int32_t* rank, int32_t* top_ids, float* top_logp,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+  g_err.clear();
+  if (N < 0 || V < 2 || V > (1 << 24)) return fail(DSPARK_ERR_INVALID, "bad shape N=%d V=%d", N, V);
+  if (top < 0 || top > 32 || top > V) return fail(DSPARK_ERR_INVALID, "top must be 0..min(32, V), not %d", top);
+  if (!(T > 0.f) || !std::isfinite(T) || !std::isfinite(1.f / T))
+    return fail(DSPARK_ERR_INVALID, "T must be finite and > 0");
+  if (zdt != DSPARK_F32 && zdt != DSPARK_BF16) return fail(DSPARK_ERR_INVALID, "unknown dtype");
+  if (ld < V) return fail(DSPARK_ERR_INVALID, "row stride %lld is below V=%d", (long long)ld, V);
+  if (!logp && !norm && !entropy && !rank && !top) return fail(DSPARK_ERR_INVALID, "no output requested");
+  if (N > 0 && !logits) return fail(DSPARK_ERR_INVALID, "logits are required");
+  if (N > 0 && !tokens && (logp || rank)) return fail(DSPARK_ERR_INVALID, "logp and rank need tokens");
+  if (N > 0 && top && (!top_ids || !top_logp))
+    return fail(DSPARK_ERR_INVALID, "top_ids and top_logp are required with top > 0");
+  if (!aligned(logits, zdt == DSPARK_BF16 ? 2 : 4) || !aligned(norm, 8))
+    return fail(DSPARK_ERR_INVALID, "logits must be aligned to their type and norm to 8 bytes");
+  const size_t need = logprobs_workspace_bytes(N, V, top);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need)
+    return fail(DSPARK_ERR_WORKSPACE, "workspace must be 256-byte aligned and >= %zu bytes", need);
+  if (N == 0) return DSPARK_OK;
+  cudaError_t e = launch_logprobs(N, V, T, zdt == DSPARK_BF16, logits, ld, tokens, top, logp, norm, entropy,
+                                  rank, top_ids, top_logp, workspace, (cudaStream_t)stream);
+  return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, "token logprobs launch");
+}
+
+dspark_status dspark_token_logprobs_grad(int N, int V, float T, dspark_dtype zdt, const void* logits,
+                                         int64_t ld, const int32_t* tokens, const float* norm,
+                                         const float* entropy, const float* grad_logp,
+                                         const float* grad_entropy, void* grad_logits, int64_t grad_ld,
+                                         void* stream) {
+  g_err.clear();
+  if (N < 0 || V < 2 || V > (1 << 24)) return fail(DSPARK_ERR_INVALID, "bad shape N=%d V=%d", N, V);
+  if (!(T > 0.f) || !std::isfinite(T) || !std::isfinite(1.f / T))
+    return fail(DSPARK_ERR_INVALID, "T must be finite and > 0");
+  if (zdt != DSPARK_F32 && zdt != DSPARK_BF16) return fail(DSPARK_ERR_INVALID, "unknown dtype");
+  if (ld < V || grad_ld < V) return fail(DSPARK_ERR_INVALID, "a row stride is below V=%d", V);
+  if (N == 0) return DSPARK_OK;
+  if (!logits || !norm || !grad_logits) return fail(DSPARK_ERR_INVALID, "logits, norm and grad_logits are required");
+  if (!grad_logp && !grad_entropy) return fail(DSPARK_ERR_INVALID, "grad_logp or grad_entropy is required");
+  if (grad_logp && !tokens) return fail(DSPARK_ERR_INVALID, "grad_logp needs tokens");
+  if (grad_entropy && !entropy) return fail(DSPARK_ERR_INVALID, "grad_entropy needs entropy");
+  const size_t es = zdt == DSPARK_BF16 ? 2 : 4;
+  if (!aligned(logits, es) || !aligned(grad_logits, es) || !aligned(norm, 8))
+    return fail(DSPARK_ERR_INVALID, "logits and grad_logits must be aligned to their type and norm to 8 bytes");
+  cudaError_t e = launch_logprobs_grad(N, V, T, zdt == DSPARK_BF16, logits, ld, tokens, norm, entropy,
+                                       grad_logp, grad_entropy, grad_logits, grad_ld, (cudaStream_t)stream);
+  return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, "token logprobs gradient launch");
+}
+
+dspark_status dspark_embedding(int N, int V, int D, float scale, dspark_dtype wdt, const void* W,
+                               const int32_t* tokens, dspark_dtype odt, void* out, void* stream) {
+  g_err.clear();
+  if (N < 0 || V < 1 || V > (1 << 24) || D < 1 || D > (1 << 20))
+    return fail(DSPARK_ERR_INVALID, "bad shape N=%d V=%d D=%d", N, V, D);
+  if (!std::isfinite(scale)) return fail(DSPARK_ERR_INVALID, "scale must be finite");
+  if ((wdt != DSPARK_F32 && wdt != DSPARK_BF16) || (odt != DSPARK_F32 && odt != DSPARK_BF16))
+    return fail(DSPARK_ERR_INVALID, "unknown dtype");
+  if (N == 0) return DSPARK_OK;
+  if (!W || !tokens || !out) return fail(DSPARK_ERR_INVALID, "W, tokens and out are required");
+  if (!aligned(W, wdt == DSPARK_BF16 ? 2 : 4) || !aligned(out, odt == DSPARK_BF16 ? 2 : 4))
+    return fail(DSPARK_ERR_INVALID, "W and out must be aligned to their types");
+  cudaError_t e = launch_embedding(N, V, D, scale, wdt == DSPARK_BF16, W, tokens, odt == DSPARK_BF16, out,
+                                   (cudaStream_t)stream);
+  return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, "embedding launch");
+}
+
+size_t dspark_embedding_grad_workspace_bytes(int N, int V, int D) {
+  if (N < 0 || N > (1 << 24) || V < 1 || V > (1 << 24) || D < 1 || D > (1 << 20)) return 0;
+  return embedding_grad_workspace_bytes(N, V, D);
+}
+
+dspark_status dspark_embedding_grad(int N, int V, int D, float scale, dspark_dtype gdt, const void* grad,
+                                    const int32_t* tokens, dspark_dtype odt, void* grad_W, int accumulate,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+  g_err.clear();
+  if (N < 0 || N > (1 << 24) || V < 1 || V > (1 << 24) || D < 1 || D > (1 << 20))
+    return fail(DSPARK_ERR_INVALID, "bad shape N=%d V=%d D=%d", N, V, D);
+  if (!std::isfinite(scale)) return fail(DSPARK_ERR_INVALID, "scale must be finite");
+  if ((gdt != DSPARK_F32 && gdt != DSPARK_BF16) || (odt != DSPARK_F32 && odt != DSPARK_BF16))
+    return fail(DSPARK_ERR_INVALID, "unknown dtype");
+  if (!grad_W || (N > 0 && (!grad || !tokens)))
+    return fail(DSPARK_ERR_INVALID, "grad, tokens and grad_W are required");
+  if (!aligned(grad, gdt == DSPARK_BF16 ? 2 : 4) || !aligned(grad_W, odt == DSPARK_BF16 ? 2 : 4))
+    return fail(DSPARK_ERR_INVALID, "grad and grad_W must be aligned to their types");
+  const size_t need = embedding_grad_workspace_bytes(N, V, D);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need)
+    return fail(DSPARK_ERR_WORKSPACE, "workspace must be 256-byte aligned and >= %zu bytes", need);
+  cudaError_t e = launch_embedding_grad(N, V, D, scale, gdt == DSPARK_BF16, grad, tokens, odt == DSPARK_BF16,
+                                        grad_W, accumulate != 0, workspace, (cudaStream_t)stream);
+  return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, "embedding gradient launch");
+}
+
+size_t dspark_bias_grad_workspace_bytes(int N, int V, int r, dspark_dtype wdt) {
+  if (N < 0 || N > (1 << 24) || V < 2 || V > (1 << 24) || r < 8 || r > 512 || r % 8) return 0;
+  DevInfo di;
+  if (!dev_info(&di)) return 0;
+  return bias_grad_workspace_bytes(N, V, r, wdt == DSPARK_BF16, di.sms);
+}
+
+dspark_status dspark_bias_grad(int N, int V, int r, dspark_dtype gdt, const void* G, dspark_dtype wdt,
+                               const void* a, const void* W2, dspark_w2_layout w2_layout, float* grad_a,
+                               float* grad_W2, int accumulate, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  g_err.clear();
+  if (N < 0 || N > (1 << 24) || V < 2 || V > (1 << 24) || r < 8 || r > 512 || r % 8)
+    return fail(DSPARK_ERR_INVALID, "bad shape N=%d V=%d r=%d", N, V, r);
+  if ((gdt != DSPARK_F32 && gdt != DSPARK_BF16) || (wdt != DSPARK_F32 && wdt != DSPARK_BF16))
+    return fail(DSPARK_ERR_INVALID, "unknown dtype");
+  if (w2_layout != DSPARK_W2_VR && w2_layout != DSPARK_W2_RV)
+    return fail(DSPARK_ERR_INVALID, "unknown W2 layout %d", (int)w2_layout);
+  if (!grad_a && !grad_W2) return fail(DSPARK_ERR_INVALID, "no output requested");
+  if (N > 0 && (!G || (grad_a && !W2) || (grad_W2 && !a)))
+    return fail(DSPARK_ERR_INVALID, "G is required, W2 with grad_a and a with grad_W2");
+  if (!aligned(G, 16) || !aligned(a, 16) || !aligned(W2, 16) || !aligned(grad_a, 16) || !aligned(grad_W2, 16))
+    return fail(DSPARK_ERR_INVALID, "G, a, W2, grad_a and grad_W2 must be 16-byte aligned");
+  DevInfo di;
+  if (!dev_info(&di)) return fail(DSPARK_ERR_CUDA, "cannot query the current device");
+  const size_t need = bias_grad_workspace_bytes(N, V, r, wdt == DSPARK_BF16, di.sms);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need)
+    return fail(DSPARK_ERR_WORKSPACE, "workspace must be 256-byte aligned and >= %zu bytes", need);
+  cudaError_t e = launch_bias_grad(N, V, r, gdt == DSPARK_BF16, G, wdt == DSPARK_BF16, a, W2,
+                                   w2_layout == DSPARK_W2_RV, grad_a, grad_W2, accumulate != 0, workspace,
+                                   di.sms, (cudaStream_t)stream);
+  return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, "bias gradient launch");
+}
+
 dspark_status dspark_get_status(void* workspace, size_t workspace_bytes, void* stream) {
   g_err.clear();
   if (!workspace || workspace_bytes < sizeof(WsHeader))

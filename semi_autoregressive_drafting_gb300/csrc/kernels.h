@@ -28,5 +28,24 @@ cudaError_t launch_sts(int N, int G, const float* conf, const int32_t* acc, int 
                        cudaStream_t stream);
 cudaError_t launch_prefix_schedule(int B, int G, const float* S, const double* sps, int32_t* len,
                                    double* theta, cudaStream_t stream);
+size_t logprobs_workspace_bytes(int N, int V, int top);
+cudaError_t launch_logprobs(int N, int V, float T, int bf16, const void* logits, long long ld,
+                            const int32_t* tokens, int top, float* logp, float* norm, float* entropy,
+                            int32_t* rank, int32_t* top_ids, float* top_logp, void* workspace,
+                            cudaStream_t stream);
+cudaError_t launch_logprobs_grad(int N, int V, float T, int bf16, const void* logits, long long ld,
+                                 const int32_t* tokens, const float* norm, const float* entropy,
+                                 const float* gl, const float* gh, void* grad, long long gld,
+                                 cudaStream_t stream);
+cudaError_t launch_embedding(int N, int V, int D, float scale, int w_bf16, const void* W,
+                             const int32_t* tokens, int o_bf16, void* out, cudaStream_t stream);
+size_t embedding_grad_workspace_bytes(int N, int V, int D);
+cudaError_t launch_embedding_grad(int N, int V, int D, float scale, int g_bf16, const void* grad,
+                                  const int32_t* tokens, int o_bf16, void* gW, int accumulate,
+                                  void* workspace, cudaStream_t stream);
+size_t bias_grad_workspace_bytes(int N, int V, int r, int w_bf16, int nsm);
+cudaError_t launch_bias_grad(int N, int V, int r, int g_bf16, const void* G, int w_bf16, const void* a,
+                             const void* W2, int w2_rv, float* grad_a, float* grad_W2, int accumulate,
+                             void* workspace, int nsm, cudaStream_t stream);
 
 }  // namespace dspark
