@@ -323,8 +323,9 @@ dspark_status dspark_markov_draft_noalloc(int B, int gamma, int V, int r, int d,
  * Masked entries are -inf (or the type's lowest number): p = 0.  They are never alternatives when
  * -inf; positions past the last alternative hold -1 and -inf.  A row that is -inf everywhere has
  * norm (-inf, 0), entropy 0 and logp -inf.  NaN or +inf logits make their row's norm[1], logp and
- * entropy NaN; NaN entries are not alternatives and count in no rank.  N = 0 does nothing.  Sums run
- * in a fixed order: the same inputs give the same bits.
+ * entropy NaN; NaN entries are not alternatives and count in no rank.  Sums run in a fixed order: the
+ * same inputs give the same bits.  Limits: 0 <= N <= 2^24 (N = 0 does nothing), 2 <= V <= 2^24,
+ * N (V / 4096 + 2) < 2^31.  One launch.
  */
 size_t dspark_token_logprobs_workspace_bytes(int N, int V, int top);
 dspark_status dspark_token_logprobs(int N, int V, float T, dspark_dtype zdt, const void* logits, int64_t ld,
@@ -339,7 +340,8 @@ dspark_status dspark_token_logprobs(int N, int V, float T, dspark_dtype zdt, con
  * call's.  At least one of grad_logp (with tokens) and grad_entropy (with entropy) is given, fp32 [N].
  * grad_logits: rows of V elements of type zdt, grad_ld elements apart; it may be `logits` itself
  * when grad_ld == ld.  A token outside [-1, V) makes its row's gradient NaN; a row that is -inf
- * everywhere has a zero gradient but for the token's g / T.  One launch, no workspace.
+ * everywhere has a zero gradient but for the token's g / T; a row whose norm[1] is NaN has a NaN gradient.
+ * Limits as above.  One launch, no workspace.
  */
 dspark_status dspark_token_logprobs_grad(int N, int V, float T, dspark_dtype zdt, const void* logits,
                                          int64_t ld, const int32_t* tokens, const float* norm,

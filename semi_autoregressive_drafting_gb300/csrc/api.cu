@@ -506,7 +506,7 @@ dspark_status dspark_sts(int N, int gamma, const float* conf_logits, const int32
 }
 
 size_t dspark_token_logprobs_workspace_bytes(int N, int V, int top) {
-  if (N < 0 || V < 2 || V > (1 << 24) || top < 0 || top > 32 || top > V) return 0;
+  if (N < 0 || N > (1 << 24) || V < 2 || V > (1 << 24) || top < 0 || top > 32 || top > V) return 0;
   return logprobs_workspace_bytes(N, V, top);
 }
 
@@ -515,7 +515,8 @@ dspark_status dspark_token_logprobs(int N, int V, float T, dspark_dtype zdt, con
                                     float* entropy, int32_t* rank, int32_t* top_ids, float* top_logp,
                                     void* workspace, size_t workspace_bytes, void* stream) {
   g_err.clear();
-  if (N < 0 || V < 2 || V > (1 << 24)) return fail(DSPARK_ERR_INVALID, "bad shape N=%d V=%d", N, V);
+  if (N < 0 || N > (1 << 24) || V < 2 || V > (1 << 24) || (long long)N * (V / 4096 + 2) >= (1ll << 31))
+    return fail(DSPARK_ERR_INVALID, "bad shape N=%d V=%d", N, V);
   if (top < 0 || top > 32 || top > V) return fail(DSPARK_ERR_INVALID, "top must be 0..min(32, V), not %d", top);
   if (!(T > 0.f) || !std::isfinite(T) || !std::isfinite(1.f / T))
     return fail(DSPARK_ERR_INVALID, "T must be finite and > 0");
@@ -543,7 +544,8 @@ dspark_status dspark_token_logprobs_grad(int N, int V, float T, dspark_dtype zdt
                                          const float* grad_entropy, void* grad_logits, int64_t grad_ld,
                                          void* stream) {
   g_err.clear();
-  if (N < 0 || V < 2 || V > (1 << 24)) return fail(DSPARK_ERR_INVALID, "bad shape N=%d V=%d", N, V);
+  if (N < 0 || N > (1 << 24) || V < 2 || V > (1 << 24) || (long long)N * (V / 4096 + 2) >= (1ll << 31))
+    return fail(DSPARK_ERR_INVALID, "bad shape N=%d V=%d", N, V);
   if (!(T > 0.f) || !std::isfinite(T) || !std::isfinite(1.f / T))
     return fail(DSPARK_ERR_INVALID, "T must be finite and > 0");
   if (zdt != DSPARK_F32 && zdt != DSPARK_BF16) return fail(DSPARK_ERR_INVALID, "unknown dtype");

@@ -9,6 +9,15 @@
 //   dL/dz_v = (1 / T) (g ([v == x] - p_v) - h p_v (ln p_v + H)) for g = dL/dlogp, h = dL/dH.
 // The maximum is subtracted before the scale is applied: a row whose entries are all the type's
 // lowest number is a uniform row, not an overflow.
+//
+// Forward, one launch and one read of the logits: a block takes a 16-byte-aligned chunk of one row,
+// every thread holds its part of it in registers (all loads issued at once), and each warp forms
+// the maximum, then the sums relative to it.  The last block of a row to finish (a counter per row,
+// no waits) merges the chunks' partial results in their order and writes the row's outputs.
+// Alternatives: each warp also leaves the largest entry of its segment.  Any of the K largest
+// entries lies in one of the K segments that lead when ordered by (maximum, position): the K
+// leaders each hold an entry that precedes it otherwise.  So the last block ranks the segments and
+// re-reads K of them, 4 KB each and still in L2, instead of keeping lists during the pass.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -16,96 +25,416 @@ namespace dspark {
 namespace {
 
 constexpr int kPThr = 256;
+constexpr int kPWarps = kPThr / 32;
+constexpr float kPL2e = 1.4426950408889634f;
+constexpr float kPLn2 = 0.6931471805599453f;
+constexpr int kPGroups = 256;   // segment groups ranked at most (one per thread)
+constexpr int kPKeep = 256;     // candidates kept before a cut to the K best
 
-__device__ __forceinline__ float block_max(float v, float* red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = red[0];
-  for (int w = 1; w < kPThr / 32; ++w) v = fmaxf(v, red[w]);
-  return v;
-}
-__device__ __forceinline__ double block_sum(double v, double* red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0.0;
-  for (int w = 0; w < kPThr / 32; ++w) v += red[w];
-  return v;
+__device__ __forceinline__ float ex2p(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// One block per row: a pass for the maximum, one for the sums, one per alternative.
+// Two fp32 values in one 64-bit register pair: one instruction per pair on sm_100 and later.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 un2(F2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// What a type needs: E entries per 16 bytes, the 32-bit word of fill entries (-inf), the largest
+// entry of 16 bytes, and the number of entries above a threshold.
 template <typename T>
-__global__ void __launch_bounds__(kPThr) logprob_kernel(
-    int V, float invT, const T* __restrict__ logits, long long ld, const int32_t* __restrict__ tokens,
-    int top, float* __restrict__ logp, float2* __restrict__ norm, float* __restrict__ entropy,
-    int32_t* __restrict__ rank, int32_t* __restrict__ top_ids, float* __restrict__ top_logp,
-    unsigned* status) {
-  __shared__ float red[kPThr / 32];
-  __shared__ double dred[kPThr / 32];
-  __shared__ unsigned long long kred[kPThr / 32];
-  const long long row = blockIdx.x;
-  const T* z = logits + row * ld;
-  float m = -INFINITY;
-  for (int v = threadIdx.x; v < V; v += kPThr) m = fmaxf(m, to_f<T>(z[v]));
-  m = block_max(m, red);
-  const int x = tokens ? tokens[row] : -1;
-  const bool bad = x < -1 || x >= V;
-  const float zx = x >= 0 && !bad ? to_f<T>(z[x]) : 0.f;
-  double s = 0.0, t = 0.0, c = 0.0;
-  for (int v = threadIdx.x; v < V; v += kPThr) {
-    const float f = to_f<T>(z[v]);
-    const float d = f == -INFINITY ? -INFINITY : (f - m) * invT, e = expf(d);
-    s += e;
-    t += e == 0.f ? 0.0 : (double)e * d;
-    c += f > zx ? 1.0 : 0.0;
+struct Lg;
+template <>
+struct Lg<float> {
+  static constexpr int E = 4;
+  static constexpr uint32_t kFill = 0xFF800000u;
+  struct Thr {
+    float x;
+  };
+  struct Cnt {
+    int n;
+  };
+  __device__ __forceinline__ static float max16(float m, const uint4& q) {
+    return fmaxf(m, fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)),
+                          fmaxf(__uint_as_float(q.z), __uint_as_float(q.w))));
   }
-  s = block_sum(s, dred);
-  t = block_sum(t, dred);
-  c = block_sum(c, dred);
-  const bool none = s == 0.0;  // every entry -inf
-  const float ls = none ? 0.f : (float)log(s);
-  if (threadIdx.x == 0) {
-    if (norm) norm[row] = make_float2(m, ls);
-    if (entropy) entropy[row] = none ? 0.f : (float)(log(s) - t / s);
-    float lp = x < 0 ? 0.f : zx == -INFINITY ? -INFINITY : (zx - m) * invT - ls;
-    if (bad) {
-      lp = NAN;
-      atomicMax(status, kErrInvalid);
-    }
-    if (isnan(s)) lp = x == -1 ? 0.f : NAN;
-    if (logp) logp[row] = lp;
-    if (rank) rank[row] = bad ? -1 : x < 0 ? 0 : (int)c + 1;
+  __device__ __forceinline__ static F2 pair(const uint4& q, int i) {
+    return i == 0 ? f2(__uint_as_float(q.x), __uint_as_float(q.y)) : f2(__uint_as_float(q.z), __uint_as_float(q.w));
   }
-  unsigned long long last = ~0ull;
-  for (int k = 0; k < top; ++k) {
-    unsigned long long best = 0ull;
-    for (int v = threadIdx.x; v < V; v += kPThr) {
-      const float f = to_f<T>(z[v]) + 0.f;
-      const unsigned long long key = f > -INFINITY ? make_key(f, (uint32_t)v) : 0ull;
-      if (key < last && key > best) best = key;
-    }
+  __device__ __forceinline__ static Thr thr(float x) { return Thr{x}; }
+  __device__ __forceinline__ static void above(Cnt& c, const uint4& q, const Thr& t) {
+    c.n += (__uint_as_float(q.x) > t.x ? 1 : 0) + (__uint_as_float(q.y) > t.x ? 1 : 0) +
+           (__uint_as_float(q.z) > t.x ? 1 : 0) + (__uint_as_float(q.w) > t.x ? 1 : 0);
+  }
+  __device__ __forceinline__ static Cnt zero() { return Cnt{0}; }
+  __device__ __forceinline__ static int total(const Cnt& c) { return c.n; }
+};
+template <>
+struct Lg<__nv_bfloat16> {
+  static constexpr int E = 8;
+  static constexpr uint32_t kFill = 0xFF80FF80u;
+  struct Thr {
+    __nv_bfloat162 x;
+  };
+  struct Cnt {
+    __nv_bfloat162 n;  // counts of up to 2 x 256 entries are exact
+  };
+  __device__ __forceinline__ static __nv_bfloat162 b2(uint32_t w) {
+    __nv_bfloat162 r;
+    memcpy(&r, &w, 4);
+    return r;
+  }
+  __device__ __forceinline__ static float max16(float m, const uint4& q) {
+    const __nv_bfloat162 a = __hmax2(__hmax2(b2(q.x), b2(q.y)), __hmax2(b2(q.z), b2(q.w)));
+    return fmaxf(m, fmaxf(__low2float(a), __high2float(a)));
+  }
+  __device__ __forceinline__ static F2 pair(const uint4& q, int i) {
+    const uint32_t w = i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w;
+    return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+  __device__ __forceinline__ static Thr thr(float x) { return Thr{__float2bfloat162_rn(x)}; }
+  __device__ __forceinline__ static void above(Cnt& c, const uint4& q, const Thr& t) {
+    c.n = __hadd2(c.n, __hadd2(__hadd2(__hgt2(b2(q.x), t.x), __hgt2(b2(q.y), t.x)),
+                               __hadd2(__hgt2(b2(q.z), t.x), __hgt2(b2(q.w), t.x))));
+  }
+  __device__ __forceinline__ static Cnt zero() { return Cnt{__float2bfloat162_rn(0.f)}; }
+  __device__ __forceinline__ static int total(const Cnt& c) {
+    return (int)(__low2float(c.n) + __high2float(c.n));
+  }
+};
+
+// The 16 bytes of a row whose first entry is v0 (16-byte aligned; v0 < 0 in front of a row that
+// starts inside them): entries outside [0, V) are not read, and are -inf.
+template <typename T>
+__device__ __forceinline__ uint4 load16(const T* z, int v0, int V) {
+  constexpr int E = Lg<T>::E;
+  if (v0 >= 0 && v0 + E <= V) return __ldg((const uint4*)(z + v0));
+  uint32_t w[4];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const unsigned long long q = __shfl_xor_sync(0xffffffffu, best, o);
-      best = q > best ? q : best;
+  for (int i = 0; i < 4; ++i) {
+    if (E == 4) {
+      w[i] = v0 + i >= 0 && v0 + i < V ? ((const uint32_t*)z)[v0 + i] : Lg<T>::kFill;
+    } else {
+      const int a = v0 + 2 * i;
+      const uint32_t lo = a >= 0 && a < V ? ((const uint16_t*)z)[a] : (Lg<T>::kFill & 0xFFFFu);
+      const uint32_t hi = a + 1 >= 0 && a + 1 < V ? ((const uint16_t*)z)[a + 1] : (Lg<T>::kFill & 0xFFFFu);
+      w[i] = lo | (hi << 16);
     }
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) kred[threadIdx.x >> 5] = best;
-    __syncthreads();
-    for (int w = 0; w < kPThr / 32; ++w) best = kred[w] > best ? kred[w] : best;
-    if (threadIdx.x == 0) {
-      top_ids[row * top + k] = best ? (int32_t)key_token(best) : -1;
-      top_logp[row * top + k] = best ? (key_score(best) - m) * invT - ls : -INFINITY;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// entries between the 16-byte boundary at or below a row's start and the start
+template <typename T>
+__device__ __forceinline__ int row_head(const T* z) {
+  return (int)(((uintptr_t)z & 15) / sizeof(T));
+}
+
+// A set of entries: maximum, S = sum 2^y and A = sum y 2^y with y = (z - m) log2(e) / T, and the
+// number of entries above the token's.
+struct Part {
+  float m, S, A;
+  int c;
+};
+__device__ __forceinline__ void part_merge(Part& a, const Part& b, float s2) {
+  const float m = fmaxf(a.m, b.m);
+  // shifts in the same units; an empty side (maximum -inf) is left out, so is one that underflows
+  const float da = a.m == -INFINITY ? -256.f : fmaxf((a.m - m) * s2, -256.f);
+  const float db = b.m == -INFINITY ? -256.f : fmaxf((b.m - m) * s2, -256.f);
+  const float wa = ex2p(da), wb = ex2p(db);
+  const float S = a.S * wa + b.S * wb;
+  a.A = fmaf(a.S, da, a.A) * wa + fmaf(b.S, db, b.A) * wb;
+  a.S = S;
+  a.m = m;
+  a.c += b.c;
+}
+__device__ __forceinline__ Part part_shfl(const Part& p, int o) {
+  Part q;
+  q.m = __shfl_xor_sync(0xffffffffu, p.m, o);
+  q.S = __shfl_xor_sync(0xffffffffu, p.S, o);
+  q.A = __shfl_xor_sync(0xffffffffu, p.A, o);
+  q.c = __shfl_xor_sync(0xffffffffu, p.c, o);
+  return q;
+}
+
+struct LpWs {
+  WsHeader* hdr;
+  unsigned* count;  // [N] blocks of the row done; zero between calls
+  Part* part;       // [N][nchunk]
+  float* seg;       // [N][nchunk][8] largest entry of each warp's segment (with alternatives)
+};
+
+struct LpArgs {
+  int V, nchunk, top;
+  float invT;
+  long long ld;
+  const int32_t* tokens;
+  float* logp;
+  float2* norm;
+  float* entropy;
+  int32_t* rank;
+  int32_t* top_ids;
+  float* top_logp;
+  LpWs ws;
+};
+
+// Shared memory of the alternatives' search.
+struct TopSm {
+  uint32_t gkey[kPGroups];                 // largest entry of each segment group, orderable
+  int list[32];                            // the leading groups, best first
+  unsigned long long buf[kPKeep + kPThr * 8];
+  unsigned long long cut;                  // candidates below this are out
+  int n;
+};
+
+// Keeps the K largest of the n candidates, sorted, and raises the cut to the K-th.
+__device__ __forceinline__ void top_prune(TopSm& t, int K) {
+  const int n = t.n;
+  constexpr int kPer = (kPKeep + kPThr * 8 + kPThr - 1) / kPThr;
+  unsigned long long k[kPer];
+  int r[kPer];
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int i = (int)threadIdx.x + u * kPThr;
+    k[u] = i < n ? t.buf[i] : 0ull;
+    r[u] = i < n ? 0 : K;
+    if (u * kPThr < n)
+      for (int j = 0; j < n; ++j) r[u] += t.buf[j] > k[u] ? 1 : 0;  // (keys differ: ranks do too)
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < kPer; ++u)
+    if (r[u] < K) {
+      t.buf[r[u]] = k[u];
+      if (r[u] == K - 1) t.cut = k[u];
     }
-    last = best ? best : 1ull;
+  if (threadIdx.x == 0) t.n = min(n, K);
+  __syncthreads();
+}
+
+// The K alternatives of a row, by the whole block (the row's last one).
+template <typename T, int PER>
+__device__ __forceinline__ void top_search(TopSm& t, const LpArgs& a, const T* z, int head, long long row,
+                                           float m, float ls) {
+  constexpr int E = Lg<T>::E;
+  constexpr int kSeg = 32 * PER;  // 16-byte groups per segment
+  const int K = a.top, tid = (int)threadIdx.x;
+  const int nseg = a.nchunk * kPWarps;
+  const int g = (nseg + kPGroups - 1) / kPGroups;  // segments per group
+  const int ng = (nseg + g - 1) / g;
+  const float* seg = a.ws.seg + row * nseg;
+  float mx = -INFINITY;
+  if (tid < ng)
+    for (int i = tid * g; i < min(nseg, tid * g + g); ++i) mx = fmaxf(mx, __ldcg(seg + i));
+  const uint32_t key = orderable(mx + 0.f);
+  t.gkey[tid] = tid < ng ? key : 0u;
+  if (tid < 32) t.list[tid] = -1;
+  if (tid == 0) {
+    t.n = 0;
+    t.cut = 1ull;
+  }
+  __syncthreads();
+  // rank among the groups: larger maximum first, then the lower position
+  if (tid < ng && mx != -INFINITY) {
+    int r = 0;
+    for (int j = 0; j < ng; ++j) r += t.gkey[j] > key - (j < tid ? 1u : 0u) ? 1 : 0;
+    if (r < K) {
+      t.list[r] = tid;
+      // no entry below the K-th group's largest can be among the K (its index: not after the group)
+      if (r == K - 1) t.cut = ((unsigned long long)key << 32) | (0xFFFFFFFFull - (uint32_t)min(a.V - 1, (tid + 1) * g * kSeg * E));
+    }
+  }
+  __syncthreads();
+  const int steps = (g * kSeg + kPThr - 1) / kPThr;
+  for (int r0 = 0; r0 < K && t.list[r0] >= 0; ++r0) {
+    const int first = t.list[r0] * g * kSeg;
+    for (int s = 0; s < steps; ++s) {
+      const int i = s * kPThr + tid;
+      if (i < g * kSeg) {
+        const int v0 = (first + i) * E - head;
+        if (v0 < a.V) {
+          const uint4 q = load16<T>(z, v0, a.V);
+          const unsigned long long cut = t.cut;
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) {
+            const float2 f = un2(Lg<T>::pair(q, e));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float x = (h ? f.y : f.x) + 0.f;
+              if (x > -INFINITY) {
+                const unsigned long long k = make_key(x, (uint32_t)(v0 + 2 * e + h));
+                if (k >= cut) t.buf[atomicAdd(&t.n, 1)] = k;
+              }
+            }
+          }
+        }
+      }
+      __syncthreads();
+      const bool full = t.n > kPKeep;
+      __syncthreads();  // (every thread has read the count before the next candidates add to it)
+      if (full) top_prune(t, K);
+    }
+  }
+  top_prune(t, K);
+  if (tid < K) {
+    const bool has = tid < t.n;
+    const unsigned long long k = has ? t.buf[tid] : 0ull;
+    a.top_ids[row * K + tid] = has ? (int32_t)key_token(k) : -1;
+    a.top_logp[row * K + tid] = has ? fmaf(key_score(k) - m, a.invT, -ls) : -INFINITY;
   }
 }
 
+template <typename T, int PER, bool TOP>
+__global__ void __launch_bounds__(kPThr) logprob_kernel(const T* __restrict__ logits, const LpArgs a) {
+  constexpr int E = Lg<T>::E;
+  __shared__ Part red[kPWarps];
+  __shared__ float fin[2];
+  __shared__ int s_last;
+  __shared__ __align__(16) unsigned char top_raw[TOP ? sizeof(TopSm) : 16];
+  const long long row = blockIdx.x / (unsigned)a.nchunk;
+  const int ch = (int)(blockIdx.x % (unsigned)a.nchunk);
+  const int lane = (int)(threadIdx.x & 31), warp = (int)(threadIdx.x >> 5);
+  const T* z = logits + row * a.ld;
+  const int head = row_head(z), V = a.V;
+  const int g0 = (ch * kPWarps + warp) * (32 * PER);  // this warp's first 16-byte group
+  const int x = a.tokens ? a.tokens[row] : -1;
+  uint4 q[PER];
+  if (g0 * E >= head && (g0 + 32 * PER) * E - head <= V) {
+#pragma unroll
+    for (int u = 0; u < PER; ++u) q[u] = __ldg((const uint4*)(z + ((g0 + u * 32 + lane) * E - head)));
+  } else {
+#pragma unroll
+    for (int u = 0; u < PER; ++u) q[u] = load16<T>(z, (g0 + u * 32 + lane) * E - head, V);
+  }
+  const bool bad = x < -1 || x >= V;
+  const float zx = x >= 0 && !bad ? to_f<T>(z[x]) : INFINITY;
+  const float s2 = a.invT * kPL2e;
+  Part p;
+  p.m = -INFINITY;
+#pragma unroll
+  for (int u = 0; u < PER; ++u) p.m = Lg<T>::max16(p.m, q[u]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) p.m = fmaxf(p.m, __shfl_xor_sync(0xffffffffu, p.m, o));
+  if (TOP && lane == 0) a.ws.seg[(row * a.nchunk + ch) * kPWarps + warp] = p.m;
+  const float mu = p.m == -INFINITY ? 0.f : p.m;
+  const F2 nm = f2(-mu, -mu), ss = f2(s2, s2);
+  F2 S = f2(0.f, 0.f), A = S;
+#pragma unroll
+  for (int u = 0; u < PER; ++u)
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) {
+      float2 y = un2(mul2(add2(Lg<T>::pair(q[u], e), nm), ss));
+      // 2^y is zero from -150 down: -inf becomes a finite factor of a zero.  (A NaN passes through
+      // the exponential, not through this maximum.)
+      const F2 ex = f2(ex2p(y.x), ex2p(y.y));
+      S = add2(S, ex);
+      A = fma2(ex, f2(fmaxf(y.x, -256.f), fmaxf(y.y, -256.f)), A);
+    }
+  const float2 S1 = un2(S), A1 = un2(A);
+  p.S = warp_sum(S1.x + S1.y);
+  p.A = warp_sum(A1.x + A1.y);
+  typename Lg<T>::Cnt cnt = Lg<T>::zero();
+  const typename Lg<T>::Thr thr = Lg<T>::thr(zx);
+#pragma unroll
+  for (int u = 0; u < PER; ++u) Lg<T>::above(cnt, q[u], thr);
+  p.c = __reduce_add_sync(0xffffffffu, Lg<T>::total(cnt));
+  if (lane == 0) red[warp] = p;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    p = red[0];
+#pragma unroll
+    for (int w = 1; w < kPWarps; ++w) part_merge(p, red[w], s2);
+    s_last = 1;
+    if (a.nchunk > 1) {
+      a.ws.part[row * a.nchunk + ch] = p;
+      __threadfence();
+      s_last = atomicAdd(&a.ws.count[row], 1u) == (unsigned)a.nchunk - 1u;
+    } else {
+      red[0] = p;
+    }
+  }
+  __syncthreads();
+  if (!s_last) return;
+  // ---- the row's last block
+  if (warp == 0) {
+    if (a.nchunk > 1) {
+      __threadfence();
+      p = Part{-INFINITY, 0.f, 0.f, 0};
+      for (int c = lane; c < a.nchunk; c += 32) {
+        const float4 v = __ldcg((const float4*)(a.ws.part + row * a.nchunk + c));
+        part_merge(p, Part{v.x, v.y, v.z, __float_as_int(v.w)}, s2);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) part_merge(p, part_shfl(p, o), s2);
+    } else {
+      p = red[0];
+    }
+    if (lane == 0) {
+      const bool none = p.S == 0.f;  // every entry -inf
+      const float ls = none ? 0.f : logf(p.S);
+      if (a.norm) a.norm[row] = make_float2(p.m, ls);
+      if (a.entropy) a.entropy[row] = none ? 0.f : fmaf(-kPLn2, p.A / p.S, ls);
+      if (a.logp)
+        a.logp[row] = x == -1 ? 0.f
+                      : bad || isnan(p.S) ? NAN
+                      : zx == -INFINITY   ? -INFINITY
+                                          : fmaf(zx - p.m, a.invT, -ls);
+      if (a.rank) a.rank[row] = bad ? -1 : x < 0 ? 0 : p.c + 1;
+      if (bad) atomicMax(&a.ws.hdr->status, kErrInvalid);
+      if (a.nchunk > 1) a.ws.count[row] = 0u;
+      fin[0] = p.m;
+      fin[1] = ls;
+    }
+  }
+  if (TOP) {
+    if (a.nchunk > 1) __threadfence();
+    __syncthreads();
+    top_search<T, PER>(*(TopSm*)top_raw, a, z, head, row, fin[0], fin[1]);
+  }
+}
+
+// ------------------------------------------------------------------ gradient
+template <typename T>
+__device__ __forceinline__ uint4 pack16(const float* f);
+template <>
+__device__ __forceinline__ uint4 pack16<float>(const float* f) {
+  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+template <>
+__device__ __forceinline__ uint4 pack16<__nv_bfloat16>(const float* f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    memcpy(&w[i], &b, 4);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 template <typename T>
 __device__ __forceinline__ T from_f(float x);
 template <>
@@ -117,67 +446,161 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
 
+constexpr int kGPer = 4;  // 16-byte groups per thread
+
+// With lp = ln p_v: dz = p (c0 + c1 lp), c0 = -(g + h H) / T, c1 = -h / T, plus g / T at the token.
 template <typename T>
 __global__ void __launch_bounds__(kPThr) logprob_grad_kernel(
-    int V, float invT, const T* __restrict__ logits, long long ld, const int32_t* __restrict__ tokens,
+    int V, int nchunk, float invT, const T* logits, long long ld, const int32_t* __restrict__ tokens,
     const float2* __restrict__ norm, const float* __restrict__ entropy, const float* __restrict__ gl,
     const float* __restrict__ gh, T* grad, long long gld) {
-  const long long row = blockIdx.y;
+  constexpr int E = Lg<T>::E;
+  const long long row = blockIdx.x / (unsigned)nchunk;
+  const int ch = (int)(blockIdx.x % (unsigned)nchunk);
+  const T* z = logits + row * ld;
+  T* o = grad + row * gld;
+  const int head = row_head(z);
+  const int g0 = ch * (kPThr * kGPer) + (int)threadIdx.x;
+  uint4 q[kGPer];
+#pragma unroll
+  for (int u = 0; u < kGPer; ++u) {
+    const int v0 = (g0 + u * kPThr) * E - head;
+    q[u] = v0 >= 0 && v0 + E <= V ? __ldcs((const uint4*)(z + v0)) : load16<T>(z, v0, V);
+  }
   const int x = tokens ? tokens[row] : -1;
   const float2 n = norm[row];
   const float g = gl && x >= 0 ? gl[row] : 0.f;
   const float h = gh ? gh[row] : 0.f, H = gh ? entropy[row] : 0.f;
-  const bool bad = x < -1 || x >= V;
-  const int v = blockIdx.x * kPThr + (int)threadIdx.x;
-  if (v >= V) return;
-  const float f = to_f<T>(logits[row * ld + v]);
-  const float lp = f == -INFINITY ? -INFINITY : (f - n.x) * invT - n.y;
-  const float p = expf(lp);
-  float d = -p * (g + (p == 0.f ? 0.f : h * (lp + H)));
-  if (v == x) d += g;
-  grad[row * gld + v] = from_f<T>(bad ? NAN : d * invT);
+  const bool bad = x < -1 || x >= V || isnan(n.y);  // (a row with NaN or +inf: NaN throughout)
+  const float nm = n.x == -INFINITY ? 0.f : -n.x;  // (then every entry is -inf and every p is zero)
+  const float c1 = bad ? NAN : -h * invT, c0 = bad ? NAN : -(g + h * H) * invT;
+  const bool same = row_head((const T*)o) == head;
+#pragma unroll
+  for (int u = 0; u < kGPer; ++u) {
+    const int v0 = (g0 + u * kPThr) * E - head;
+    if (v0 >= V) break;
+    float f[E];
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) {
+      const float2 zz = un2(Lg<T>::pair(q[u], e));
+      // -inf becomes a finite factor of a p that is zero
+      const float la = fmaxf(fmaf(zz.x + nm, invT, -n.y), -1000.f);
+      const float lb = fmaxf(fmaf(zz.y + nm, invT, -n.y), -1000.f);
+      f[2 * e] = ex2p(la * kPL2e) * fmaf(c1, la, c0);
+      f[2 * e + 1] = ex2p(lb * kPL2e) * fmaf(c1, lb, c0);
+    }
+    if (x >= v0 && x < v0 + E) {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (v0 + e == x) f[e] = fmaf(g, invT, f[e]);
+    }
+    if (same && v0 >= 0 && v0 + E <= V) {
+      __stcs((uint4*)(o + v0), pack16<T>(f));
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (v0 + e >= 0 && v0 + e < V) o[v0 + e] = from_f<T>(f[e]);
+    }
+  }
+}
+
+constexpr size_t lp_align(size_t x) { return (x + 255) / 256 * 256; }
+
+// chunks of a row for 16-byte groups of E entries, PER per thread; one more group when rows may
+// start off a 16-byte boundary
+int lp_chunks(int V, int E, int per, bool aligned_rows) {
+  const int groups = (V + (aligned_rows ? 0 : E - 1) + E - 1) / E;
+  return (groups + kPThr * per - 1) / (kPThr * per);
+}
+
+template <typename T, int PER>
+cudaError_t lp_launch(int N, const T* logits, const LpArgs& a, cudaStream_t stream) {
+  const unsigned grid = (unsigned)N * (unsigned)a.nchunk;
+  if (a.top)
+    logprob_kernel<T, PER, true><<<grid, kPThr, 0, stream>>>(logits, a);
+  else
+    logprob_kernel<T, PER, false><<<grid, kPThr, 0, stream>>>(logits, a);
+  return cudaGetLastError();
+}
+
+// Sixteen-byte loads per thread.  Small problems take short chunks so that every SM has some.
+constexpr int kPerMany = 8, kPerFew = 2;
+constexpr long long kFewBytes = 8ll << 20;
+
+template <typename T>
+cudaError_t lp_run(int N, const T* logits, LpArgs a, cudaStream_t stream) {
+  constexpr int E = Lg<T>::E;
+  const bool al = ((uintptr_t)logits % 16) == 0 && (a.ld * (long long)sizeof(T)) % 16 == 0;
+  if ((long long)N * a.V * (long long)sizeof(T) <= kFewBytes) {
+    a.nchunk = lp_chunks(a.V, E, kPerFew, al);
+    return lp_launch<T, kPerFew>(N, logits, a, stream);
+  }
+  a.nchunk = lp_chunks(a.V, E, kPerMany, al);
+  return lp_launch<T, kPerMany>(N, logits, a, stream);
+}
+
+// Room for the chunks of N rows of at most V entries, whatever their type and alignment.  Short
+// chunks (problems of at most kFewBytes, so 2^22 entries, of 2^11 or more per chunk) are bounded by
+// their total: the room never shrinks as N or V grows, so a workspace serves smaller problems too.
+size_t lp_slots(int N, int V) {
+  const size_t many = (size_t)N * lp_chunks(V, 4, kPerMany, false);
+  const size_t few = (size_t)N * lp_chunks(V, 4, kPerFew, false), cap = 2048 + 2 * (size_t)N;
+  return many > (few < cap ? few : cap) ? many : few < cap ? few : cap;
 }
 
 }  // namespace
 
-size_t logprobs_workspace_bytes(int, int, int) { return sizeof(WsHeader); }
+size_t logprobs_workspace_bytes(int N, int V, int top) {
+  const size_t slots = lp_slots(N, V);
+  size_t o = sizeof(WsHeader) + lp_align((size_t)N * sizeof(unsigned)) + lp_align(slots * sizeof(Part));
+  if (top) o += lp_align(slots * kPWarps * sizeof(float));
+  return o;
+}
 
 cudaError_t launch_logprobs(int N, int V, float T, int bf16, const void* logits, long long ld,
                             const int32_t* tokens, int top, float* logp, float* norm, float* entropy,
                             int32_t* rank, int32_t* top_ids, float* top_logp, void* workspace,
                             cudaStream_t stream) {
-  if (bf16)
-    logprob_kernel<__nv_bfloat16><<<N, kPThr, 0, stream>>>(
-        V, 1.f / T, (const __nv_bfloat16*)logits, ld, tokens, top, logp, (float2*)norm, entropy, rank,
-        top_ids, top_logp, &((WsHeader*)workspace)->status);
-  else
-    logprob_kernel<float><<<N, kPThr, 0, stream>>>(V, 1.f / T, (const float*)logits, ld, tokens, top, logp,
-                                                   (float2*)norm, entropy, rank, top_ids, top_logp,
-                                                   &((WsHeader*)workspace)->status);
-  return cudaGetLastError();
+  LpArgs a;
+  a.V = V;
+  a.top = top;
+  a.invT = 1.f / T;
+  a.ld = ld;
+  a.tokens = tokens;
+  a.logp = logp;
+  a.norm = (float2*)norm;
+  a.entropy = entropy;
+  a.rank = rank;
+  a.top_ids = top_ids;
+  a.top_logp = top_logp;
+  uint8_t* w = (uint8_t*)workspace;
+  a.ws.hdr = (WsHeader*)w;
+  w += sizeof(WsHeader);
+  a.ws.count = (unsigned*)w;
+  w += lp_align((size_t)N * sizeof(unsigned));
+  a.ws.part = (Part*)w;
+  w += lp_align(lp_slots(N, V) * sizeof(Part));
+  a.ws.seg = (float*)w;
+  return bf16 ? lp_run<__nv_bfloat16>(N, (const __nv_bfloat16*)logits, a, stream)
+              : lp_run<float>(N, (const float*)logits, a, stream);
 }
 
 cudaError_t launch_logprobs_grad(int N, int V, float T, int bf16, const void* logits, long long ld,
                                  const int32_t* tokens, const float* norm, const float* entropy,
                                  const float* gl, const float* gh, void* grad, long long gld,
                                  cudaStream_t stream) {
-  for (int r0 = 0; r0 < N; r0 += 65535) {
-    const int n = N - r0 < 65535 ? N - r0 : 65535;
-    const dim3 grid((V + kPThr - 1) / kPThr, n);
-    const int32_t* tk = tokens ? tokens + r0 : nullptr;
-    const float2* nm = (const float2*)norm + r0;
-    const float *en = entropy ? entropy + r0 : nullptr, *a = gl ? gl + r0 : nullptr, *b = gh ? gh + r0 : nullptr;
-    if (bf16)
-      logprob_grad_kernel<__nv_bfloat16><<<grid, kPThr, 0, stream>>>(
-          V, 1.f / T, (const __nv_bfloat16*)logits + r0 * ld, ld, tk, nm, en, a, b,
-          (__nv_bfloat16*)grad + r0 * gld, gld);
-    else
-      logprob_grad_kernel<float><<<grid, kPThr, 0, stream>>>(V, 1.f / T, (const float*)logits + r0 * ld, ld,
-                                                             tk, nm, en, a, b, (float*)grad + r0 * gld, gld);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  const bool al = ((uintptr_t)logits % 16) == 0 && (ld * (bf16 ? 2 : 4)) % 16 == 0;
+  const int nchunk = lp_chunks(V, bf16 ? 8 : 4, kGPer, al);
+  const unsigned grid = (unsigned)N * (unsigned)nchunk;
+  if (bf16)
+    logprob_grad_kernel<__nv_bfloat16><<<grid, kPThr, 0, stream>>>(
+        V, nchunk, 1.f / T, (const __nv_bfloat16*)logits, ld, tokens, (const float2*)norm, entropy, gl, gh,
+        (__nv_bfloat16*)grad, gld);
+  else
+    logprob_grad_kernel<float><<<grid, kPThr, 0, stream>>>(V, nchunk, 1.f / T, (const float*)logits, ld, tokens,
+                                                           (const float2*)norm, entropy, gl, gh, (float*)grad,
+                                                           gld);
+  return cudaGetLastError();
 }
 
 }  // namespace dspark
