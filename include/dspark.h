@@ -354,7 +354,8 @@ dspark_status dspark_token_logprobs_grad(int N, int V, float T, dspark_dtype zdt
  *   out[i] = scale * W[tokens[i]],  zero for tokens[i] = -1 (padding), NaN for another token outside
  *   [0, V) (no status word; no workspace needed).
  * W [V][D] of type wdt, tokens [N] int32, out [N][D] of type odt (rounded once).  Any D >= 1; arrays
- * aligned to their type (16-byte aligned rows move fastest).  N = 0 does nothing.  One launch.
+ * aligned to their type (16-byte aligned rows move fastest).  Limits: 0 <= N <= 2^24 (N = 0 does
+ * nothing), 1 <= V <= 2^24, 1 <= D <= 2^20.  One launch.
  */
 dspark_status dspark_embedding(int N, int V, int D, float scale, dspark_dtype wdt, const void* W,
                                const int32_t* tokens, dspark_dtype odt, void* out, void* stream);
@@ -367,7 +368,9 @@ dspark_status dspark_embedding(int N, int V, int D, float scale, dspark_dtype wd
  * once).  accumulate = 0 writes every row (zero for tokens that do not occur); otherwise the sums are
  * added to grad_W and other rows are neither read nor written.  tokens[i] = -1 adds nothing; another
  * token outside [0, V) adds nothing and sets DSPARK_ERR_INVALID in the workspace status.
- * workspace: dspark_embedding_grad_workspace_bytes(N, V, D) bytes, 256-byte aligned, zeroed once.
+ * workspace: dspark_embedding_grad_workspace_bytes(N, V, D) bytes, 256-byte aligned, zeroed once; it
+ * serves any V and fewer tokens and columns too.  Limits as above.  Three launches up to 4096 tokens
+ * (two up to 32), else two and one per 9 bits of V.
  */
 size_t dspark_embedding_grad_workspace_bytes(int N, int V, int D);
 dspark_status dspark_embedding_grad(int N, int V, int D, float scale, dspark_dtype gdt, const void* grad,

@@ -566,7 +566,7 @@ dspark_status dspark_token_logprobs_grad(int N, int V, float T, dspark_dtype zdt
 dspark_status dspark_embedding(int N, int V, int D, float scale, dspark_dtype wdt, const void* W,
                                const int32_t* tokens, dspark_dtype odt, void* out, void* stream) {
   g_err.clear();
-  if (N < 0 || V < 1 || V > (1 << 24) || D < 1 || D > (1 << 20))
+  if (N < 0 || N > (1 << 24) || V < 1 || V > (1 << 24) || D < 1 || D > (1 << 20))
     return fail(DSPARK_ERR_INVALID, "bad shape N=%d V=%d D=%d", N, V, D);
   if (!std::isfinite(scale)) return fail(DSPARK_ERR_INVALID, "scale must be finite");
   if ((wdt != DSPARK_F32 && wdt != DSPARK_BF16) || (odt != DSPARK_F32 && odt != DSPARK_BF16))

@@ -1,7 +1,16 @@
 // embedding.cu -- rows of a table for given tokens, scaled, and the table's gradient.
 //
 //   out[i] = scale W[t_i]  (zero for t_i = -1: padding);
-//   grad_W[v] = scale sum_{i : t_i = v} grad[i], the sum in the order of i.
+//   grad_W[v] = scale sum_{i : t_i = v} grad[i].
+//
+// The gradient sums every token's rows in an order that the tokens alone decide.  The positions are
+// sorted by token first (stable), so that a token's rows are a run of consecutive positions:
+//   - up to 4096 tokens, one launch counts for every position how many precede it (all pairs);
+//   - more, a stable radix sort with digits of at most 9 bits: two or three scatter launches.
+// Then one launch sums slices of the sorted positions (a warp per slice and 512 bytes of columns,
+// eight rows in flight) and, in other blocks, zeroes the rows of tokens that do not occur, which a
+// bitmap names.  A run inside one slice is written at once; a longer one leaves one fp32 partial
+// sum per slice, and a last launch adds those up in their order.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -9,90 +18,575 @@ namespace dspark {
 namespace {
 
 constexpr int kEThr = 256;
+using bf16 = __nv_bfloat16;
 
-__device__ __forceinline__ void put(float* p, float x) { *p = x; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+// E consecutive elements as floats, from a 16-byte (or, for E = 1, a single-element) load
+template <typename T, int E>
+struct Row;
+template <>
+struct Row<float, 4> {
+  uint4 q;
+  __device__ __forceinline__ void load(const float* p) { q = __ldg((const uint4*)p); }
+  __device__ __forceinline__ void get(float* f) const { Vec<float>::unpack(q, f); }
+};
+template <>
+struct Row<bf16, 8> {
+  uint4 q;
+  __device__ __forceinline__ void load(const bf16* p) { q = __ldg((const uint4*)p); }
+  __device__ __forceinline__ void get(float* f) const { Vec<bf16>::unpack(q, f); }
+};
+template <typename T>
+struct Row<T, 1> {
+  T x;
+  __device__ __forceinline__ void load(const T* p) { x = *p; }
+  __device__ __forceinline__ void get(float* f) const { f[0] = to_f<T>(x); }
+};
 
-template <typename TW, typename TO>
-__global__ void __launch_bounds__(kEThr) embed_kernel(int V, int D, float scale, const TW* __restrict__ W,
+// E floats to consecutive elements (aligned to E elements for E > 1), rounded once
+template <int E>
+__device__ __forceinline__ void store(float* p, const float* f) {
+  if (E == 1) {
+    *p = f[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; i += 4) __stcs((float4*)(p + i), make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]));
+  }
+}
+template <int E>
+__device__ __forceinline__ void store(bf16* p, const float* f) {
+  if (E == 1) {
+    *p = __float2bfloat16_rn(f[0]);
+  } else {
+    uint32_t w[E / 2 > 0 ? E / 2 : 1];
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      memcpy(&w[i], &b, 4);
+    }
+    if (E == 4) __stcs((uint2*)p, make_uint2(w[0], w[1]));
+    if (E == 8) __stcs((uint4*)p, make_uint4(w[0], w[1], w[2 % (E / 2 > 0 ? E / 2 : 1)], w[3 % (E / 2 > 0 ? E / 2 : 1)]));
+  }
+}
+template <int E>
+__device__ __forceinline__ void load_out(const float* p, float* f) {
+#pragma unroll
+  for (int i = 0; i < E; ++i) f[i] = p[i];
+}
+template <int E>
+__device__ __forceinline__ void load_out(const bf16* p, float* f) {
+#pragma unroll
+  for (int i = 0; i < E; ++i) f[i] = __bfloat162float(p[i]);
+}
+
+// ------------------------------------------------------------------ lookup
+constexpr int kLook = 4;  // pieces of E elements per thread
+
+template <typename TW, typename TO, int E>
+__global__ void __launch_bounds__(kEThr) embed_kernel(int N, int V, int D, float scale,
+                                                      const TW* __restrict__ W,
                                                       const int32_t* __restrict__ tokens,
                                                       TO* __restrict__ out) {
-  const long long i = blockIdx.x;
-  const int t = tokens[i];
-  for (int j = threadIdx.x; j < D; j += kEThr) {
-    float x = 0.f;
-    if (t < -1 || t >= V)
-      x = NAN;
-    else if (t >= 0)
-      x = scale * to_f<TW>(W[(long long)t * D + j]);
-    put(out + i * D + j, x);
+  const unsigned per = (unsigned)D / E;  // pieces of a row
+  const unsigned long long first = (unsigned long long)blockIdx.x * (kEThr * kLook);
+  const unsigned long long row0 = first / per;
+  const unsigned off = (unsigned)(first - row0 * per) + threadIdx.x;
+  int t[kLook];
+  unsigned c[kLook];
+  long long row[kLook];
+#pragma unroll
+  for (int u = 0; u < kLook; ++u) {
+    const unsigned p = off + u * kEThr;
+    row[u] = (long long)row0 + p / per;
+    c[u] = (p % per) * E;
+    t[u] = row[u] < N ? tokens[row[u]] : -1;
+  }
+  Row<TW, E> r[kLook];
+#pragma unroll
+  for (int u = 0; u < kLook; ++u)
+    if (t[u] >= 0 && t[u] < V) r[u].load(W + (long long)t[u] * D + c[u]);
+#pragma unroll
+  for (int u = 0; u < kLook; ++u) {
+    if (row[u] >= N) break;
+    float f[E];
+    if (t[u] >= 0 && t[u] < V) {
+      r[u].get(f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] *= scale;
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] = t[u] == -1 ? 0.f : NAN;
+    }
+    store<E>(out + row[u] * D + c[u], f);
   }
 }
 
-// One block per table row: it looks through all tokens for its own.
-template <typename TG, typename TO>
-__global__ void __launch_bounds__(kEThr) embed_grad_kernel(int N, int D, float scale,
-                                                           const TG* __restrict__ grad,
-                                                           const int32_t* __restrict__ tokens,
-                                                           TO* __restrict__ gW, int accumulate) {
-  const int v = blockIdx.x;
-  for (int j0 = 0; j0 < D; j0 += kEThr) {
-    const int j = j0 + (int)threadIdx.x;
-    float s = 0.f;
-    bool any = false;
-    for (int i = 0; i < N; ++i)
-      if (tokens[i] == v) {
-        any = true;
-        if (j < D) s += to_f<TG>(grad[(long long)i * D + j]);
+template <typename TW, typename TO>
+cudaError_t embed_run(int N, int V, int D, float scale, const TW* W, const int32_t* tokens, TO* out,
+                      cudaStream_t stream) {
+  constexpr int E = 16 / (int)sizeof(TW);
+  const bool vec = D % E == 0 && ((uintptr_t)W % 16) == 0 && ((uintptr_t)out % (E * sizeof(TO) < 16 ? 8 : 16)) == 0;
+  const long long pieces = (long long)N * (vec ? D / E : D);
+  const unsigned grid = (unsigned)((pieces + kEThr * kLook - 1) / (kEThr * kLook));
+  if (vec)
+    embed_kernel<TW, TO, E><<<grid, kEThr, 0, stream>>>(N, V, D, scale, W, tokens, out);
+  else
+    embed_kernel<TW, TO, 1><<<grid, kEThr, 0, stream>>>(N, V, D, scale, W, tokens, out);
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ gradient: workspace
+constexpr int kPairs = 4096;      // most tokens that are sorted by counting all pairs
+constexpr int kBinBits = 9, kBins = 1 << kBinBits;
+constexpr int kSortThr = 512, kSortWarps = kSortThr / 32;
+constexpr int kTile = 2048;       // keys per tile of a sort block
+constexpr int kSortBlocks = 64;   // most blocks of a sort launch
+constexpr int kMaxSlices = 2048;
+constexpr size_t kMapBytes = (1u << 24) / 8;
+
+struct EgWs {
+  WsHeader* hdr;
+  unsigned* nrun;      // [1] runs that cross slices
+  unsigned* run;       // [slices] the slices in which they begin
+  uint32_t* map;       // bit v: token v occurs; zero between calls
+  uint32_t* key[2];    // [N] sorted tokens
+  uint32_t* pos[2];    // [N] their positions
+  unsigned* hist[2];   // [kSortBlocks][kBins]
+  float* part;         // [slices][2][D]
+};
+
+constexpr size_t eg_align(size_t x) { return (x + 255) / 256 * 256; }
+
+// positions per slice: 32, more once there would be over kMaxSlices of them
+int slice_len(int N) { return 32 * ((N + 32 * kMaxSlices - 1) / (32 * kMaxSlices)); }
+size_t slice_room(int N) {
+  const size_t s = ((size_t)N + 31) / 32;
+  return s < (size_t)kMaxSlices ? s : (size_t)kMaxSlices;
+}
+
+size_t eg_layout(int N, int D, uint8_t* base, EgWs* ws) {
+  size_t o = sizeof(WsHeader);
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += eg_align(bytes);
+    return base + at;
+  };
+  EgWs w;
+  w.hdr = (WsHeader*)base;
+  w.map = (uint32_t*)take(kMapBytes);  // (one size and place for every V: it stays clear)
+  w.nrun = (unsigned*)take(4);
+  w.run = (unsigned*)take(slice_room(N) * 4);
+  for (int i = 0; i < 2; ++i) {
+    w.key[i] = (uint32_t*)take((size_t)N * 4);
+    w.pos[i] = (uint32_t*)take((size_t)N * 4);
+    w.hist[i] = (unsigned*)take((size_t)kSortBlocks * kBins * 4);
+  }
+  w.part = (float*)take(slice_room(N) * 2 * (size_t)D * 4);
+  if (ws) *ws = w;
+  return o;
+}
+
+// the sort key of a position: its token, or V (after every token) for padding and invalid tokens
+__device__ __forceinline__ uint32_t key_of(int t, int V, unsigned* status) {
+  if (t >= 0 && t < V) return (uint32_t)t;
+  if (t != -1) atomicMax(status, kErrInvalid);
+  return (uint32_t)V;
+}
+
+// ------------------------------------------------------------------ sort, few tokens
+// A block ranks 32 positions, one per lane; its warps share out the positions compared with.
+__global__ void __launch_bounds__(kEThr) pairs_kernel(int N, int V, const int32_t* __restrict__ tokens,
+                                                      int mark, EgWs ws) {
+  __shared__ __align__(16) uint32_t key[kPairs];
+  __shared__ int cnt[kEThr / 32][32];
+  const int lane = (int)(threadIdx.x & 31), warp = (int)(threadIdx.x >> 5);
+  const int n4 = (N + 3) & ~3;
+  for (int i = threadIdx.x; i < n4; i += kEThr)
+    key[i] = i < N ? key_of(tokens[i], V, &ws.hdr->status) : 0xFFFFFFFFu;  // (larger than any)
+  if (blockIdx.x == 0 && threadIdx.x == 0) *ws.nrun = 0u;
+  __syncthreads();
+  const int i0 = (int)blockIdx.x * 32, i = i0 + lane;
+  const uint32_t k = i < N ? key[i] : 0u;
+  const int per = ((n4 / 4 + kEThr / 32 - 1) / (kEThr / 32)) * 4;
+  const int ja = min(n4, warp * per), jb = min(n4, ja + per);
+  int c = 0;
+  // before the block's own positions an equal token precedes, after them it does not
+  const int je = min(jb, max(ja, i0)), jl = min(jb, max(ja, i0 + 32));
+  for (int j = ja; j < je; j += 4) {
+    const uint4 q = *(const uint4*)(key + j);
+    c += (q.x <= k) + (q.y <= k) + (q.z <= k) + (q.w <= k);
+  }
+  for (int j = je; j < jl; ++j) c += key[j] < k || (key[j] == k && j < i);
+  for (int j = jl; j < jb; j += 4) {
+    const uint4 q = *(const uint4*)(key + j);
+    c += (q.x < k) + (q.y < k) + (q.z < k) + (q.w < k);
+  }
+  cnt[warp][lane] = c;
+  __syncthreads();
+  if (warp == 0 && i < N) {
+    for (int w = 1; w < kEThr / 32; ++w) c += cnt[w][lane];
+    ws.key[0][c] = k;
+    ws.pos[0][c] = (uint32_t)i;
+    if (mark && k < (uint32_t)V) atomicOr(&ws.map[k >> 5], 1u << (k & 31));
+  }
+}
+
+// ------------------------------------------------------------------ sort, many tokens
+// Digit counts of every block's share of the tokens (the first pass; later passes' counts are made
+// by the scatter before them).
+__global__ void __launch_bounds__(kSortThr) count_kernel(int N, int V, int per_block, int bits,
+                                                         const int32_t* __restrict__ tokens, int mark,
+                                                         EgWs ws) {
+  __shared__ unsigned h[kBins];
+  for (int b = threadIdx.x; b < kBins; b += kSortThr) {
+    h[b] = 0u;
+    ws.hist[1][blockIdx.x * kBins + b] = 0u;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *ws.nrun = 0u;
+  __syncthreads();
+  const int i1 = min((long long)N, (long long)(blockIdx.x + 1) * per_block);
+  for (int i = (int)blockIdx.x * per_block + (int)threadIdx.x; i < i1; i += kSortThr) {
+    const uint32_t k = key_of(tokens[i], V, &ws.hdr->status);
+    atomicAdd(&h[k & ((1u << bits) - 1u)], 1u);
+    if (mark && k < (uint32_t)V) atomicOr(&ws.map[k >> 5], 1u << (k & 31));
+  }
+  __syncthreads();
+  for (int b = threadIdx.x; b < kBins; b += kSortThr) ws.hist[0][blockIdx.x * kBins + b] = h[b];
+}
+
+// One stable pass: block b moves its share of the keys to where their digit's keys go, after those
+// of the blocks before it.  The first pass reads the tokens (key_in null); every pass but the last
+// counts the next digit of the keys at their new places.
+__global__ void __launch_bounds__(kSortThr) scatter_kernel(int N, int V, int per_block, int shift, int bits,
+                                                           int last, const int32_t* __restrict__ tokens,
+                                                           const uint32_t* __restrict__ key_in,
+                                                           const uint32_t* __restrict__ pos_in,
+                                                           const unsigned* __restrict__ hist,
+                                                           unsigned* __restrict__ next,
+                                                           uint32_t* __restrict__ key_out,
+                                                           uint32_t* __restrict__ pos_out) {
+  __shared__ unsigned cnt[kSortWarps][kBins];
+  __shared__ unsigned base[kBins];
+  __shared__ unsigned wsum[kSortWarps];
+  const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nb = (int)gridDim.x;
+  {  // base[d]: keys of lower digits, and of this digit in the blocks before
+    unsigned below = 0u, all = 0u;
+    for (int b = 0; b < nb; ++b) {
+      const unsigned h = hist[b * kBins + tid];
+      all += h;
+      below += b < (int)blockIdx.x ? h : 0u;
+    }
+    unsigned inc = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    unsigned w0 = 0u;
+    for (int w = 0; w < warp; ++w) w0 += wsum[w];
+    base[tid] = w0 + inc - all + below;
+  }
+  const uint32_t mask = (1u << bits) - 1u;
+  const long long i1 = min((long long)N, (long long)(blockIdx.x + 1) * per_block);
+  for (long long t0 = (long long)blockIdx.x * per_block; t0 < i1; t0 += kTile) {
+    for (int j = tid; j < kSortWarps * kBins; j += kSortThr) (&cnt[0][0])[j] = 0u;
+    __syncthreads();
+    uint32_t k[kTile / kSortThr], r[kTile / kSortThr];
+#pragma unroll
+    for (int u = 0; u < kTile / kSortThr; ++u) {  // the warp's 128 keys, 32 consecutive ones at a time
+      const long long i = t0 + warp * (kTile / kSortWarps) + u * 32 + lane;
+      const bool in = i < i1;
+      k[u] = !in ? 0xFFFFFFFFu : tokens ? (tokens[i] >= 0 && tokens[i] < V ? (uint32_t)tokens[i] : (uint32_t)V) : key_in[i];
+      const uint32_t d = in ? (k[u] >> shift) & mask : kBins;
+      const unsigned same = __match_any_sync(0xffffffffu, d);
+      const unsigned before = __popc(same & ((1u << lane) - 1u));
+      r[u] = in ? cnt[warp][d] + before : 0u;
+      __syncwarp();
+      if (in && before == 0u) cnt[warp][d] += (unsigned)__popc(same);
+      __syncwarp();
+    }
+    __syncthreads();
+    {
+      unsigned b = base[tid];
+      for (int w = 0; w < kSortWarps; ++w) {
+        const unsigned c = cnt[w][tid];
+        cnt[w][tid] = b;
+        b += c;
       }
-    if (j < D && (any || !accumulate)) {
-      TO* o = gW + (long long)v * D + j;
-      put(o, accumulate ? to_f<TO>(*o) + scale * s : scale * s);
+      base[tid] = b;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kTile / kSortThr; ++u) {
+      const long long i = t0 + warp * (kTile / kSortWarps) + u * 32 + lane;
+      if (i < i1) {
+        const unsigned p = cnt[warp][(k[u] >> shift) & mask] + r[u];
+        key_out[p] = k[u];
+        pos_out[p] = pos_in ? pos_in[i] : (uint32_t)i;
+        if (!last) atomicAdd(&next[(p / (unsigned)per_block) * kBins + ((k[u] >> (shift + bits)) & mask)], 1u);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+__global__ void __launch_bounds__(kSortThr) clear_kernel(unsigned* __restrict__ h) {
+  h[blockIdx.x * kBins + threadIdx.x] = 0u;
+}
+
+// ------------------------------------------------------------------ sums
+constexpr int kAhead = 8;  // rows in flight per warp
+
+struct SumArgs {
+  int N, V, D, plen, nslice, ntile;  // positions per slice, slices, column tiles of 32 E
+  float scale;
+  int accumulate;
+  int fill_blocks;                   // blocks that zero absent rows (they come after the others)
+  const uint32_t *key, *pos;
+  EgWs ws;
+};
+
+template <typename TO, int E>
+__device__ __forceinline__ void put_row(TO* o, const float* s, float scale, int accumulate) {
+  float f[E];
+  if (accumulate) {
+    load_out<E>(o, f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = fmaf(scale, s[e], f[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = scale * s[e];
+  }
+  store<E>(o, f);
+}
+
+template <typename TG, typename TO, int E>
+__global__ void __launch_bounds__(kEThr) sum_kernel(const SumArgs a, const TG* __restrict__ grad,
+                                                    TO* __restrict__ gW) {
+  const int lane = (int)(threadIdx.x & 31);
+  const int sum_blocks = (int)gridDim.x - a.fill_blocks;
+  if ((int)blockIdx.x >= sum_blocks) {  // zero the rows of absent tokens, 32 rows at a time
+    const int words = (a.V + 31) / 32;
+    const unsigned per = (unsigned)a.D / E;
+    for (int w = (int)blockIdx.x - sum_blocks; w < words; w += a.fill_blocks) {
+      const uint32_t m = a.ws.map[w];
+      const unsigned rows = (unsigned)min(32, a.V - 32 * w);
+      TO* o = gW + (long long)w * 32 * a.D;
+      const float zero[E] = {};
+      unsigned r = threadIdx.x / per, c = threadIdx.x % per;
+      const unsigned dr = kEThr / per, dc = kEThr % per;
+      while (r < rows) {
+        if (!((m >> r) & 1u)) store<E>(o + (long long)r * a.D + (long long)c * E, zero);
+        r += dr;
+        c += dc;
+        if (c >= per) {
+          c -= per;
+          ++r;
+        }
+      }
+      __syncthreads();
+      if (threadIdx.x == 0 && m) a.ws.map[w] = 0u;
+    }
+    return;
+  }
+  const long long unit = (long long)blockIdx.x * (kEThr / 32) + (threadIdx.x >> 5);
+  const int slice = (int)(unit / a.ntile), tile = (int)(unit % a.ntile);
+  if (slice >= a.nslice) return;
+  const long long p0 = (long long)slice * a.plen, p1 = min((long long)a.N, p0 + a.plen);
+  const int col = (tile * 32 + lane) * E;
+  const bool live = col < a.D;
+  const uint32_t none = (uint32_t)a.V;
+  const uint32_t before = p0 > 0 ? a.key[p0 - 1] : 0xFFFFFFFFu;
+  const uint32_t after = p1 < a.N ? a.key[p1] : 0xFFFFFFFFu;
+  uint32_t cur = a.key[p0];
+  bool begun = cur != before;  // the current run begins in this slice
+  float s[E] = {};
+  for (long long b = p0; b < p1; b += 32) {
+    const int n = (int)min(32ll, p1 - b);
+    const uint32_t kl = lane < n ? a.key[b + lane] : none, pl = lane < n ? a.pos[b + lane] : 0u;
+    for (int i0 = 0; i0 < n; i0 += kAhead) {
+      Row<TG, E> r[kAhead];
+      uint32_t k[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        k[j] = __shfl_sync(0xffffffffu, kl, (i0 + j) & 31);
+        const uint32_t p = __shfl_sync(0xffffffffu, pl, (i0 + j) & 31);
+        if (i0 + j >= n) k[j] = none;
+        if (k[j] != none && live) r[j].load(grad + (long long)p * a.D + col);
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (k[j] == none) continue;  // padding sorts last
+        if (k[j] != cur) {
+          if (live) {
+            if (begun)
+              put_row<TO, E>(gW + (long long)cur * a.D + col, s, a.scale, a.accumulate);
+            else
+              store<E>(a.ws.part + (long long)slice * 2 * a.D + col, s);
+          }
+          cur = k[j];
+          begun = true;
+#pragma unroll
+          for (int e = 0; e < E; ++e) s[e] = 0.f;
+        }
+        if (live) {
+          float f[E];
+          r[j].get(f);
+#pragma unroll
+          for (int e = 0; e < E; ++e) s[e] += f[e];
+        }
+      }
     }
   }
+  if (cur == none) return;
+  if (!begun) {
+    if (live) store<E>(a.ws.part + (long long)slice * 2 * a.D + col, s);
+  } else if (cur == after) {
+    if (live) store<E>(a.ws.part + ((long long)slice * 2 + 1) * a.D + col, s);
+    if (tile == 0 && lane == 0) a.ws.run[atomicAdd(a.ws.nrun, 1u)] = (unsigned)slice;
+  } else if (live) {
+    put_row<TO, E>(gW + (long long)cur * a.D + col, s, a.scale, a.accumulate);
+  }
 }
 
-__global__ void embed_check_kernel(int N, int V, const int32_t* __restrict__ tokens, unsigned* status) {
-  const int i = blockIdx.x * blockDim.x + threadIdx.x;
-  if (i < N && (tokens[i] < -1 || tokens[i] >= V)) atomicMax(status, kErrInvalid);
+// Runs that cross slices: the begun part, then the part of every slice that the run goes on in.
+// A block takes one run and column tile; its warps add contiguous shares of the parts, joined in order.
+template <typename TO, int E>
+__global__ void __launch_bounds__(kEThr) join_kernel(const SumArgs a, TO* __restrict__ gW) {
+  __shared__ float sh[kEThr / 32][32 * E];
+  const int lane = (int)(threadIdx.x & 31), warp = (int)(threadIdx.x >> 5);
+  const long long items = (long long)*a.ws.nrun * a.ntile;
+  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+    const int s0 = (int)a.ws.run[it / a.ntile], tile = (int)(it % a.ntile);
+    const uint32_t k = a.key[(long long)s0 * a.plen + a.plen - 1];
+    int m = 0;  // slices after s0 whose first key is still k
+    for (;;) {
+      const int s = s0 + 1 + m + lane;
+      const unsigned go = __ballot_sync(0xffffffffu, s < a.nslice && a.key[(long long)s * a.plen] == k);
+      if (go == 0xffffffffu) {
+        m += 32;
+        continue;
+      }
+      m += __ffs(~go) - 1;
+      break;
+    }
+    const int per = (m + 1 + kEThr / 32 - 1) / (kEThr / 32);
+    const int c0 = warp * per, c1 = min(m + 1, c0 + per);  // part 0 is s0's second, part i s0 + i's first
+    const int col = (tile * 32 + lane) * E;
+    float s[E] = {};
+    if (col < a.D) {
+      for (int c = c0; c < c1; c += kAhead) {
+        float f[kAhead][E];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+          if (c + j < c1) load_out<E>(a.ws.part + ((long long)(s0 + c + j) * 2 + (c + j == 0 ? 1 : 0)) * a.D + col, f[j]);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+          if (c + j < c1) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) s[e] += f[j][e];
+          }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) sh[warp][lane * E + e] = s[e];
+    __syncthreads();
+    if (warp == 0 && col < a.D) {
+      for (int w = 1; w < kEThr / 32; ++w)
+#pragma unroll
+        for (int e = 0; e < E; ++e) s[e] += sh[w][lane * E + e];
+      put_row<TO, E>(gW + (long long)k * a.D + col, s, a.scale, a.accumulate);
+    }
+    __syncthreads();
+  }
+}
+
+template <typename TG, typename TO, int E>
+cudaError_t sums(SumArgs a, const TG* grad, TO* gW, cudaStream_t stream) {
+  a.ntile = (a.D + 32 * E - 1) / (32 * E);
+  const int words = (a.V + 31) / 32;
+  a.fill_blocks = a.accumulate ? 0 : words < 16384 ? words : 16384;
+  const long long warps = (long long)a.nslice * a.ntile;
+  const unsigned grid = (unsigned)((warps + kEThr / 32 - 1) / (kEThr / 32)) + (unsigned)a.fill_blocks;
+  if (grid == 0) return cudaSuccess;
+  sum_kernel<TG, TO, E><<<grid, kEThr, 0, stream>>>(a, grad, gW);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || a.nslice < 2) return e;
+  join_kernel<TO, E><<<304, kEThr, 0, stream>>>(a, gW);
+  return cudaGetLastError();
+}
+
+template <typename TG, typename TO>
+cudaError_t sums_by_shape(const SumArgs& a, const TG* grad, TO* gW, cudaStream_t stream) {
+  constexpr int E = 16 / (int)sizeof(TG);
+  if (a.D % E == 0 && ((uintptr_t)grad % 16) == 0 && ((uintptr_t)gW % 16) == 0)
+    return sums<TG, TO, E>(a, grad, gW, stream);
+  return sums<TG, TO, 1>(a, grad, gW, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_embedding(int N, int V, int D, float scale, int w_bf16, const void* W,
                              const int32_t* tokens, int o_bf16, void* out, cudaStream_t stream) {
-  using bf = __nv_bfloat16;
-  if (w_bf16 && o_bf16)
-    embed_kernel<bf, bf><<<N, kEThr, 0, stream>>>(V, D, scale, (const bf*)W, tokens, (bf*)out);
-  else if (w_bf16)
-    embed_kernel<bf, float><<<N, kEThr, 0, stream>>>(V, D, scale, (const bf*)W, tokens, (float*)out);
-  else if (o_bf16)
-    embed_kernel<float, bf><<<N, kEThr, 0, stream>>>(V, D, scale, (const float*)W, tokens, (bf*)out);
-  else
-    embed_kernel<float, float><<<N, kEThr, 0, stream>>>(V, D, scale, (const float*)W, tokens, (float*)out);
-  return cudaGetLastError();
+  if (w_bf16 && o_bf16) return embed_run(N, V, D, scale, (const bf16*)W, tokens, (bf16*)out, stream);
+  if (w_bf16) return embed_run(N, V, D, scale, (const bf16*)W, tokens, (float*)out, stream);
+  if (o_bf16) return embed_run(N, V, D, scale, (const float*)W, tokens, (bf16*)out, stream);
+  return embed_run(N, V, D, scale, (const float*)W, tokens, (float*)out, stream);
 }
 
-size_t embedding_grad_workspace_bytes(int, int, int) { return sizeof(WsHeader); }
+size_t embedding_grad_workspace_bytes(int N, int, int D) { return eg_layout(N, D, nullptr, nullptr); }
 
 cudaError_t launch_embedding_grad(int N, int V, int D, float scale, int g_bf16, const void* grad,
                                   const int32_t* tokens, int o_bf16, void* gW, int accumulate,
                                   void* workspace, cudaStream_t stream) {
-  using bf = __nv_bfloat16;
-  if (N > 0) {
-    embed_check_kernel<<<(N + 255) / 256, 256, 0, stream>>>(N, V, tokens, &((WsHeader*)workspace)->status);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+  SumArgs a;
+  eg_layout(N, D, (uint8_t*)workspace, &a.ws);
+  a.N = N;
+  a.V = V;
+  a.D = D;
+  a.scale = scale;
+  a.accumulate = accumulate;
+  a.plen = N > 0 ? slice_len(N) : 32;
+  a.nslice = (int)(((long long)N + a.plen - 1) / a.plen);
+  const int mark = !accumulate;
+  cudaError_t e = cudaSuccess;
+  int at = 0;
+  if (N > 0 && N <= kPairs) {
+    pairs_kernel<<<(N + 31) / 32, kEThr, 0, stream>>>(N, V, tokens, mark, a.ws);
+    e = cudaGetLastError();
+  } else if (N > 0) {
+    int bits = 1;  // keys are 0 .. V
+    while ((1 << bits) <= V) ++bits;
+    const int passes = (bits + kBinBits - 1) / kBinBits, digit = (bits + passes - 1) / passes;
+    const int tiles = (N + kTile - 1) / kTile;
+    const int nb0 = tiles < kSortBlocks ? tiles : kSortBlocks;
+    const int per_block = (tiles + nb0 - 1) / nb0 * kTile;
+    const int nb = (N + per_block - 1) / per_block;
+    count_kernel<<<nb, kSortThr, 0, stream>>>(N, V, per_block, digit, tokens, mark, a.ws);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    for (int p = 0; p < passes; ++p) {
+      const int last = p == passes - 1;
+      if (p >= 1 && !last) {  // (three passes: the counts of the first digit make room for the third's)
+        clear_kernel<<<nb, kSortThr, 0, stream>>>(a.ws.hist[(p + 1) & 1]);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      }
+      scatter_kernel<<<nb, kSortThr, 0, stream>>>(N, V, per_block, p * digit, digit, last,
+                                                  p == 0 ? tokens : nullptr, p ? a.ws.key[(p + 1) & 1] : nullptr,
+                                                  p ? a.ws.pos[(p + 1) & 1] : nullptr, a.ws.hist[p & 1],
+                                                  a.ws.hist[(p + 1) & 1], a.ws.key[p & 1], a.ws.pos[p & 1]);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      at = p & 1;
+    }
   }
-  if (g_bf16 && o_bf16)
-    embed_grad_kernel<bf, bf><<<V, kEThr, 0, stream>>>(N, D, scale, (const bf*)grad, tokens, (bf*)gW, accumulate);
-  else if (g_bf16)
-    embed_grad_kernel<bf, float><<<V, kEThr, 0, stream>>>(N, D, scale, (const bf*)grad, tokens, (float*)gW, accumulate);
-  else if (o_bf16)
-    embed_grad_kernel<float, bf><<<V, kEThr, 0, stream>>>(N, D, scale, (const float*)grad, tokens, (bf*)gW, accumulate);
-  else
-    embed_grad_kernel<float, float><<<V, kEThr, 0, stream>>>(N, D, scale, (const float*)grad, tokens, (float*)gW, accumulate);
-  return cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  a.key = a.ws.key[at];
+  a.pos = a.ws.pos[at];
+  if (g_bf16 && o_bf16) return sums_by_shape(a, (const bf16*)grad, (bf16*)gW, stream);
+  if (g_bf16) return sums_by_shape(a, (const bf16*)grad, (float*)gW, stream);
+  if (o_bf16) return sums_by_shape(a, (const float*)grad, (bf16*)gW, stream);
+  return sums_by_shape(a, (const float*)grad, (float*)gW, stream);
 }
 
 }  // namespace dspark
