@@ -369,8 +369,8 @@ dspark_status dspark_embedding(int N, int V, int D, float scale, dspark_dtype wd
  * added to grad_W and other rows are neither read nor written.  tokens[i] = -1 adds nothing; another
  * token outside [0, V) adds nothing and sets DSPARK_ERR_INVALID in the workspace status.
  * workspace: dspark_embedding_grad_workspace_bytes(N, V, D) bytes, 256-byte aligned, zeroed once; it
- * serves any V and fewer tokens and columns too.  Limits as above.  Three launches up to 4096 tokens
- * (two up to 32), else two and one per 9 bits of V.
+ * serves any V and fewer tokens and columns too.  Limits as above.  Two launches up to 4096 tokens, one
+ * with none, else two and one per 9 bits of V (and one to clear counts from 2^18 entries on).
  */
 size_t dspark_embedding_grad_workspace_bytes(int N, int V, int D);
 dspark_status dspark_embedding_grad(int N, int V, int D, float scale, dspark_dtype gdt, const void* grad,

@@ -9,8 +9,9 @@
 //   - more, a stable radix sort with digits of at most 9 bits: two or three scatter launches.
 // Then one launch sums slices of the sorted positions (a warp per slice and 512 bytes of columns,
 // eight rows in flight) and, in other blocks, zeroes the rows of tokens that do not occur, which a
-// bitmap names.  A run inside one slice is written at once; a longer one leaves one fp32 partial
-// sum per slice, and a last launch adds those up in their order.
+// bitmap names.  A run inside one slice is written at once; of a longer one every slice's warp leaves
+// an fp32 partial sum, and the last of them to arrive (a counter per run and columns, no waits) adds
+// those up in their order.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -42,11 +43,15 @@ struct Row<T, 1> {
   __device__ __forceinline__ void get(float* f) const { f[0] = to_f<T>(x); }
 };
 
-// E floats to consecutive elements (aligned to E elements for E > 1), rounded once
+// E floats to consecutive elements (aligned to E elements), rounded once
 template <int E>
 __device__ __forceinline__ void store(float* p, const float* f) {
   if (E == 1) {
     *p = f[0];
+  } else if (E == 8) {  // one 32-byte store: whole sectors
+    asm volatile("st.global.cs.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0]), "f"(f[1 % E]),
+                 "f"(f[2 % E]), "f"(f[3 % E]), "f"(f[4 % E]), "f"(f[5 % E]), "f"(f[6 % E]), "f"(f[7 % E])
+                 : "memory");
   } else {
 #pragma unroll
     for (int i = 0; i < E; i += 4) __stcs((float4*)(p + i), make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]));
@@ -76,6 +81,23 @@ template <int E>
 __device__ __forceinline__ void load_out(const bf16* p, float* f) {
 #pragma unroll
   for (int i = 0; i < E; ++i) f[i] = __bfloat162float(p[i]);
+}
+
+// partial sums that other blocks have written
+template <int E>
+__device__ __forceinline__ void load_part(const float* p, float* f) {
+  if (E == 1) {
+    f[0] = __ldcg(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; i += 4) {
+      const float4 v = __ldcg((const float4*)(p + i));
+      f[i] = v.x;
+      f[(i + 1) % E] = v.y;
+      f[(i + 2) % E] = v.z;
+      f[(i + 3) % E] = v.w;
+    }
+  }
 }
 
 // ------------------------------------------------------------------ lookup
@@ -124,7 +146,7 @@ template <typename TW, typename TO>
 cudaError_t embed_run(int N, int V, int D, float scale, const TW* W, const int32_t* tokens, TO* out,
                       cudaStream_t stream) {
   constexpr int E = 16 / (int)sizeof(TW);
-  const bool vec = D % E == 0 && ((uintptr_t)W % 16) == 0 && ((uintptr_t)out % (E * sizeof(TO) < 16 ? 8 : 16)) == 0;
+  const bool vec = D % E == 0 && ((uintptr_t)W % 16) == 0 && ((uintptr_t)out % (E * sizeof(TO))) == 0;
   const long long pieces = (long long)N * (vec ? D / E : D);
   const unsigned grid = (unsigned)((pieces + kEThr * kLook - 1) / (kEThr * kLook));
   if (vec)
@@ -138,15 +160,14 @@ cudaError_t embed_run(int N, int V, int D, float scale, const TW* W, const int32
 constexpr int kPairs = 4096;      // most tokens that are sorted by counting all pairs
 constexpr int kBinBits = 9, kBins = 1 << kBinBits;
 constexpr int kSortThr = 512, kSortWarps = kSortThr / 32;
-constexpr int kTile = 2048;       // keys per tile of a sort block
+constexpr int kTile = 1024;       // keys per tile of a sort block
 constexpr int kSortBlocks = 64;   // most blocks of a sort launch
 constexpr int kMaxSlices = 2048;
 constexpr size_t kMapBytes = (1u << 24) / 8;
 
 struct EgWs {
   WsHeader* hdr;
-  unsigned* nrun;      // [1] runs that cross slices
-  unsigned* run;       // [slices] the slices in which they begin
+  unsigned* count;     // [slices][column tiles] arrivals at the run that begins in the slice
   uint32_t* map;       // bit v: token v occurs; zero between calls
   uint32_t* key[2];    // [N] sorted tokens
   uint32_t* pos[2];    // [N] their positions
@@ -173,8 +194,7 @@ size_t eg_layout(int N, int D, uint8_t* base, EgWs* ws) {
   EgWs w;
   w.hdr = (WsHeader*)base;
   w.map = (uint32_t*)take(kMapBytes);  // (one size and place for every V: it stays clear)
-  w.nrun = (unsigned*)take(4);
-  w.run = (unsigned*)take(slice_room(N) * 4);
+  w.count = (unsigned*)take(slice_room(N) * (((size_t)D + 31) / 32) * 4);
   for (int i = 0; i < 2; ++i) {
     w.key[i] = (uint32_t*)take((size_t)N * 4);
     w.pos[i] = (uint32_t*)take((size_t)N * 4);
@@ -195,14 +215,14 @@ __device__ __forceinline__ uint32_t key_of(int t, int V, unsigned* status) {
 // ------------------------------------------------------------------ sort, few tokens
 // A block ranks 32 positions, one per lane; its warps share out the positions compared with.
 __global__ void __launch_bounds__(kEThr) pairs_kernel(int N, int V, const int32_t* __restrict__ tokens,
-                                                      int mark, EgWs ws) {
+                                                      int mark, int ncount, EgWs ws) {
   __shared__ __align__(16) uint32_t key[kPairs];
   __shared__ int cnt[kEThr / 32][32];
   const int lane = (int)(threadIdx.x & 31), warp = (int)(threadIdx.x >> 5);
   const int n4 = (N + 3) & ~3;
   for (int i = threadIdx.x; i < n4; i += kEThr)
     key[i] = i < N ? key_of(tokens[i], V, &ws.hdr->status) : 0xFFFFFFFFu;  // (larger than any)
-  if (blockIdx.x == 0 && threadIdx.x == 0) *ws.nrun = 0u;
+  for (int i = (int)(blockIdx.x * kEThr + threadIdx.x); i < ncount; i += (int)gridDim.x * kEThr) ws.count[i] = 0u;
   __syncthreads();
   const int i0 = (int)blockIdx.x * 32, i = i0 + lane;
   const uint32_t k = i < N ? key[i] : 0u;
@@ -235,13 +255,13 @@ __global__ void __launch_bounds__(kEThr) pairs_kernel(int N, int V, const int32_
 // by the scatter before them).
 __global__ void __launch_bounds__(kSortThr) count_kernel(int N, int V, int per_block, int bits,
                                                          const int32_t* __restrict__ tokens, int mark,
-                                                         EgWs ws) {
+                                                         int ncount, EgWs ws) {
   __shared__ unsigned h[kBins];
   for (int b = threadIdx.x; b < kBins; b += kSortThr) {
     h[b] = 0u;
     ws.hist[1][blockIdx.x * kBins + b] = 0u;
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) *ws.nrun = 0u;
+  for (int i = (int)(blockIdx.x * kSortThr + threadIdx.x); i < ncount; i += (int)gridDim.x * kSortThr) ws.count[i] = 0u;
   __syncthreads();
   const int i1 = min((long long)N, (long long)(blockIdx.x + 1) * per_block);
   for (int i = (int)blockIdx.x * per_block + (int)threadIdx.x; i < i1; i += kSortThr) {
@@ -271,6 +291,7 @@ __global__ void __launch_bounds__(kSortThr) scatter_kernel(int N, int V, int per
   const int nb = (int)gridDim.x;
   {  // base[d]: keys of lower digits, and of this digit in the blocks before
     unsigned below = 0u, all = 0u;
+#pragma unroll 8
     for (int b = 0; b < nb; ++b) {
       const unsigned h = hist[b * kBins + tid];
       all += h;
@@ -362,6 +383,53 @@ __device__ __forceinline__ void put_row(TO* o, const float* s, float scale, int 
   store<E>(o, f);
 }
 
+// One slice's part of a run that crosses slices has been stored (part 1 of the slice in which it
+// begins, part 0 of the others).  The last warp to arrive adds the parts up in their order.
+template <typename TO, int E>
+__device__ __noinline__ void join(const SumArgs& a, TO* gW, uint32_t k, int slice, bool begun, int tile,
+                                  int lane, int col, bool live) {
+  int s0 = slice, s1 = slice;  // the slices in which the run begins and ends
+  if (!begun) {
+    for (s0 = slice - 1;; s0 -= 32) {
+      const int t = s0 - lane;  // does the run go on from slice t - 1 into t?
+      const unsigned in = __ballot_sync(0xffffffffu, t >= 1 && a.key[(long long)t * a.plen - 1] == k);
+      if (in != 0xffffffffu) {
+        s0 -= __ffs(~in) - 1;
+        break;
+      }
+    }
+  }
+  for (;; s1 += 32) {
+    const int t = s1 + 1 + lane;
+    const unsigned in = __ballot_sync(0xffffffffu, t < a.nslice && a.key[(long long)t * a.plen] == k);
+    if (in != 0xffffffffu) {
+      s1 += __ffs(~in) - 1;
+      break;
+    }
+  }
+  __threadfence();
+  __syncwarp();
+  unsigned last = 0u;
+  if (lane == 0) last = atomicAdd(&a.ws.count[(long long)s0 * a.ntile + tile], 1u) == (unsigned)(s1 - s0);
+  if (!__shfl_sync(0xffffffffu, last, 0)) return;
+  __threadfence();
+  if (!live) return;
+  float s[E] = {};
+  for (int c = s0; c <= s1; c += kAhead) {
+    float f[kAhead][E];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (c + j <= s1) load_part<E>(a.ws.part + ((long long)(c + j) * 2 + (c + j == s0 ? 1 : 0)) * a.D + col, f[j]);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (c + j <= s1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) s[e] += f[j][e];
+      }
+  }
+  put_row<TO, E>(gW + (long long)k * a.D + col, s, a.scale, a.accumulate);
+}
+
 template <typename TG, typename TO, int E>
 __global__ void __launch_bounds__(kEThr) sum_kernel(const SumArgs a, const TG* __restrict__ grad,
                                                     TO* __restrict__ gW) {
@@ -402,6 +470,7 @@ __global__ void __launch_bounds__(kEThr) sum_kernel(const SumArgs a, const TG* _
   const uint32_t after = p1 < a.N ? a.key[p1] : 0xFFFFFFFFu;
   uint32_t cur = a.key[p0];
   bool begun = cur != before;  // the current run begins in this slice
+  uint32_t crossed = none;     // the run that came from the slice before, once it has ended
   float s[E] = {};
   for (long long b = p0; b < p1; b += 32) {
     const int n = (int)min(32ll, p1 - b);
@@ -426,6 +495,7 @@ __global__ void __launch_bounds__(kEThr) sum_kernel(const SumArgs a, const TG* _
             else
               store<E>(a.ws.part + (long long)slice * 2 * a.D + col, s);
           }
+          if (!begun) crossed = cur;
           cur = k[j];
           begun = true;
 #pragma unroll
@@ -440,90 +510,30 @@ __global__ void __launch_bounds__(kEThr) sum_kernel(const SumArgs a, const TG* _
       }
     }
   }
+  if (crossed != none) join<TO, E>(a, gW, crossed, slice, false, tile, lane, col, live);
   if (cur == none) return;
-  if (!begun) {
-    if (live) store<E>(a.ws.part + (long long)slice * 2 * a.D + col, s);
-  } else if (cur == after) {
-    if (live) store<E>(a.ws.part + ((long long)slice * 2 + 1) * a.D + col, s);
-    if (tile == 0 && lane == 0) a.ws.run[atomicAdd(a.ws.nrun, 1u)] = (unsigned)slice;
-  } else if (live) {
-    put_row<TO, E>(gW + (long long)cur * a.D + col, s, a.scale, a.accumulate);
+  if (begun && cur != after) {
+    if (live) put_row<TO, E>(gW + (long long)cur * a.D + col, s, a.scale, a.accumulate);
+    return;
   }
-}
-
-// Runs that cross slices: the begun part, then the part of every slice that the run goes on in.
-// A block takes one run and column tile; its warps add contiguous shares of the parts, joined in order.
-template <typename TO, int E>
-__global__ void __launch_bounds__(kEThr) join_kernel(const SumArgs a, TO* __restrict__ gW) {
-  __shared__ float sh[kEThr / 32][32 * E];
-  const int lane = (int)(threadIdx.x & 31), warp = (int)(threadIdx.x >> 5);
-  const long long items = (long long)*a.ws.nrun * a.ntile;
-  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-    const int s0 = (int)a.ws.run[it / a.ntile], tile = (int)(it % a.ntile);
-    const uint32_t k = a.key[(long long)s0 * a.plen + a.plen - 1];
-    int m = 0;  // slices after s0 whose first key is still k
-    for (;;) {
-      const int s = s0 + 1 + m + lane;
-      const unsigned go = __ballot_sync(0xffffffffu, s < a.nslice && a.key[(long long)s * a.plen] == k);
-      if (go == 0xffffffffu) {
-        m += 32;
-        continue;
-      }
-      m += __ffs(~go) - 1;
-      break;
-    }
-    const int per = (m + 1 + kEThr / 32 - 1) / (kEThr / 32);
-    const int c0 = warp * per, c1 = min(m + 1, c0 + per);  // part 0 is s0's second, part i s0 + i's first
-    const int col = (tile * 32 + lane) * E;
-    float s[E] = {};
-    if (col < a.D) {
-      for (int c = c0; c < c1; c += kAhead) {
-        float f[kAhead][E];
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-          if (c + j < c1) load_out<E>(a.ws.part + ((long long)(s0 + c + j) * 2 + (c + j == 0 ? 1 : 0)) * a.D + col, f[j]);
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-          if (c + j < c1) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) s[e] += f[j][e];
-          }
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) sh[warp][lane * E + e] = s[e];
-    __syncthreads();
-    if (warp == 0 && col < a.D) {
-      for (int w = 1; w < kEThr / 32; ++w)
-#pragma unroll
-        for (int e = 0; e < E; ++e) s[e] += sh[w][lane * E + e];
-      put_row<TO, E>(gW + (long long)k * a.D + col, s, a.scale, a.accumulate);
-    }
-    __syncthreads();
-  }
+  if (live) store<E>(a.ws.part + ((long long)slice * 2 + (begun ? 1 : 0)) * a.D + col, s);
+  join<TO, E>(a, gW, cur, slice, begun, tile, lane, col, live);
 }
 
 template <typename TG, typename TO, int E>
 cudaError_t sums(SumArgs a, const TG* grad, TO* gW, cudaStream_t stream) {
-  a.ntile = (a.D + 32 * E - 1) / (32 * E);
   const int words = (a.V + 31) / 32;
   a.fill_blocks = a.accumulate ? 0 : words < 16384 ? words : 16384;
   const long long warps = (long long)a.nslice * a.ntile;
   const unsigned grid = (unsigned)((warps + kEThr / 32 - 1) / (kEThr / 32)) + (unsigned)a.fill_blocks;
   if (grid == 0) return cudaSuccess;
   sum_kernel<TG, TO, E><<<grid, kEThr, 0, stream>>>(a, grad, gW);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || a.nslice < 2) return e;
-  join_kernel<TO, E><<<304, kEThr, 0, stream>>>(a, gW);
   return cudaGetLastError();
 }
 
 template <typename TG, typename TO>
-cudaError_t sums_by_shape(const SumArgs& a, const TG* grad, TO* gW, cudaStream_t stream) {
-  constexpr int E = 16 / (int)sizeof(TG);
-  if (a.D % E == 0 && ((uintptr_t)grad % 16) == 0 && ((uintptr_t)gW % 16) == 0)
-    return sums<TG, TO, E>(a, grad, gW, stream);
-  return sums<TG, TO, 1>(a, grad, gW, stream);
+cudaError_t sums_by_shape(const SumArgs& a, bool vec, const TG* grad, TO* gW, cudaStream_t stream) {
+  return vec ? sums<TG, TO, 16 / (int)sizeof(TG)>(a, grad, gW, stream) : sums<TG, TO, 1>(a, grad, gW, stream);
 }
 
 }  // namespace
@@ -550,11 +560,14 @@ cudaError_t launch_embedding_grad(int N, int V, int D, float scale, int g_bf16, 
   a.accumulate = accumulate;
   a.plen = N > 0 ? slice_len(N) : 32;
   a.nslice = (int)(((long long)N + a.plen - 1) / a.plen);
-  const int mark = !accumulate;
+  const int E = g_bf16 ? 8 : 4;
+  const bool vec = D % E == 0 && ((uintptr_t)grad % 16) == 0 && ((uintptr_t)gW % 32) == 0;
+  a.ntile = vec ? (D / E + 31) / 32 : (D + 31) / 32;
+  const int mark = !accumulate, ncount = a.nslice * a.ntile;
   cudaError_t e = cudaSuccess;
   int at = 0;
   if (N > 0 && N <= kPairs) {
-    pairs_kernel<<<(N + 31) / 32, kEThr, 0, stream>>>(N, V, tokens, mark, a.ws);
+    pairs_kernel<<<(N + 31) / 32, kEThr, 0, stream>>>(N, V, tokens, mark, ncount, a.ws);
     e = cudaGetLastError();
   } else if (N > 0) {
     int bits = 1;  // keys are 0 .. V
@@ -564,7 +577,7 @@ cudaError_t launch_embedding_grad(int N, int V, int D, float scale, int g_bf16, 
     const int nb0 = tiles < kSortBlocks ? tiles : kSortBlocks;
     const int per_block = (tiles + nb0 - 1) / nb0 * kTile;
     const int nb = (N + per_block - 1) / per_block;
-    count_kernel<<<nb, kSortThr, 0, stream>>>(N, V, per_block, digit, tokens, mark, a.ws);
+    count_kernel<<<nb, kSortThr, 0, stream>>>(N, V, per_block, digit, tokens, mark, ncount, a.ws);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     for (int p = 0; p < passes; ++p) {
       const int last = p == passes - 1;
@@ -583,10 +596,10 @@ cudaError_t launch_embedding_grad(int N, int V, int D, float scale, int g_bf16, 
   if (e != cudaSuccess) return e;
   a.key = a.ws.key[at];
   a.pos = a.ws.pos[at];
-  if (g_bf16 && o_bf16) return sums_by_shape(a, (const bf16*)grad, (bf16*)gW, stream);
-  if (g_bf16) return sums_by_shape(a, (const bf16*)grad, (float*)gW, stream);
-  if (o_bf16) return sums_by_shape(a, (const float*)grad, (bf16*)gW, stream);
-  return sums_by_shape(a, (const float*)grad, (float*)gW, stream);
+  if (g_bf16 && o_bf16) return sums_by_shape(a, vec, (const bf16*)grad, (bf16*)gW, stream);
+  if (g_bf16) return sums_by_shape(a, vec, (const bf16*)grad, (float*)gW, stream);
+  if (o_bf16) return sums_by_shape(a, vec, (const float*)grad, (bf16*)gW, stream);
+  return sums_by_shape(a, vec, (const float*)grad, (float*)gW, stream);
 }
 
 }  // namespace dspark
