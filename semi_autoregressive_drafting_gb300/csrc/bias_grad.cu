@@ -5,16 +5,19 @@
 //   grad_a[n][j] = sum_v G[n][v] W2[v][j],   grad_W2[v][j] = sum_n G[n][v] a[n][j].
 //
 // bf16 weights: two tensor-core products (tcgen05, kind::f16, fp32 accumulation in TMEM), each with
-// G as the M-side operand in tiles of up to 256 x 64, so that the 256-column operand that passes by
-// (W2 or a) is read once per 256 rows of M:
-//   grad_W2: M = 256 vocabulary entries (G as it lies is M-major), K = N; one tile per work item;
-//   grad_a:  M = 256 rows, K = a share of the vocabulary (G as it lies is K-major); the shares'
+// G as the M-side operand and 256 columns of the other one:
+//   grad_W2: M = 128 vocabulary entries (G as it lies is M-major), K = N; one tile per work item;
+//   grad_a:  M = 128 rows, K = a share of the vocabulary (G as it lies is K-major); the shares'
 //            fp32 results are added in order by a second launch.
-// A block per SM walks over its work items: a TMA thread, one thread that issues the MMAs, four
+// A block per SM walks over its work items: a TMA thread, one thread that issues the MMAs, eight
 // warps that read the accumulators out of TMEM.  An fp32 G enters as two bf16 parts, G = hi + lo with
 // hi = bf16(G), lo = bf16(G - hi) (16 significant bits or more, an error of at most 2^-18 |G|,
 // below that of an fp32 sum of these lengths); eight warps split it on its way from global to
 // shared memory.  The same warps bring a G whose rows TMA cannot address.
+//
+// The tensor cores add into fp32 accumulators with truncation: over a long K the sums shrink by about
+// 2e-8 of themselves per MMA (measured: 1.5e-5 after 784).  So after every 32 MMAs of a tile the
+// accumulators are added, rounded to nearest, to a second set of 256 TMEM columns and start anew.
 // fp32 weights (small heads): CUDA-core tiles.
 #include <cuda.h>
 
@@ -88,11 +91,12 @@ constexpr int kTileA = 2 * kBox;      // 128 (M) x 64 (K) of G
 constexpr int kBytesB = 4 * kBox;     // 64 (K) x 256 of W2 or a
 constexpr int kBN = 256;              // columns per work item
 constexpr int kMaxItems = 2;          // work items per SM at most when the vocabulary is shared out
+constexpr int kRun = 32;              // MMAs of K = 16 into one set of accumulators
 
 struct BgArgs {
   int N, V, r;
   int items, nrb;       // work items; blocks of 256 columns of r
-  int nmb;              // grad_a: blocks of 256 rows
+  int nmb;              // grad_a: blocks of 128 rows
   int per_split;        // grad_a: K stages per share of the vocabulary
   int nstage_k;         // K stages in all
   int b_kmajor;         // grad_a: W2 is [r][V]
@@ -119,9 +123,9 @@ __device__ __forceinline__ bool wait_or(uint64_t* bar, uint32_t parity, volatile
   return true;
 }
 
-// One work item: M tiles of 128 (1 or 2), their first row, the first and last K stage, the first column.
+// One work item: the tile's first row, its first and last K stage, its columns.
 struct Item {
-  int m0, tiles, k0, k1, c0, cols, split;
+  int m0, k0, k1, c0, cols, split;
 };
 template <bool WANT_A>
 __device__ __forceinline__ Item item_of(const BgArgs& a, int i) {
@@ -131,17 +135,15 @@ __device__ __forceinline__ Item item_of(const BgArgs& a, int i) {
   t.c0 = rb * kBN;
   t.cols = min(kBN, a.r - t.c0);
   if (WANT_A) {
-    t.m0 = (i % a.nmb) * 256;
+    t.m0 = (i % a.nmb) * 128;
     t.split = i / a.nmb;
     t.k0 = t.split * a.per_split;
     t.k1 = min(a.nstage_k, t.k0 + a.per_split);
-    t.tiles = a.N - t.m0 > 128 ? 2 : 1;
   } else {
-    t.m0 = i * 256;
+    t.m0 = i * 128;
     t.split = 0;
     t.k0 = 0;
     t.k1 = a.nstage_k;
-    t.tiles = a.V - t.m0 > 128 ? 2 : 1;
   }
   return t;
 }
@@ -172,11 +174,52 @@ template <int MODE>
 struct Src {
   static constexpr bool kTma = MODE == 0, kVec = MODE == 1;
   static constexpr int kParts = MODE == 1 || MODE == 2 ? 2 : 1;
-  static constexpr int kStages = kParts == 2 ? 2 : 3;
-  static constexpr int kStage = kParts * 2 * kTileA + kBytesB;
-  static constexpr int kThreads = kTma ? 256 : 512;
+  static constexpr int kStages = kParts == 2 ? 3 : 4;
+  static constexpr int kStage = kParts * kTileA + kBytesB;
+  static constexpr int kRunStages = kRun / 4 / kParts;
+  static constexpr int kThreads = kTma ? 384 : 640;
   using T = typename std::conditional<MODE == 3, bf16, float>::type;
 };
+
+// Uses of registers that a TMEM load writes come after the wait for it.
+__device__ __forceinline__ void loaded(uint32_t (&v)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(v[j]));
+}
+
+// 32 columns of one row of a tile, from column c of the item's on.
+template <bool WANT_A>
+__device__ __forceinline__ void write_out(const BgArgs& a, const Item& t, int row, int c, const uint32_t (&v)[32]) {
+  if (!WANT_A && a.out_rv) {
+    float* o = a.out + (size_t)(t.c0 + c) * a.V + row;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (c + j < t.cols) {
+        float x = __uint_as_float(v[j]);
+        if (a.accumulate) x += o[(size_t)j * a.V];
+        __stcs(o + (size_t)j * a.V, x);
+      }
+  } else {
+    float* o = a.out + (WANT_A ? ((size_t)t.split * a.N + row) : (size_t)row) * a.r + t.c0 + c;
+#pragma unroll
+    for (int j = 0; j < 32; j += 4)  // (r is a multiple of 8)
+      if (c + j < t.cols) {
+        float4 f = make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]), __uint_as_float(v[j + 2]),
+                               __uint_as_float(v[j + 3]));
+        if (!WANT_A && a.accumulate) {
+          const float4 x = *(const float4*)(o + j);
+          f.x += x.x;
+          f.y += x.y;
+          f.z += x.z;
+          f.w += x.w;
+        }
+        if (WANT_A)
+          *(float4*)(o + j) = f;
+        else
+          __stcs((float4*)(o + j), f);
+      }
+  }
+}
 
 template <bool WANT_A, int MODE>
 __global__ void __launch_bounds__(Src<MODE>::kThreads, 1)
@@ -192,7 +235,7 @@ __global__ void __launch_bounds__(Src<MODE>::kThreads, 1)
   uint32_t* tbase = (uint32_t*)(tfree + 1);
   volatile int* stop = (volatile int*)(tbase + 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kOffB = S::kParts * 2 * kTileA;
+  constexpr int kOffB = S::kParts * kTileA;
 
   if (tid == 0) {
     for (int i = 0; i < S::kStages; ++i) {
@@ -200,7 +243,7 @@ __global__ void __launch_bounds__(Src<MODE>::kThreads, 1)
       mbar_init(&empty[i], 1);
     }
     mbar_init(done, 1);
-    mbar_init(tfree, 4);
+    mbar_init(tfree, 8);
     *stop = 0;
     fence_mbar_init();
   }
@@ -221,7 +264,7 @@ __global__ void __launch_bounds__(Src<MODE>::kThreads, 1)
       for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
         const Item t = item_of<WANT_A>(a, i);
         const int nb = (t.cols + 63) / 64;
-        const uint32_t bytes = (uint32_t)(nb * kBox + (S::kTma ? t.tiles * kTileA : 0));
+        const uint32_t bytes = (uint32_t)(nb * kBox + (S::kTma ? kTileA : 0));
         for (int s = t.k0; s < t.k1; ++s, ++g) {
           const int slot = g % S::kStages;
           if (g >= S::kStages && !wait_or(&empty[slot], (uint32_t)((g / S::kStages - 1) & 1), stop)) {
@@ -231,7 +274,7 @@ __global__ void __launch_bounds__(Src<MODE>::kThreads, 1)
           uint8_t* st = smem + slot * S::kStage;
           mbar_expect_tx(&full[slot], bytes);
           if (S::kTma) {
-            for (int b = 0; b < 2 * t.tiles; ++b)
+            for (int b = 0; b < 2; ++b)
               if (WANT_A)
                 tc::tma_load_2d(st + b * kBox, &tmG, s * 64, t.m0 + 64 * b, &full[slot], once);
               else
@@ -250,43 +293,46 @@ __global__ void __launch_bounds__(Src<MODE>::kThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0) {  // ---- MMA
-      int g = 0, n = 0;
+      int g = 0, n = 0;  // stages and runs so far
       bool ok = true;
-      for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x, ++n) {
+      for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
         const Item t = item_of<WANT_A>(a, i);
         const uint32_t idesc = tc::idesc_bf16_f32(128, (t.cols + 15) / 16 * 16) |
                                (WANT_A ? 0u : tc::kIdescAMajorMN) |
                                (WANT_A && a.b_kmajor ? 0u : tc::kIdescBMajorMN);
-        if (n > 0 && !wait_or(tfree, (uint32_t)((n - 1) & 1), stop)) {
-          ok = false;
-          break;
-        }
-        tc::fence_after_sync();
-        for (int s = t.k0; s < t.k1; ++s, ++g) {
-          const int slot = g % S::kStages;
-          if (!wait_or(&full[slot], (uint32_t)((g / S::kStages) & 1), stop)) {
+        for (int s0 = t.k0; ok && s0 < t.k1; s0 += S::kRunStages) {
+          if (n > 0 && !wait_or(tfree, (uint32_t)((n - 1) & 1), stop)) {
             ok = false;
             break;
           }
           tc::fence_after_sync();
-          const uint32_t sa = smem_u32(smem + slot * S::kStage), sb = sa + kOffB;
-          // K-major: 16 elements of K are 32 bytes along the rows; M- or N-major: 16 rows of 128 bytes
-          const uint64_t bd = WANT_A && a.b_kmajor ? tc::sdesc_sw128(sb) : tc::sdesc_sw128_mn(sb, kBox);
-          const uint64_t bstep = WANT_A && a.b_kmajor ? 2 : 128;
-          for (int m = 0; m < t.tiles; ++m) {
+          const int s1 = min(t.k1, s0 + S::kRunStages);
+          for (int s = s0; s < s1; ++s, ++g) {
+            const int slot = g % S::kStages;
+            if (!wait_or(&full[slot], (uint32_t)((g / S::kStages) & 1), stop)) {
+              ok = false;
+              break;
+            }
+            tc::fence_after_sync();
+            const uint32_t sa = smem_u32(smem + slot * S::kStage), sb = sa + kOffB;
+            // K-major: 16 elements of K are 32 bytes along the rows; M- or N-major: 16 rows of 128 bytes
+            const uint64_t bd = WANT_A && a.b_kmajor ? tc::sdesc_sw128(sb) : tc::sdesc_sw128_mn(sb, kBox);
+            const uint64_t bstep = WANT_A && a.b_kmajor ? 2 : 128;
 #pragma unroll
             for (int h = 0; h < S::kParts; ++h) {
-              const uint32_t at = sa + (uint32_t)(h * 2 + m) * kTileA;
+              const uint32_t at = sa + (uint32_t)h * kTileA;
               const uint64_t ad = WANT_A ? tc::sdesc_sw128(at) : tc::sdesc_sw128_mn(at, kBox);
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                tc::mma_bf16(tmem + m * kBN, ad + (WANT_A ? 2 : 128) * kk, bd + bstep * kk, idesc,
-                             (s - t.k0) | h | kk);
+                tc::mma_bf16(tmem, ad + (WANT_A ? 2 : 128) * kk, bd + bstep * kk, idesc, (s - s0) | h | kk);
             }
+            tc::mma_commit(&empty[slot]);
           }
-          tc::mma_commit(&empty[slot]);
+          if (ok) {
+            tc::mma_commit(done);
+            ++n;
+          }
         }
-        if (ok) tc::mma_commit(done);
       }
       if (!ok) {
         atomicMax(a.status, kErrTimeout);
@@ -296,131 +342,119 @@ __global__ void __launch_bounds__(Src<MODE>::kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp >= 4 && warp < 8) {  // ---- accumulators to global memory
-    const int q = warp & 3;
+  } else if (warp >= 4 && warp < 12) {  // ---- accumulators: to the sums, or to global memory
+    const int q = warp & 3, c_lo = warp < 8 ? 0 : kBN / 2;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
     int n = 0;
-    for (int i = blockIdx.x; i < a.items; i += gridDim.x, ++n) {
+    bool ok = true;
+    for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
       const Item t = item_of<WANT_A>(a, i);
-      bool ok = true;
-      if (lane == 0) ok = wait_or(done, (uint32_t)(n & 1), stop, kWaitLimitNs + 20000ull * (unsigned)(t.k1 - t.k0));
-      if (!__shfl_sync(0xffffffffu, ok, 0)) {
-        if (lane == 0) atomicMax(a.status, kErrTimeout);
-        break;
-      }
-      tc::fence_after_sync();
-      for (int m = 0; m < t.tiles; ++m) {
-        const int row = t.m0 + 128 * m + 32 * q + lane;
-        const bool live = row < (WANT_A ? a.N : a.V);
-        for (int c = 0; c < t.cols; c += 32) {
-          uint32_t v[32];
-          __syncwarp();
-          tc::tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + m * kBN + c, v);
-          tc::tmem_ld_wait();
-          if (!live) continue;
-          if (!WANT_A && a.out_rv) {
-            float* o = a.out + (size_t)(t.c0 + c) * a.V + row;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c + j < t.cols) {
-                float x = __uint_as_float(v[j]);
-                if (a.accumulate) x += o[(size_t)j * a.V];
-                __stcs(o + (size_t)j * a.V, x);
-              }
-          } else {
-            float* o = a.out + (WANT_A ? ((size_t)t.split * a.N + row) : (size_t)row) * a.r + t.c0 + c;
-#pragma unroll
-            for (int j = 0; j < 32; j += 8)  // (r is a multiple of 8)
-              if (c + j < t.cols) {
-                float f[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[j + e]);
-                if (!WANT_A && a.accumulate) {
-                  const float4 x = *(const float4*)(o + j), y = *(const float4*)(o + j + 4);
-                  f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
-                  f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
-                }
-                if (WANT_A) {
-                  *(float4*)(o + j) = make_float4(f[0], f[1], f[2], f[3]);
-                  *(float4*)(o + j + 4) = make_float4(f[4], f[5], f[6], f[7]);
-                } else {
-                  __stcs((float4*)(o + j), make_float4(f[0], f[1], f[2], f[3]));
-                  __stcs((float4*)(o + j + 4), make_float4(f[4], f[5], f[6], f[7]));
-                }
-              }
-          }
-        }
-      }
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(tfree);
-    }
-  } else if (!S::kTma && warp >= 8) {  // ---- G from global memory, split into its parts
-    using TG = typename S::T;
-    const TG* G = (const TG*)a.G;
-    const int pt = tid - 256;
-    // a thread's sixteen quads of a stage: grad_a: row (16 i + pt / 16) of 256, quad pt % 16 of the
-    // 64 entries; grad_W2: row (4 i + pt / 64) of 64, quad pt % 64 of the 256 entries
-    const int prow = WANT_A ? pt >> 4 : pt >> 6, pq = WANT_A ? pt & 15 : pt & 63;
-    constexpr int kRowStep = WANT_A ? 16 : 4;
-    float4 r[2][8];
-    auto fetch = [&](const Item& t, int s, int half) {
-      const int row0 = (WANT_A ? t.m0 : s * 64) + prow + half * 8 * kRowStep;
-      const int col = (WANT_A ? s * 64 : t.m0) + 4 * pq;
-      const int n = (WANT_A || pq < 32 * t.tiles) ? a.V - col : 0;
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int row = row0 + u * kRowStep;
-        const bool in = row < a.N && (!WANT_A || half == 0 || t.tiles == 2);
-        r[half][u] = load_quad<TG, S::kVec>(G + (long long)row * a.V + col, in ? n : 0);
-      }
-    };
-    auto put = [&](uint8_t* st, const Item& t, int half) {
-      if (WANT_A ? (half == 1 && t.tiles == 1) : pq >= 32 * t.tiles) return;
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int row = prow + (half * 8 + u) * kRowStep;
-        const int box = WANT_A ? row >> 6 : pq >> 4, y = row & 63, x = pq & 15;
-        const uint32_t at = (uint32_t)(box * kBox + y * 128 + (((x >> 1) ^ (y & 7)) << 4) + (x & 1) * 8);
-        const uint2 hi = pack_hi(r[half][u]);
-        *(uint2*)(st + at) = hi;
-        if (S::kParts == 2) *(uint2*)(st + 2 * kTileA + at) = pack_lo(r[half][u], hi);
-      }
-    };
-    int i = blockIdx.x, g = 0;
-    if (i < a.items) {
-      Item t = item_of<WANT_A>(a, i);
-      int s = t.k0;
-      fetch(t, s, 0);
-      for (;;) {
-        fetch(t, s, 1);
-        Item nt = t;
-        int ns = s + 1, ni = i;
-        if (ns == t.k1) {
-          ni = i + gridDim.x;
-          if (ni < a.items) {
-            nt = item_of<WANT_A>(a, ni);
-            ns = nt.k0;
-          }
-        }
-        const int slot = g % S::kStages;
-        bool ok = true;
-        if (g >= S::kStages && lane == 0) ok = wait_or(&empty[slot], (uint32_t)((g / S::kStages - 1) & 1), stop);
-        if (!__shfl_sync(0xffffffffu, ok, 0)) {
+      const int row = t.m0 + 32 * q + lane, c_hi = min(t.cols, c_lo + kBN / 2);
+      const bool live = row < (WANT_A ? a.N : a.V);
+      for (int s0 = t.k0; s0 < t.k1; s0 += S::kRunStages, ++n) {
+        const bool first = s0 == t.k0, last = s0 + S::kRunStages >= t.k1;
+        if (lane == 0) ok = wait_or(done, (uint32_t)(n & 1), stop);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) {
           if (lane == 0) atomicMax(a.status, kErrTimeout);
           break;
         }
-        uint8_t* st = smem + slot * S::kStage;
-        put(st, t, 0);
-        if (ni < a.items) fetch(nt, ns, 0);
-        put(st, t, 1);
-        fence_proxy_async_smem();
+        tc::fence_after_sync();
+        for (int c = c_lo; c < c_hi; c += 32) {
+          uint32_t v[32];
+          __syncwarp();
+          tc::tmem_ld32(lanes + c, v);
+          if (!first) {
+            uint32_t w[32];
+            tc::tmem_ld32(lanes + kBN + c, w);
+            tc::tmem_ld_wait();
+            loaded(v);
+            loaded(w);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(w[j]));
+          } else {
+            tc::tmem_ld_wait();
+            loaded(v);
+          }
+          if (!last) {
+            tc::tmem_st32(lanes + kBN + c, v);
+          } else if (live) {
+            write_out<WANT_A>(a, t, row, c, v);
+          }
+        }
+        tc::tmem_st_wait();
+        tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[slot]);
-        ++g;
-        if (ni >= a.items) break;
-        t = nt;
-        s = ns;
-        i = ni;
+        if (lane == 0) mbar_arrive(tfree);
+      }
+    }
+  } else if (!S::kTma && warp >= 12) {  // ---- G from global memory, split into its parts
+    using TG = typename S::T;
+    const TG* G = (const TG*)a.G;
+    const int pt = tid - 384;
+    // a thread's eight quads of a stage: grad_a: row (16 u + pt / 16) of 128, quad pt % 16 of the 64
+    // entries; grad_W2: row (8 u + pt / 32) of 64, quad pt % 32 of the 128 entries
+    const int prow = WANT_A ? pt >> 4 : pt >> 5, pq = WANT_A ? pt & 15 : pt & 31;
+    constexpr int kRowStep = WANT_A ? 16 : 8;
+    float4 r[2][8];
+    auto fetch = [&](const Item& t, int s, float4 (&x)[8]) {
+      const int row0 = (WANT_A ? t.m0 : s * 64) + prow;
+      const int col = (WANT_A ? s * 64 : t.m0) + 4 * pq, n = a.V - col;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int row = row0 + u * kRowStep;
+        x[u] = load_quad<TG, S::kVec>(G + (long long)row * a.V + col, row < a.N ? n : 0);
+      }
+    };
+    // the stage after (i, s); i past the last item: none
+    auto step = [&](int& i, Item& t, int& s) {
+      if (++s == t.k1) {
+        i += gridDim.x;
+        if (i < a.items) {
+          t = item_of<WANT_A>(a, i);
+          s = t.k0;
+        }
+      }
+    };
+    int i = blockIdx.x, g = 0, s = 0;
+    Item t = {};
+    if (i < a.items) {
+      t = item_of<WANT_A>(a, i);
+      s = t.k0;
+      fetch(t, s, r[0]);
+      step(i, t, s);
+      for (bool more = true; more;) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {  // stage g is in r[p]; the next goes to the other half
+          if (!more) break;
+          more = i < a.items;
+          if (more) {
+            fetch(t, s, r[p ^ 1]);
+            step(i, t, s);
+          }
+          const int slot = g % S::kStages;
+          bool ok = true;
+          if (g >= S::kStages && lane == 0) ok = wait_or(&empty[slot], (uint32_t)((g / S::kStages - 1) & 1), stop);
+          if (!__shfl_sync(0xffffffffu, ok, 0)) {
+            if (lane == 0) atomicMax(a.status, kErrTimeout);
+            more = false;
+            break;
+          }
+          uint8_t* st = smem + slot * S::kStage;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int row = prow + u * kRowStep;
+            const int box = WANT_A ? row >> 6 : pq >> 4, y = row & 63, x = pq & 15;
+            const uint32_t at = (uint32_t)(box * kBox + y * 128 + (((x >> 1) ^ (y & 7)) << 4) + (x & 1) * 8);
+            const uint2 hi = pack_hi(r[p][u]);
+            *(uint2*)(st + at) = hi;
+            if (S::kParts == 2) *(uint2*)(st + kTileA + at) = pack_lo(r[p][u], hi);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[slot]);
+          ++g;
+        }
       }
     }
   }
@@ -467,10 +501,10 @@ __global__ void __launch_bounds__(256) share_sum_kernel(long long quads, int spl
 
 size_t bg_align(size_t x) { return (x + 255) / 256 * 256; }
 
-// floats of shared-out results at most: kMaxItems work items of 256 x 256 per SM, and no more shares
+// floats of shared-out results at most: kMaxItems work items of 128 x 256 per SM, and no more shares
 // than that many work items
 size_t share_floats(int N, int r, int nsm) {
-  const size_t cap = (size_t)kMaxItems * nsm, all = cap * N * r, tiles = cap * 65536;
+  const size_t cap = (size_t)kMaxItems * nsm, all = cap * N * r, tiles = cap * 128 * kBN;
   return all < tiles ? all : tiles;
 }
 
@@ -517,7 +551,7 @@ cudaError_t tensor(int N, int V, int r, int g_bf16, const void* G, const bf16* a
   if (gW) {
     if (!encode_bf16_2d(&tb, a, N, r, r, 64)) return cudaErrorInvalidValue;
     if (mode != 0) tg = tb;  // (not used)
-    p.items = (V + 255) / 256 * p.nrb;
+    p.items = (V + 127) / 128 * p.nrb;
     p.nstage_k = (N + 63) / 64;
     p.out = gW;
     if ((e = bg_mode<false>(mode, p, tg, tb, nsm, stream)) != cudaSuccess) return e;
@@ -534,12 +568,12 @@ cudaError_t tensor(int N, int V, int r, int g_bf16, const void* G, const bf16* a
     if (!(p.b_kmajor ? encode_bf16_2d(&tb, W, r, V, V, 64) : encode_bf16_2d(&tb, W, V, r, r, 64)))
       return cudaErrorInvalidValue;
     if (mode != 0) tg = tb;
-    p.nmb = (N + 255) / 256;
+    p.nmb = (N + 127) / 128;
     p.nstage_k = (V + 63) / 64;
     // Shares of the vocabulary: the rounds of work items times the stages of one, against writing and
-    // reading the shares' results (microseconds: a stage of 256 x 64 at the memory's rate per SM)
+    // reading the shares' results (microseconds: a stage of 128 x 64 at the memory's rate per SM)
     const int base = p.nmb * p.nrb;
-    const double stage = (g_bf16 ? 0.75 : 1.5), io = (double)N * r * 8 / 6.7e6;
+    const double stage = (g_bf16 ? 0.38 : 0.75), io = (double)N * r * 8 / 6.7e6;
     int splits = 1;
     double best = 1e300;
     for (int s = 1; s <= p.nstage_k && (long long)base * s <= (long long)kMaxItems * nsm; ++s) {
