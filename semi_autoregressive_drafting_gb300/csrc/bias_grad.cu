@@ -9,15 +9,17 @@
 //   grad_W2: M = 128 vocabulary entries (G as it lies is M-major), K = N; one tile per work item;
 //   grad_a:  M = 128 rows, K = a share of the vocabulary (G as it lies is K-major); the shares'
 //            fp32 results are added in order by a second launch.
-// A block per SM walks over its work items: a TMA thread, one thread that issues the MMAs, eight
+// A block per SM walks over its work items: TMA threads, one thread that issues the MMAs, eight
 // warps that read the accumulators out of TMEM.  An fp32 G enters as two bf16 parts, G = hi + lo with
 // hi = bf16(G), lo = bf16(G - hi) (16 significant bits or more, an error of at most 2^-18 |G|,
-// below that of an fp32 sum of these lengths); eight warps split it on its way from global to
-// shared memory.  The same warps bring a G whose rows TMA cannot address.
+// below that of an fp32 sum of these lengths): TMA brings it as it lies, and eight warps split it
+// from one shared-memory buffer into another.  A G whose rows TMA cannot address is read by the same
+// warps, element by element.
 //
 // The tensor cores add into fp32 accumulators with truncation: over a long K the sums shrink by about
-// 2e-8 of themselves per MMA (measured: 1.5e-5 after 784).  So after every 32 MMAs of a tile the
-// accumulators are added, rounded to nearest, to a second set of 256 TMEM columns and start anew.
+// 2e-8 of themselves per MMA (measured: 1.5e-5 after 784).  So a run of 16 MMAs goes to one half of
+// TMEM, and while the next run goes to the other half, the eight warps add the first to sums in their
+// registers (128 columns of a row per thread), rounded to nearest.
 // fp32 weights (small heads): CUDA-core tiles.
 #include <cuda.h>
 
@@ -91,7 +93,12 @@ constexpr int kTileA = 2 * kBox;      // 128 (M) x 64 (K) of G
 constexpr int kBytesB = 4 * kBox;     // 64 (K) x 256 of W2 or a
 constexpr int kBN = 256;              // columns per work item
 constexpr int kMaxItems = 2;          // work items per SM at most when the vocabulary is shared out
-constexpr int kRun = 32;              // MMAs of K = 16 into one set of accumulators
+constexpr int kRun = 16;              // MMAs of K = 16 into one set of accumulators
+constexpr int kRawBytes = 128 * 64 * 4;  // a stage of an fp32 G as it lies
+constexpr int kRaw = 2;               // such stages in flight
+// Registers per thread where eight more warps bring G (640 threads, launched with 96 each): the
+// three shares, 128 x (40 + 2 x 160 + 2 x 56), stay below the launch's 640 x 96.
+constexpr int kRegsIssue = 40, kRegsSums = 160, kRegsBring = 56;
 
 struct BgArgs {
   int N, V, r;
@@ -102,6 +109,7 @@ struct BgArgs {
   int b_kmajor;         // grad_a: W2 is [r][V]
   int out_rv;           // grad_W2 is [r][V]
   int accumulate;
+  int wide;             // out is 32-byte aligned
   float* out;           // grad_W2, or grad_a's shares [split][N][r]
   const void* G;
   unsigned* status;
@@ -149,10 +157,9 @@ __device__ __forceinline__ Item item_of(const BgArgs& a, int i) {
 }
 
 // Four consecutive elements of a row of G, zero from `n` on.
-template <typename TG, bool VEC>
+template <typename TG>
 __device__ __forceinline__ float4 load_quad(const TG* p, int n) {
   if (n <= 0) return make_float4(0.f, 0.f, 0.f, 0.f);
-  if (VEC) return __ldcg((const float4*)p);  // (fp32 only; V is a multiple of 4)
   return make_float4(to_f<TG>(p[0]), n > 1 ? to_f<TG>(p[1]) : 0.f, n > 2 ? to_f<TG>(p[2]) : 0.f,
                      n > 3 ? to_f<TG>(p[3]) : 0.f);
 }
@@ -168,55 +175,49 @@ __device__ __forceinline__ uint2 pack_lo(const float4& f, const uint2& hi) {
                              f.z - __uint_as_float(hi.y << 16), f.w - __uint_as_float(hi.y & 0xFFFF0000u)));
 }
 
-// MODE 0: bf16 G by TMA.  1: fp32 G by 16-byte loads, two parts.  2: fp32 G element by element.
+// MODE 0: bf16 G by TMA.  1: fp32 G by TMA, split into two parts.  2: fp32 G element by element.
 // 3: bf16 G element by element (one part).
 template <int MODE>
 struct Src {
-  static constexpr bool kTma = MODE == 0, kVec = MODE == 1;
+  static constexpr bool kTma = MODE == 0, kTmaRaw = MODE == 1;
   static constexpr int kParts = MODE == 1 || MODE == 2 ? 2 : 1;
-  static constexpr int kStages = kParts == 2 ? 3 : 4;
+  static constexpr int kStages = kParts == 2 ? 2 : 4;
+  static constexpr int kRawAll = kTmaRaw ? kRaw * kRawBytes : 0;
   static constexpr int kStage = kParts * kTileA + kBytesB;
   static constexpr int kRunStages = kRun / 4 / kParts;
   static constexpr int kThreads = kTma ? 384 : 640;
   using T = typename std::conditional<MODE == 3, bf16, float>::type;
 };
 
-// Uses of registers that a TMEM load writes come after the wait for it.
-__device__ __forceinline__ void loaded(uint32_t (&v)[32]) {
-#pragma unroll
-  for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(v[j]));
-}
-
-// 32 columns of one row of a tile, from column c of the item's on.
+// A thread's part of a finished tile: columns c0 .. c0 + 127 of the item's, of one row.
 template <bool WANT_A>
-__device__ __forceinline__ void write_out(const BgArgs& a, const Item& t, int row, int c, const uint32_t (&v)[32]) {
+__device__ __forceinline__ void write_out(const BgArgs& a, const Item& t, int row, int c0, const float (&x)[kBN / 2]) {
   if (!WANT_A && a.out_rv) {
-    float* o = a.out + (size_t)(t.c0 + c) * a.V + row;
+    float* o = a.out + (size_t)(t.c0 + c0) * a.V + row;
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (c + j < t.cols) {
-        float x = __uint_as_float(v[j]);
-        if (a.accumulate) x += o[(size_t)j * a.V];
-        __stcs(o + (size_t)j * a.V, x);
+    for (int j = 0; j < kBN / 2; ++j)
+      if (c0 + j < t.cols) {
+        float f = x[j];
+        if (a.accumulate) f += *o;
+        __stcs(o, f);
+        o += a.V;
       }
   } else {
-    float* o = a.out + (WANT_A ? ((size_t)t.split * a.N + row) : (size_t)row) * a.r + t.c0 + c;
+    float* o = a.out + (WANT_A ? ((size_t)t.split * a.N + row) : (size_t)row) * a.r + t.c0 + c0;
 #pragma unroll
-    for (int j = 0; j < 32; j += 4)  // (r is a multiple of 8)
-      if (c + j < t.cols) {
-        float4 f = make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]), __uint_as_float(v[j + 2]),
-                               __uint_as_float(v[j + 3]));
-        if (!WANT_A && a.accumulate) {
-          const float4 x = *(const float4*)(o + j);
-          f.x += x.x;
-          f.y += x.y;
-          f.z += x.z;
-          f.w += x.w;
+    for (int j = 0; j < kBN / 2; j += 8)  // (r is a multiple of 8)
+      if (c0 + j < t.cols) {
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = !WANT_A && a.accumulate ? x[j + e] + o[j + e] : x[j + e];
+        if (a.wide) {  // whole sectors
+          asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o + j), "f"(f[0]), "f"(f[1]),
+                       "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+                       : "memory");
+        } else {
+          *(float4*)(o + j) = make_float4(f[0], f[1], f[2], f[3]);
+          *(float4*)(o + j + 4) = make_float4(f[4], f[5], f[6], f[7]);
         }
-        if (WANT_A)
-          *(float4*)(o + j) = f;
-        else
-          __stcs((float4*)(o + j), f);
       }
   }
 }
@@ -228,11 +229,14 @@ __global__ void __launch_bounds__(Src<MODE>::kThreads, 1)
   using S = Src<MODE>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint64_t* full = (uint64_t*)(smem + S::kStages * S::kStage);
+  uint8_t* raw = smem + S::kStages * S::kStage;
+  uint64_t* full = (uint64_t*)(raw + S::kRawAll);
   uint64_t* empty = full + S::kStages;
-  uint64_t* done = empty + S::kStages;
-  uint64_t* tfree = done + 1;
-  uint32_t* tbase = (uint32_t*)(tfree + 1);
+  uint64_t* done = empty + S::kStages;  // [2]: a run's MMAs are complete
+  uint64_t* tfree = done + 2;           // [2]: its accumulators have been read
+  uint64_t* rfull = tfree + 2;          // [kRaw]
+  uint64_t* rempty = rfull + kRaw;
+  uint32_t* tbase = (uint32_t*)(rempty + kRaw);
   volatile int* stop = (volatile int*)(tbase + 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kOffB = S::kParts * kTileA;
@@ -242,8 +246,14 @@ __global__ void __launch_bounds__(Src<MODE>::kThreads, 1)
       mbar_init(&full[i], 1 + (S::kTma ? 0 : 8));
       mbar_init(&empty[i], 1);
     }
-    mbar_init(done, 1);
-    mbar_init(tfree, 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&done[i], 1);
+      mbar_init(&tfree[i], 8);
+    }
+    for (int i = 0; i < kRaw; ++i) {
+      mbar_init(&rfull[i], 1);
+      mbar_init(&rempty[i], 8);
+    }
     *stop = 0;
     fence_mbar_init();
   }
@@ -256,6 +266,8 @@ __global__ void __launch_bounds__(Src<MODE>::kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = *tbase;
 
+  if (warp < 4) {
+  if (!S::kTma) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
   if (warp == 0) {
     if (lane == 0) {  // ---- TMA
       const uint64_t once = policy_evict_first(), keep = policy_evict_last();
@@ -291,6 +303,26 @@ __global__ void __launch_bounds__(Src<MODE>::kThreads, 1)
       // every copy lands before the block ends (the phase of each slot's last use)
       for (int j = max(0, g - S::kStages); j < g; ++j) mbar_wait(&full[j % S::kStages], (uint32_t)((j / S::kStages) & 1));
     }
+  } else if (S::kTmaRaw && warp == 2) {
+    if (lane == 0) {  // ---- TMA, an fp32 G as it lies
+      const uint64_t once = policy_evict_first();
+      int g = 0;
+      bool ok = true;
+      for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
+        const Item t = item_of<WANT_A>(a, i);
+        for (int s = t.k0; s < t.k1; ++s, ++g) {
+          const int slot = g % kRaw;
+          if (g >= kRaw && !wait_or(&rempty[slot], (uint32_t)((g / kRaw - 1) & 1), stop)) {
+            ok = false;
+            break;
+          }
+          mbar_expect_tx(&rfull[slot], kRawBytes);
+          tc::tma_load_2d(raw + slot * kRawBytes, &tmG, WANT_A ? s * 64 : t.m0, WANT_A ? t.m0 : s * 64, &rfull[slot], once);
+        }
+      }
+      if (!ok) atomicMax(a.status, kErrTimeout);
+      for (int j = max(0, g - kRaw); j < g; ++j) mbar_wait(&rfull[j % kRaw], (uint32_t)((j / kRaw) & 1));
+    }
   } else if (warp == 1) {
     if (lane == 0) {  // ---- MMA
       int g = 0, n = 0;  // stages and runs so far
@@ -301,7 +333,8 @@ __global__ void __launch_bounds__(Src<MODE>::kThreads, 1)
                                (WANT_A ? 0u : tc::kIdescAMajorMN) |
                                (WANT_A && a.b_kmajor ? 0u : tc::kIdescBMajorMN);
         for (int s0 = t.k0; ok && s0 < t.k1; s0 += S::kRunStages) {
-          if (n > 0 && !wait_or(tfree, (uint32_t)((n - 1) & 1), stop)) {
+          const int buf = n & 1;
+          if (n > 1 && !wait_or(&tfree[buf], (uint32_t)((n / 2 - 1) & 1), stop)) {
             ok = false;
             break;
           }
@@ -324,12 +357,12 @@ __global__ void __launch_bounds__(Src<MODE>::kThreads, 1)
               const uint64_t ad = WANT_A ? tc::sdesc_sw128(at) : tc::sdesc_sw128_mn(at, kBox);
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                tc::mma_bf16(tmem, ad + (WANT_A ? 2 : 128) * kk, bd + bstep * kk, idesc, (s - s0) | h | kk);
+                tc::mma_bf16(tmem + buf * kBN, ad + (WANT_A ? 2 : 128) * kk, bd + bstep * kk, idesc, (s - s0) | h | kk);
             }
             tc::mma_commit(&empty[slot]);
           }
           if (ok) {
-            tc::mma_commit(done);
+            tc::mma_commit(&done[buf]);
             ++n;
           }
         }
@@ -337,58 +370,50 @@ __global__ void __launch_bounds__(Src<MODE>::kThreads, 1)
       if (!ok) {
         atomicMax(a.status, kErrTimeout);
         // what was issued completes before TMEM is freed
-        tc::mma_commit(done);
-        mbar_wait(done, (uint32_t)(n & 1));
+        tc::mma_commit(&done[n & 1]);
+        mbar_wait(&done[n & 1], (uint32_t)((n / 2) & 1));
       }
     }
     __syncwarp();
-  } else if (warp >= 4 && warp < 12) {  // ---- accumulators: to the sums, or to global memory
+  }
+  } else if (warp < 12) {  // ---- accumulators to the sums, sums to global memory
+    if (!S::kTma) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSums));
     const int q = warp & 3, c_lo = warp < 8 ? 0 : kBN / 2;
-    const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
+    const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + c_lo;
     int n = 0;
     bool ok = true;
     for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
       const Item t = item_of<WANT_A>(a, i);
-      const int row = t.m0 + 32 * q + lane, c_hi = min(t.cols, c_lo + kBN / 2);
-      const bool live = row < (WANT_A ? a.N : a.V);
+      float x[kBN / 2];
+#pragma unroll
+      for (int j = 0; j < kBN / 2; ++j) x[j] = 0.f;
       for (int s0 = t.k0; s0 < t.k1; s0 += S::kRunStages, ++n) {
-        const bool first = s0 == t.k0, last = s0 + S::kRunStages >= t.k1;
-        if (lane == 0) ok = wait_or(done, (uint32_t)(n & 1), stop);
+        const int buf = n & 1;
+        if (lane == 0) ok = wait_or(&done[buf], (uint32_t)((n / 2) & 1), stop);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) {
           if (lane == 0) atomicMax(a.status, kErrTimeout);
           break;
         }
         tc::fence_after_sync();
-        for (int c = c_lo; c < c_hi; c += 32) {
-          uint32_t v[32];
-          __syncwarp();
-          tc::tmem_ld32(lanes + c, v);
-          if (!first) {
-            uint32_t w[32];
-            tc::tmem_ld32(lanes + kBN + c, w);
-            tc::tmem_ld_wait();
-            loaded(v);
-            loaded(w);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(w[j]));
-          } else {
-            tc::tmem_ld_wait();
-            loaded(v);
+        for (int c = 0; c < kBN / 2; c += 16)
+          if (c_lo + c < t.cols) {
+            uint32_t v[16];
+            tc::tmem_ld16_wait(lanes + buf * kBN + c, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[c + j] += __uint_as_float(v[j]);
           }
-          if (!last) {
-            tc::tmem_st32(lanes + kBN + c, v);
-          } else if (live) {
-            write_out<WANT_A>(a, t, row, c, v);
-          }
-        }
-        tc::tmem_st_wait();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(tfree);
+        if (lane == 0) mbar_arrive(&tfree[buf]);
       }
+      const int row = t.m0 + 32 * q + lane;
+      if (ok && row < (WANT_A ? a.N : a.V)) write_out<WANT_A>(a, t, row, c_lo, x);
+      __syncwarp();
     }
-  } else if (!S::kTma && warp >= 12) {  // ---- G from global memory, split into its parts
+  } else if (!S::kTma) {  // ---- G from global memory, split into its parts
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsBring));
     using TG = typename S::T;
     const TG* G = (const TG*)a.G;
     const int pt = tid - 384;
@@ -396,64 +421,50 @@ __global__ void __launch_bounds__(Src<MODE>::kThreads, 1)
     // entries; grad_W2: row (8 u + pt / 32) of 64, quad pt % 32 of the 128 entries
     const int prow = WANT_A ? pt >> 4 : pt >> 5, pq = WANT_A ? pt & 15 : pt & 31;
     constexpr int kRowStep = WANT_A ? 16 : 8;
-    float4 r[2][8];
-    auto fetch = [&](const Item& t, int s, float4 (&x)[8]) {
-      const int row0 = (WANT_A ? t.m0 : s * 64) + prow;
-      const int col = (WANT_A ? s * 64 : t.m0) + 4 * pq, n = a.V - col;
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int row = row0 + u * kRowStep;
-        x[u] = load_quad<TG, S::kVec>(G + (long long)row * a.V + col, row < a.N ? n : 0);
-      }
-    };
-    // the stage after (i, s); i past the last item: none
-    auto step = [&](int& i, Item& t, int& s) {
-      if (++s == t.k1) {
-        i += gridDim.x;
-        if (i < a.items) {
-          t = item_of<WANT_A>(a, i);
-          s = t.k0;
-        }
-      }
-    };
-    int i = blockIdx.x, g = 0, s = 0;
-    Item t = {};
-    if (i < a.items) {
-      t = item_of<WANT_A>(a, i);
-      s = t.k0;
-      fetch(t, s, r[0]);
-      step(i, t, s);
-      for (bool more = true; more;) {
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {  // stage g is in r[p]; the next goes to the other half
-          if (!more) break;
-          more = i < a.items;
-          if (more) {
-            fetch(t, s, r[p ^ 1]);
-            step(i, t, s);
-          }
-          const int slot = g % S::kStages;
-          bool ok = true;
-          if (g >= S::kStages && lane == 0) ok = wait_or(&empty[slot], (uint32_t)((g / S::kStages - 1) & 1), stop);
-          if (!__shfl_sync(0xffffffffu, ok, 0)) {
-            if (lane == 0) atomicMax(a.status, kErrTimeout);
-            more = false;
-            break;
-          }
-          uint8_t* st = smem + slot * S::kStage;
+    int g = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
+      const Item t = item_of<WANT_A>(a, i);
+      for (int s = t.k0; s < t.k1; ++s, ++g) {
+        const int slot = g % S::kStages;
+        float4 r[8];
+        if (S::kTmaRaw) {
+          if (lane == 0) ok = wait_or(&rfull[g % kRaw], (uint32_t)((g / kRaw) & 1), stop);
+        } else {
+          const int row0 = (WANT_A ? t.m0 : s * 64) + prow;
+          const int col = (WANT_A ? s * 64 : t.m0) + 4 * pq, n = a.V - col;
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
-            const int row = prow + u * kRowStep;
-            const int box = WANT_A ? row >> 6 : pq >> 4, y = row & 63, x = pq & 15;
-            const uint32_t at = (uint32_t)(box * kBox + y * 128 + (((x >> 1) ^ (y & 7)) << 4) + (x & 1) * 8);
-            const uint2 hi = pack_hi(r[p][u]);
-            *(uint2*)(st + at) = hi;
-            if (S::kParts == 2) *(uint2*)(st + kTileA + at) = pack_lo(r[p][u], hi);
+            const int row = row0 + u * kRowStep;
+            r[u] = load_quad<TG>(G + (long long)row * a.V + col, row < a.N ? n : 0);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full[slot]);
-          ++g;
+        }
+        if (ok && g >= S::kStages && lane == 0) ok = wait_or(&empty[slot], (uint32_t)((g / S::kStages - 1) & 1), stop);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) {
+          if (lane == 0) atomicMax(a.status, kErrTimeout);
+          break;
+        }
+        if (S::kTmaRaw) {
+          const float4* in = (const float4*)(raw + (g % kRaw) * kRawBytes) + pt;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) r[u] = in[u * 256];
+        }
+        uint8_t* st = smem + slot * S::kStage;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int row = prow + u * kRowStep;
+          const int box = WANT_A ? row >> 6 : pq >> 4, y = row & 63, x = pq & 15;
+          const uint32_t at = (uint32_t)(box * kBox + y * 128 + (((x >> 1) ^ (y & 7)) << 4) + (x & 1) * 8);
+          const uint2 hi = pack_hi(r[u]);
+          *(uint2*)(st + at) = hi;
+          if (S::kParts == 2) *(uint2*)(st + kTileA + at) = pack_lo(r[u], hi);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (S::kTmaRaw) mbar_arrive(&rempty[g % kRaw]);
+          mbar_arrive(&full[slot]);
         }
       }
     }
@@ -511,7 +522,7 @@ size_t share_floats(int N, int r, int nsm) {
 template <bool WANT_A, int MODE>
 cudaError_t bg_launch(const BgArgs& a, const CUtensorMap& tg, const CUtensorMap& tb, int nsm, cudaStream_t stream) {
   using S = Src<MODE>;
-  const size_t smem = (size_t)S::kStages * S::kStage + 1024 + 256;
+  const size_t smem = (size_t)S::kStages * S::kStage + S::kRawAll + 1024 + 256;
   cudaError_t e = cudaFuncSetAttribute(bias_grad_kernel<WANT_A, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);
   if (e != cudaSuccess) return e;
@@ -544,16 +555,16 @@ cudaError_t tensor(int N, int V, int r, int g_bf16, const void* G, const bf16* a
   p.status = &((WsHeader*)ws)->status;
   p.nmb = p.per_split = p.b_kmajor = 0;
   CUtensorMap tg, tb;
-  if (mode == 0) {
-    if (!encode_bf16_2d(&tg, G, N, V, V, 64)) return cudaErrorInvalidValue;
-  }
+  if (mode == 0 && !encode_bf16_2d(&tg, G, N, V, V, 64)) return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
   if (gW) {
     if (!encode_bf16_2d(&tb, a, N, r, r, 64)) return cudaErrorInvalidValue;
-    if (mode != 0) tg = tb;  // (not used)
+    if (mode == 1 && !encode_f32_2d(&tg, G, N, V, 128, 64)) return cudaErrorInvalidValue;
+    if (mode > 1) tg = tb;  // (not used)
     p.items = (V + 127) / 128 * p.nrb;
     p.nstage_k = (N + 63) / 64;
     p.out = gW;
+    p.wide = ((uintptr_t)gW % 32) == 0;
     if ((e = bg_mode<false>(mode, p, tg, tb, nsm, stream)) != cudaSuccess) return e;
   }
   if (ga) {
@@ -567,7 +578,8 @@ cudaError_t tensor(int N, int V, int r, int g_bf16, const void* G, const bf16* a
     }
     if (!(p.b_kmajor ? encode_bf16_2d(&tb, W, r, V, V, 64) : encode_bf16_2d(&tb, W, V, r, r, 64)))
       return cudaErrorInvalidValue;
-    if (mode != 0) tg = tb;
+    if (mode == 1 && !encode_f32_2d(&tg, G, N, V, 64, 128)) return cudaErrorInvalidValue;
+    if (mode > 1) tg = tb;
     p.nmb = (N + 127) / 128;
     p.nstage_k = (V + 63) / 64;
     // Shares of the vocabulary: the rounds of work items times the stages of one, against writing and
@@ -588,6 +600,7 @@ cudaError_t tensor(int N, int V, int r, int g_bf16, const void* G, const bf16* a
     splits = (p.nstage_k + p.per_split - 1) / p.per_split;
     p.items = base * splits;
     p.out = splits > 1 ? part : ga;
+    p.wide = ((uintptr_t)p.out % 32) == 0;
     if ((e = bg_mode<true>(mode, p, tg, tb, nsm, stream)) != cudaSuccess) return e;
     if (splits > 1) {
       const long long quads = (long long)N * r / 4;

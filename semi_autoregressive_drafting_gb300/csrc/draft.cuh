@@ -88,6 +88,9 @@ int draft_tc_supported(int B, int r, int w_bf16);
 // 2-D tensor map of a row-major bf16 matrix [rows][cols] (row stride ld elements) for TMA tile
 // loads of box_rows rows x 64 columns into the 128-byte-swizzled K-major layout.
 bool encode_bf16_2d(CUtensorMap* m, const void* base, int rows, int cols, int ld, int box_rows);
+// 2-D tensor map of a row-major fp32 matrix [rows][cols] (cols a multiple of 4) for TMA tile loads of
+// box_rows rows x box_cols columns, stored as they lie.
+bool encode_f32_2d(CUtensorMap* m, const void* base, int rows, int cols, int box_cols, int box_rows);
 // 3-D tensor map of U [B][G][V] bf16 for TMA loads of box_rows requests x one position x 64
 // vocabulary entries, 128-byte swizzle (V a multiple of 8).
 bool encode_u_bf16_3d(CUtensorMap* m, const void* U, int B, int G, int V, int box_rows);
