@@ -6,20 +6,22 @@
 //
 // bf16 weights: two tensor-core products (tcgen05, kind::f16, fp32 accumulation in TMEM), each with
 // G as the M-side operand and 256 columns of the other one:
-//   grad_W2: M = 128 vocabulary entries (G as it lies is M-major), K = N; one tile per work item;
-//   grad_a:  M = 128 rows, K = a share of the vocabulary (G as it lies is K-major); the shares'
+//   grad_W2: M = 256 vocabulary entries (G as it lies is M-major), K = N; one tile per work item;
+//   grad_a:  M = 256 rows, K = a share of the vocabulary (G as it lies is K-major); the shares'
 //            fp32 results are added in order by a second launch.
-// A block per SM walks over its work items: TMA threads, one thread that issues the MMAs, eight
-// warps that read the accumulators out of TMEM.  An fp32 G enters as two bf16 parts, G = hi + lo with
-// hi = bf16(G), lo = bf16(G - hi) (16 significant bits or more, an error of at most 2^-18 |G|,
-// below that of an fp32 sum of these lengths): TMA brings it as it lies, and eight warps split it
-// from one shared-memory buffer into another.  A G whose rows TMA cannot address is read by the same
-// warps, element by element.
+// A pair of CTAs (cta_group::2) takes a work item: each holds 128 of the rows and half the columns,
+// so that W2 or a reaches each SM's shared memory once per 256 rows of G.  One block per SM walks
+// over its pair's items: TMA threads, one thread of the pair that issues the MMAs, eight warps that
+// read the accumulators out of TMEM.
+// An fp32 G enters as three bf16 parts, hi = bf16(G), mid = bf16(G - hi), lo = bf16(G - hi - mid): all
+// 24 bits (two parts measured 2.5e-6 of the result off, an fp32 product 1e-6).  TMA brings it as it
+// lies, and eight warps split it from one shared-memory buffer into another.  A G whose rows TMA
+// cannot address is read by the same warps, element by element.
 //
 // The tensor cores add into fp32 accumulators with truncation: over a long K the sums shrink by about
-// 2e-8 of themselves per MMA (measured: 1.5e-5 after 784).  So a run of 16 MMAs goes to one half of
-// TMEM, and while the next run goes to the other half, the eight warps add the first to sums in their
-// registers (128 columns of a row per thread), rounded to nearest.
+// 2e-8 of themselves per MMA (measured: 1.5e-5 after 784).  So a run of 16 or 24 MMAs goes to one half
+// of TMEM, and while the next run goes to the other half, the eight warps add the first to sums in
+// their registers (128 columns of a row per thread), rounded to nearest.
 // fp32 weights (small heads): CUDA-core tiles.
 #include <cuda.h>
 
@@ -89,21 +91,20 @@ cudaError_t plain(int N, int V, int r, const TG* G, const TW* a, const TW* W2, i
 
 // ------------------------------------------------------------------ bf16 weights: tensor cores
 constexpr int kBox = 64 * 128;        // bytes of one shared-memory box: 64 rows of 64 bf16
-constexpr int kTileA = 2 * kBox;      // 128 (M) x 64 (K) of G
-constexpr int kBytesB = 4 * kBox;     // 64 (K) x 256 of W2 or a
-constexpr int kBN = 256;              // columns per work item
-constexpr int kMaxItems = 2;          // work items per SM at most when the vocabulary is shared out
-constexpr int kRun = 16;              // MMAs of K = 16 into one set of accumulators
+constexpr int kTileA = 2 * kBox;      // 128 (M) x 64 (K) of G: a CTA's half of a pair's tile
+constexpr int kTileB = 2 * kBox;      // 64 (K) x 128 of W2 or a: a CTA's half of the columns
+constexpr int kBM = 256;              // rows of a work item (a pair of CTAs)
+constexpr int kBN = 256;              // columns of a work item
+constexpr int kMaxItems = 2;          // work items per pair at most when the vocabulary is shared out
 constexpr int kRawBytes = 128 * 64 * 4;  // a stage of an fp32 G as it lies
-constexpr int kRaw = 2;               // such stages in flight
 // Registers per thread where eight more warps bring G (640 threads, launched with 96 each): the
-// three shares, 128 x (40 + 2 x 160 + 2 x 56), stay below the launch's 640 x 96.
-constexpr int kRegsIssue = 40, kRegsSums = 160, kRegsBring = 56;
+// three shares, 128 x (48 + 2 x 160 + 2 x 56), are the launch's 640 x 96.
+constexpr int kRegsIssue = 48, kRegsSums = 160, kRegsBring = 56;
 
 struct BgArgs {
   int N, V, r;
   int items, nrb;       // work items; blocks of 256 columns of r
-  int nmb;              // grad_a: blocks of 128 rows
+  int nmb;              // grad_a: blocks of 256 rows
   int per_split;        // grad_a: K stages per share of the vocabulary
   int nstage_k;         // K stages in all
   int b_kmajor;         // grad_a: W2 is [r][V]
@@ -116,14 +117,12 @@ struct BgArgs {
 };
 
 // A bounded wait of one thread that also ends when another role of the block gave up.
-// (limit: for the accumulators, whose K stages all come first)
-__device__ __forceinline__ bool wait_or(uint64_t* bar, uint32_t parity, volatile int* stop,
-                                        unsigned long long limit = kWaitLimitNs) {
-  if (mbar_try_wait(bar, parity)) return true;
+__device__ __forceinline__ bool wait_or(uint64_t* bar, uint32_t parity, volatile int* stop) {
+  if (tc::mbar_try_wait_cluster(bar, parity, 0)) return true;
   const unsigned long long t0 = globaltimer();
-  while (!mbar_try_wait_sleep(bar, parity, kSuspendHintNs)) {
+  while (!tc::mbar_try_wait_cluster(bar, parity, kSuspendHintNs)) {
     if (*stop) return false;
-    if (globaltimer() - t0 > limit) {
+    if (globaltimer() - t0 > kWaitLimitNs) {
       *stop = 1;
       return false;
     }
@@ -131,24 +130,27 @@ __device__ __forceinline__ bool wait_or(uint64_t* bar, uint32_t parity, volatile
   return true;
 }
 
-// One work item: the tile's first row, its first and last K stage, its columns.
+// One work item as a CTA of the pair sees it: its 128 rows, the K stages, the columns; the columns
+// that the MMA takes (a multiple of 16) and this CTA's half of them.
 struct Item {
-  int m0, k0, k1, c0, cols, split;
+  int m0, k0, k1, c0, cols, split, n, half0;
 };
 template <bool WANT_A>
-__device__ __forceinline__ Item item_of(const BgArgs& a, int i) {
+__device__ __forceinline__ Item item_of(const BgArgs& a, int i, int rank) {
   Item t;
   const int rb = i % a.nrb;
   i /= a.nrb;
   t.c0 = rb * kBN;
   t.cols = min(kBN, a.r - t.c0);
+  t.n = (t.cols + 15) / 16 * 16;
+  t.half0 = t.c0 + rank * (t.n / 2);
   if (WANT_A) {
-    t.m0 = (i % a.nmb) * 128;
+    t.m0 = (i % a.nmb) * kBM + rank * 128;
     t.split = i / a.nmb;
     t.k0 = t.split * a.per_split;
     t.k1 = min(a.nstage_k, t.k0 + a.per_split);
   } else {
-    t.m0 = i * 128;
+    t.m0 = i * kBM + rank * 128;
     t.split = 0;
     t.k0 = 0;
     t.k1 = a.nstage_k;
@@ -163,29 +165,34 @@ __device__ __forceinline__ float4 load_quad(const TG* p, int n) {
   return make_float4(to_f<TG>(p[0]), n > 1 ? to_f<TG>(p[1]) : 0.f, n > 2 ? to_f<TG>(p[2]) : 0.f,
                      n > 3 ? to_f<TG>(p[3]) : 0.f);
 }
-__device__ __forceinline__ uint2 pack_hi(const float4& f) {
+// bf16 of four values, and what it leaves of them (exactly)
+__device__ __forceinline__ uint2 take_bf16(float4& f) {
   const __nv_bfloat162 a = __floats2bfloat162_rn(f.x, f.y), b = __floats2bfloat162_rn(f.z, f.w);
   uint2 w;
   memcpy(&w.x, &a, 4);
   memcpy(&w.y, &b, 4);
+  f.x -= __uint_as_float(w.x << 16);
+  f.y -= __uint_as_float(w.x & 0xFFFF0000u);
+  f.z -= __uint_as_float(w.y << 16);
+  f.w -= __uint_as_float(w.y & 0xFFFF0000u);
   return w;
 }
-__device__ __forceinline__ uint2 pack_lo(const float4& f, const uint2& hi) {
-  return pack_hi(make_float4(f.x - __uint_as_float(hi.x << 16), f.y - __uint_as_float(hi.x & 0xFFFF0000u),
-                             f.z - __uint_as_float(hi.y << 16), f.w - __uint_as_float(hi.y & 0xFFFF0000u)));
-}
 
-// MODE 0: bf16 G by TMA.  1: fp32 G by TMA, split into two parts.  2: fp32 G element by element.
+// MODE 0: bf16 G by TMA.  1: fp32 G by TMA, split into three parts.  2: fp32 G element by element.
 // 3: bf16 G element by element (one part).
 template <int MODE>
 struct Src {
   static constexpr bool kTma = MODE == 0, kTmaRaw = MODE == 1;
-  static constexpr int kParts = MODE == 1 || MODE == 2 ? 2 : 1;
-  static constexpr int kStages = kParts == 2 ? 2 : 4;
-  static constexpr int kRawAll = kTmaRaw ? kRaw * kRawBytes : 0;
-  static constexpr int kStage = kParts * kTileA + kBytesB;
-  static constexpr int kRunStages = kRun / 4 / kParts;
+  static constexpr int kParts = MODE == 1 || MODE == 2 ? 3 : 1;
+  static constexpr int kStagesA = kParts == 3 ? 2 : 6;  // of G's parts
+  static constexpr int kStagesB = kParts == 3 ? 4 : 6;  // of W2 or a
+  static constexpr int kRaw = kTmaRaw ? 2 : 0;          // of an fp32 G as it lies
+  static constexpr int kStageA = kParts * kTileA;
+  static constexpr int kRunStages = kParts == 3 ? 2 : 4;  // 24 or 16 MMAs into one set of accumulators
   static constexpr int kThreads = kTma ? 384 : 640;
+  static constexpr int kOffB = kStagesA * kStageA, kOffRaw = kOffB + kStagesB * kTileB,
+                       kOffBar = kOffRaw + kRaw * kRawBytes;
+  static constexpr int kSmem = kOffBar + 256 + 1024;
   using T = typename std::conditional<MODE == 3, bf16, float>::type;
 };
 
@@ -223,32 +230,43 @@ __device__ __forceinline__ void write_out(const BgArgs& a, const Item& t, int ro
 }
 
 template <bool WANT_A, int MODE>
-__global__ void __launch_bounds__(Src<MODE>::kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads, 1)
     bias_grad_kernel(const BgArgs a, const __grid_constant__ CUtensorMap tmG,
                      const __grid_constant__ CUtensorMap tmB) {
   using S = Src<MODE>;
+  constexpr int kSA = S::kStagesA, kSB = S::kStagesB, kRaw = S::kRaw > 0 ? S::kRaw : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t* raw = smem + S::kStages * S::kStage;
-  uint64_t* full = (uint64_t*)(raw + S::kRawAll);
-  uint64_t* empty = full + S::kStages;
-  uint64_t* done = empty + S::kStages;  // [2]: a run's MMAs are complete
-  uint64_t* tfree = done + 2;           // [2]: its accumulators have been read
-  uint64_t* rfull = tfree + 2;          // [kRaw]
+  uint8_t* raw = smem + S::kOffRaw;
+  // Of the pair's two copies, rank 0's count: G's parts in place (afull), W2 or a in place (bfull),
+  // accumulators read (tfree).  Both ranks' own: MMAs have read a stage (aempty, bempty), a run's MMAs
+  // are complete (done), an fp32 G has arrived or been split (rfull, rempty).
+  uint64_t* afull = (uint64_t*)(smem + S::kOffBar);
+  uint64_t* aempty = afull + kSA;
+  uint64_t* bfull = aempty + kSA;
+  uint64_t* bempty = bfull + kSB;
+  uint64_t* done = bempty + kSB;
+  uint64_t* tfree = done + 2;
+  uint64_t* rfull = tfree + 2;
   uint64_t* rempty = rfull + kRaw;
   uint32_t* tbase = (uint32_t*)(rempty + kRaw);
   volatile int* stop = (volatile int*)(tbase + 1);
+  static_assert((2 * kSA + 2 * kSB + 4 + 2 * kRaw) * 8 + 8 <= 256, "barriers fit");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kOffB = S::kParts * kTileA;
+  const int rank = (int)cluster_rank(), pair = (int)blockIdx.x >> 1, pairs = (int)gridDim.x >> 1;
 
   if (tid == 0) {
-    for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(&full[i], 1 + (S::kTma ? 0 : 8));
-      mbar_init(&empty[i], 1);
+    for (int i = 0; i < kSA; ++i) {
+      mbar_init(&afull[i], S::kTma ? 1 : 16);
+      mbar_init(&aempty[i], 1);
+    }
+    for (int i = 0; i < kSB; ++i) {
+      mbar_init(&bfull[i], 1);
+      mbar_init(&bempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&done[i], 1);
-      mbar_init(&tfree[i], 8);
+      mbar_init(&tfree[i], 16);
     }
     for (int i = 0; i < kRaw; ++i) {
       mbar_init(&rfull[i], 1);
@@ -257,80 +275,86 @@ __global__ void __launch_bounds__(Src<MODE>::kThreads, 1)
     *stop = 0;
     fence_mbar_init();
   }
+  __syncthreads();
+  cluster_sync_all();  // both CTAs are there
   if (warp == 1) {
-    tc::tmem_alloc(tbase, 512);
-    tc::tmem_relinquish();
+    tc::tmem_alloc_pair(tbase, 512);
+    tc::tmem_relinquish_pair();
   }
   tc::fence_before_sync();
   __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers and TMEM are ready
   tc::fence_after_sync();
   const uint32_t tmem = *tbase;
 
   if (warp < 4) {
-  if (!S::kTma) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-  if (warp == 0) {
-    if (lane == 0) {  // ---- TMA
-      const uint64_t once = policy_evict_first(), keep = policy_evict_last();
+    if (!S::kTma) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == 0 && lane == 0) {  // ---- TMA: W2 or a
+      const uint64_t keep = policy_evict_last();
       int g = 0;
       bool ok = true;
-      for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
-        const Item t = item_of<WANT_A>(a, i);
-        const int nb = (t.cols + 63) / 64;
-        const uint32_t bytes = (uint32_t)(nb * kBox + (S::kTma ? kTileA : 0));
+      for (int i = pair; ok && i < a.items; i += pairs) {
+        const Item t = item_of<WANT_A>(a, i, rank);
+        const int nb = (t.n / 2 + 63) / 64;
         for (int s = t.k0; s < t.k1; ++s, ++g) {
-          const int slot = g % S::kStages;
-          if (g >= S::kStages && !wait_or(&empty[slot], (uint32_t)((g / S::kStages - 1) & 1), stop)) {
+          const int slot = g % kSB;
+          if (g >= kSB && !wait_or(&bempty[slot], (uint32_t)((g / kSB - 1) & 1), stop)) {
             ok = false;
             break;
           }
-          uint8_t* st = smem + slot * S::kStage;
-          mbar_expect_tx(&full[slot], bytes);
-          if (S::kTma) {
-            for (int b = 0; b < 2; ++b)
-              if (WANT_A)
-                tc::tma_load_2d(st + b * kBox, &tmG, s * 64, t.m0 + 64 * b, &full[slot], once);
-              else
-                tc::tma_load_2d(st + b * kBox, &tmG, t.m0 + 64 * b, s * 64, &full[slot], once);
-          }
+          if (rank == 0) mbar_expect_tx(&bfull[slot], (uint32_t)(2 * nb * kBox));  // both CTAs' boxes
+          const uint32_t bar = cluster_addr(&bfull[slot], 0);
+          uint8_t* st = smem + S::kOffB + slot * kTileB;
           for (int b = 0; b < nb; ++b)
             if (WANT_A && a.b_kmajor)
-              tc::tma_load_2d(st + kOffB + b * kBox, &tmB, s * 64, t.c0 + 64 * b, &full[slot], keep);
+              tc::tma_load_2d_pair(st + b * kBox, &tmB, s * 64, t.half0 + 64 * b, bar, keep);
             else
-              tc::tma_load_2d(st + kOffB + b * kBox, &tmB, t.c0 + 64 * b, s * 64, &full[slot], keep);
+              tc::tma_load_2d_pair(st + b * kBox, &tmB, t.half0 + 64 * b, s * 64, bar, keep);
         }
       }
       if (!ok) atomicMax(a.status, kErrTimeout);
-      // every copy lands before the block ends (the phase of each slot's last use)
-      for (int j = max(0, g - S::kStages); j < g; ++j) mbar_wait(&full[j % S::kStages], (uint32_t)((j / S::kStages) & 1));
-    }
-  } else if (S::kTmaRaw && warp == 2) {
-    if (lane == 0) {  // ---- TMA, an fp32 G as it lies
+      // every copy lands before the pair ends (the phase of each slot's last use)
+      if (rank == 0)
+        for (int j = max(0, g - kSB); j < g; ++j) mbar_wait(&bfull[j % kSB], (uint32_t)((j / kSB) & 1));
+    } else if ((S::kTma || S::kTmaRaw) && warp == 2 && lane == 0) {  // ---- TMA: G
       const uint64_t once = policy_evict_first();
+      constexpr int kS = S::kTma ? kSA : kRaw;
       int g = 0;
       bool ok = true;
-      for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
-        const Item t = item_of<WANT_A>(a, i);
+      for (int i = pair; ok && i < a.items; i += pairs) {
+        const Item t = item_of<WANT_A>(a, i, rank);
         for (int s = t.k0; s < t.k1; ++s, ++g) {
-          const int slot = g % kRaw;
-          if (g >= kRaw && !wait_or(&rempty[slot], (uint32_t)((g / kRaw - 1) & 1), stop)) {
+          const int slot = g % kS;
+          if (g >= kS && !wait_or(S::kTma ? &aempty[slot] : &rempty[slot], (uint32_t)((g / kS - 1) & 1), stop)) {
             ok = false;
             break;
           }
-          mbar_expect_tx(&rfull[slot], kRawBytes);
-          tc::tma_load_2d(raw + slot * kRawBytes, &tmG, WANT_A ? s * 64 : t.m0, WANT_A ? t.m0 : s * 64, &rfull[slot], once);
+          if (S::kTma) {
+            if (rank == 0) mbar_expect_tx(&afull[slot], 2 * kTileA);
+            const uint32_t bar = cluster_addr(&afull[slot], 0);
+            uint8_t* st = smem + slot * S::kStageA;
+            for (int b = 0; b < 2; ++b)
+              if (WANT_A)
+                tc::tma_load_2d_pair(st + b * kBox, &tmG, s * 64, t.m0 + 64 * b, bar, once);
+              else
+                tc::tma_load_2d_pair(st + b * kBox, &tmG, t.m0 + 64 * b, s * 64, bar, once);
+          } else {
+            mbar_expect_tx(&rfull[slot], kRawBytes);
+            tc::tma_load_2d(raw + slot * kRawBytes, &tmG, WANT_A ? s * 64 : t.m0, WANT_A ? t.m0 : s * 64,
+                            &rfull[slot], once);
+          }
         }
       }
       if (!ok) atomicMax(a.status, kErrTimeout);
-      for (int j = max(0, g - kRaw); j < g; ++j) mbar_wait(&rfull[j % kRaw], (uint32_t)((j / kRaw) & 1));
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {  // ---- MMA
+      if (!S::kTma || rank == 0)
+        for (int j = max(0, g - kS); j < g; ++j)
+          mbar_wait(S::kTma ? &afull[j % kS] : &rfull[j % kS], (uint32_t)((j / kS) & 1));
+    } else if (warp == 1 && lane == 0 && rank == 0) {  // ---- MMA, for both CTAs
       int g = 0, n = 0;  // stages and runs so far
       bool ok = true;
-      for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
-        const Item t = item_of<WANT_A>(a, i);
-        const uint32_t idesc = tc::idesc_bf16_f32(128, (t.cols + 15) / 16 * 16) |
-                               (WANT_A ? 0u : tc::kIdescAMajorMN) |
+      for (int i = pair; ok && i < a.items; i += pairs) {
+        const Item t = item_of<WANT_A>(a, i, 0);
+        const uint32_t idesc = tc::idesc_bf16_f32(kBM, t.n) | (WANT_A ? 0u : tc::kIdescAMajorMN) |
                                (WANT_A && a.b_kmajor ? 0u : tc::kIdescBMajorMN);
         for (int s0 = t.k0; ok && s0 < t.k1; s0 += S::kRunStages) {
           const int buf = n & 1;
@@ -338,16 +362,16 @@ __global__ void __launch_bounds__(Src<MODE>::kThreads, 1)
             ok = false;
             break;
           }
-          tc::fence_after_sync();
           const int s1 = min(t.k1, s0 + S::kRunStages);
           for (int s = s0; s < s1; ++s, ++g) {
-            const int slot = g % S::kStages;
-            if (!wait_or(&full[slot], (uint32_t)((g / S::kStages) & 1), stop)) {
+            const int sla = g % kSA, slb = g % kSB;
+            if (!wait_or(&bfull[slb], (uint32_t)((g / kSB) & 1), stop) ||
+                !wait_or(&afull[sla], (uint32_t)((g / kSA) & 1), stop)) {
               ok = false;
               break;
             }
             tc::fence_after_sync();
-            const uint32_t sa = smem_u32(smem + slot * S::kStage), sb = sa + kOffB;
+            const uint32_t sa = smem_u32(smem + sla * S::kStageA), sb = smem_u32(smem + S::kOffB + slb * kTileB);
             // K-major: 16 elements of K are 32 bytes along the rows; M- or N-major: 16 rows of 128 bytes
             const uint64_t bd = WANT_A && a.b_kmajor ? tc::sdesc_sw128(sb) : tc::sdesc_sw128_mn(sb, kBox);
             const uint64_t bstep = WANT_A && a.b_kmajor ? 2 : 128;
@@ -357,12 +381,14 @@ __global__ void __launch_bounds__(Src<MODE>::kThreads, 1)
               const uint64_t ad = WANT_A ? tc::sdesc_sw128(at) : tc::sdesc_sw128_mn(at, kBox);
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                tc::mma_bf16(tmem + buf * kBN, ad + (WANT_A ? 2 : 128) * kk, bd + bstep * kk, idesc, (s - s0) | h | kk);
+                tc::mma_bf16_pair(tmem + buf * kBN, ad + (WANT_A ? 2 : 128) * kk, bd + bstep * kk, idesc,
+                                  (s - s0) | h | kk);
             }
-            tc::mma_commit(&empty[slot]);
+            tc::mma_commit_pair(&aempty[sla]);
+            tc::mma_commit_pair(&bempty[slb]);
           }
           if (ok) {
-            tc::mma_commit(&done[buf]);
+            tc::mma_commit_pair(&done[buf]);
             ++n;
           }
         }
@@ -370,20 +396,19 @@ __global__ void __launch_bounds__(Src<MODE>::kThreads, 1)
       if (!ok) {
         atomicMax(a.status, kErrTimeout);
         // what was issued completes before TMEM is freed
-        tc::mma_commit(&done[n & 1]);
+        tc::mma_commit_pair(&done[n & 1]);
         mbar_wait(&done[n & 1], (uint32_t)((n / 2) & 1));
       }
     }
     __syncwarp();
-  }
   } else if (warp < 12) {  // ---- accumulators to the sums, sums to global memory
     if (!S::kTma) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSums));
     const int q = warp & 3, c_lo = warp < 8 ? 0 : kBN / 2;
     const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + c_lo;
     int n = 0;
     bool ok = true;
-    for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
-      const Item t = item_of<WANT_A>(a, i);
+    for (int i = pair; ok && i < a.items; i += pairs) {
+      const Item t = item_of<WANT_A>(a, i, rank);
       float x[kBN / 2];
 #pragma unroll
       for (int j = 0; j < kBN / 2; ++j) x[j] = 0.f;
@@ -406,13 +431,13 @@ __global__ void __launch_bounds__(Src<MODE>::kThreads, 1)
           }
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&tfree[buf]);
+        if (lane == 0) tc::mbar_arrive_cluster(cluster_addr(&tfree[buf], 0));
       }
       const int row = t.m0 + 32 * q + lane;
       if (ok && row < (WANT_A ? a.N : a.V)) write_out<WANT_A>(a, t, row, c_lo, x);
       __syncwarp();
     }
-  } else if (!S::kTma) {  // ---- G from global memory, split into its parts
+  } else if (!S::kTma) {  // ---- G into its parts
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsBring));
     using TG = typename S::T;
     const TG* G = (const TG*)a.G;
@@ -423,10 +448,10 @@ __global__ void __launch_bounds__(Src<MODE>::kThreads, 1)
     constexpr int kRowStep = WANT_A ? 16 : 8;
     int g = 0;
     bool ok = true;
-    for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
-      const Item t = item_of<WANT_A>(a, i);
+    for (int i = pair; ok && i < a.items; i += pairs) {
+      const Item t = item_of<WANT_A>(a, i, rank);
       for (int s = t.k0; s < t.k1; ++s, ++g) {
-        const int slot = g % S::kStages;
+        const int slot = g % kSA;
         float4 r[8];
         if (S::kTmaRaw) {
           if (lane == 0) ok = wait_or(&rfull[g % kRaw], (uint32_t)((g / kRaw) & 1), stop);
@@ -439,7 +464,7 @@ __global__ void __launch_bounds__(Src<MODE>::kThreads, 1)
             r[u] = load_quad<TG>(G + (long long)row * a.V + col, row < a.N ? n : 0);
           }
         }
-        if (ok && g >= S::kStages && lane == 0) ok = wait_or(&empty[slot], (uint32_t)((g / S::kStages - 1) & 1), stop);
+        if (ok && g >= kSA && lane == 0) ok = wait_or(&aempty[slot], (uint32_t)((g / kSA - 1) & 1), stop);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) {
           if (lane == 0) atomicMax(a.status, kErrTimeout);
@@ -450,30 +475,32 @@ __global__ void __launch_bounds__(Src<MODE>::kThreads, 1)
 #pragma unroll
           for (int u = 0; u < 8; ++u) r[u] = in[u * 256];
         }
-        uint8_t* st = smem + slot * S::kStage;
+        uint8_t* st = smem + slot * S::kStageA;
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           const int row = prow + u * kRowStep;
           const int box = WANT_A ? row >> 6 : pq >> 4, y = row & 63, x = pq & 15;
           const uint32_t at = (uint32_t)(box * kBox + y * 128 + (((x >> 1) ^ (y & 7)) << 4) + (x & 1) * 8);
-          const uint2 hi = pack_hi(r[u]);
-          *(uint2*)(st + at) = hi;
-          if (S::kParts == 2) *(uint2*)(st + kTileA + at) = pack_lo(r[u], hi);
+#pragma unroll
+          for (int h = 0; h < S::kParts; ++h) *(uint2*)(st + h * kTileA + at) = take_bf16(r[u]);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
           if (S::kTmaRaw) mbar_arrive(&rempty[g % kRaw]);
-          mbar_arrive(&full[slot]);
+          tc::mbar_arrive_cluster(cluster_addr(&afull[slot], 0));
         }
       }
     }
   }
+  tc::fence_before_sync();
   __syncthreads();
+  cluster_sync_all();  // the other CTA no longer reads this one's shared memory or arrives here
   if (warp == 1) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 512);
+    tc::tmem_dealloc_pair(tmem, 512);
   }
+  cluster_sync_all();  // neither CTA ends before both have freed
 }
 
 // grad_a from the shares, in their order: four threads per 16 bytes, each a contiguous quarter.
@@ -512,21 +539,21 @@ __global__ void __launch_bounds__(256) share_sum_kernel(long long quads, int spl
 
 size_t bg_align(size_t x) { return (x + 255) / 256 * 256; }
 
-// floats of shared-out results at most: kMaxItems work items of 128 x 256 per SM, and no more shares
-// than that many work items
+// floats of shared-out results at most: kMaxItems work items of 256 x 256 per pair of SMs, and no more
+// shares than that many work items
 size_t share_floats(int N, int r, int nsm) {
-  const size_t cap = (size_t)kMaxItems * nsm, all = cap * N * r, tiles = cap * 128 * kBN;
+  const size_t cap = (size_t)kMaxItems * (nsm / 2), all = cap * N * r, tiles = cap * kBM * kBN;
   return all < tiles ? all : tiles;
 }
 
 template <bool WANT_A, int MODE>
 cudaError_t bg_launch(const BgArgs& a, const CUtensorMap& tg, const CUtensorMap& tb, int nsm, cudaStream_t stream) {
   using S = Src<MODE>;
-  const size_t smem = (size_t)S::kStages * S::kStage + S::kRawAll + 1024 + 256;
   cudaError_t e = cudaFuncSetAttribute(bias_grad_kernel<WANT_A, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+                                       S::kSmem);
   if (e != cudaSuccess) return e;
-  bias_grad_kernel<WANT_A, MODE><<<a.items < nsm ? a.items : nsm, S::kThreads, smem, stream>>>(a, tg, tb);
+  const int pairs = a.items < nsm / 2 ? a.items : nsm / 2;
+  bias_grad_kernel<WANT_A, MODE><<<2 * pairs, S::kThreads, S::kSmem, stream>>>(a, tg, tb);
   return cudaGetLastError();
 }
 template <bool WANT_A>
@@ -561,7 +588,7 @@ cudaError_t tensor(int N, int V, int r, int g_bf16, const void* G, const bf16* a
     if (!encode_bf16_2d(&tb, a, N, r, r, 64)) return cudaErrorInvalidValue;
     if (mode == 1 && !encode_f32_2d(&tg, G, N, V, 128, 64)) return cudaErrorInvalidValue;
     if (mode > 1) tg = tb;  // (not used)
-    p.items = (V + 127) / 128 * p.nrb;
+    p.items = (V + kBM - 1) / kBM * p.nrb;
     p.nstage_k = (N + 63) / 64;
     p.out = gW;
     p.wide = ((uintptr_t)gW % 32) == 0;
@@ -580,17 +607,17 @@ cudaError_t tensor(int N, int V, int r, int g_bf16, const void* G, const bf16* a
       return cudaErrorInvalidValue;
     if (mode == 1 && !encode_f32_2d(&tg, G, N, V, 64, 128)) return cudaErrorInvalidValue;
     if (mode > 1) tg = tb;
-    p.nmb = (N + 127) / 128;
+    p.nmb = (N + kBM - 1) / kBM;
     p.nstage_k = (V + 63) / 64;
     // Shares of the vocabulary: the rounds of work items times the stages of one, against writing and
     // reading the shares' results (microseconds: a stage of 128 x 64 at the memory's rate per SM)
-    const int base = p.nmb * p.nrb;
+    const int base = p.nmb * p.nrb, pairs = nsm / 2;
     const double stage = (g_bf16 ? 0.38 : 0.75), io = (double)N * r * 8 / 6.7e6;
     int splits = 1;
     double best = 1e300;
-    for (int s = 1; s <= p.nstage_k && (long long)base * s <= (long long)kMaxItems * nsm; ++s) {
+    for (int s = 1; s <= p.nstage_k && (long long)base * s <= (long long)kMaxItems * pairs; ++s) {
       const int per = (p.nstage_k + s - 1) / s;
-      const double t = (double)((base * s + nsm - 1) / nsm) * per * stage + (s > 1 ? s * io + 2.0 : 0.0);
+      const double t = (double)((base * s + pairs - 1) / pairs) * per * stage + (s > 1 ? s * io + 2.0 : 0.0);
       if (t < best) {
         best = t;
         splits = s;
