@@ -19,7 +19,7 @@
 // cannot address is read by the same warps, element by element.
 //
 // The tensor cores add into fp32 accumulators with truncation: over a long K the sums shrink by about
-// 2e-8 of themselves per MMA (measured: 1.5e-5 after 784).  So a run of 16 or 24 MMAs goes to one half
+// 2e-8 of themselves per MMA (measured: 1.5e-5 after 784).  So a run of 24 or 32 MMAs goes to one half
 // of TMEM, and while the next run goes to the other half, the eight warps add the first to sums in
 // their registers (128 columns of a row per thread), rounded to nearest.
 // fp32 weights (small heads): CUDA-core tiles.
@@ -96,7 +96,7 @@ constexpr int kTileB = 2 * kBox;      // 64 (K) x 128 of W2 or a: a CTA's half o
 constexpr int kBM = 256;              // rows of a work item (a pair of CTAs)
 constexpr int kBN = 256;              // columns of a work item
 constexpr int kMaxItems = 2;          // work items per pair at most when the vocabulary is shared out
-constexpr int kRawBytes = 128 * 64 * 4;  // a stage of an fp32 G as it lies
+constexpr int kRawBytes = 128 * 32 * 4;  // half a stage of an fp32 G as it lies
 // Registers per thread where eight more warps bring G (640 threads, launched with 96 each): the
 // three shares, 128 x (48 + 2 x 160 + 2 x 56), are the launch's 640 x 96.
 constexpr int kRegsIssue = 48, kRegsSums = 160, kRegsBring = 56;
@@ -118,9 +118,9 @@ struct BgArgs {
 
 // A bounded wait of one thread that also ends when another role of the block gave up.
 __device__ __forceinline__ bool wait_or(uint64_t* bar, uint32_t parity, volatile int* stop) {
-  if (tc::mbar_try_wait_cluster(bar, parity, 0)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = globaltimer();
-  while (!tc::mbar_try_wait_cluster(bar, parity, kSuspendHintNs)) {
+  while (!mbar_try_wait_sleep(bar, parity, kSuspendHintNs)) {
     if (*stop) return false;
     if (globaltimer() - t0 > kWaitLimitNs) {
       *stop = 1;
@@ -186,13 +186,17 @@ struct Src {
   static constexpr int kParts = MODE == 1 || MODE == 2 ? 3 : 1;
   static constexpr int kStagesA = kParts == 3 ? 2 : 6;  // of G's parts
   static constexpr int kStagesB = kParts == 3 ? 4 : 6;  // of W2 or a
-  static constexpr int kRaw = kTmaRaw ? 2 : 0;          // of an fp32 G as it lies
+  // Where warps bring G, a stage is filled, multiplied and freed in halves of 32 of its K: twice the
+  // steps in flight in the same memory (the chain of fill, MMAs and signals bounds this path).
+  static constexpr int kHalves = kTma ? 1 : 2;
+  static constexpr int kSlotsA = kStagesA * kHalves;
+  static constexpr int kRaw = kTmaRaw ? 4 : 0;          // half stages of an fp32 G as it lies
   static constexpr int kStageA = kParts * kTileA;
-  static constexpr int kRunStages = kParts == 3 ? 2 : 4;  // 24 or 16 MMAs into one set of accumulators
+  static constexpr int kRunStages = kParts == 3 ? 2 : 8;  // 24 or 32 MMAs into one set of accumulators
   static constexpr int kThreads = kTma ? 384 : 640;
   static constexpr int kOffB = kStagesA * kStageA, kOffRaw = kOffB + kStagesB * kTileB,
                        kOffBar = kOffRaw + kRaw * kRawBytes;
-  static constexpr int kSmem = kOffBar + 256 + 1024;
+  static constexpr int kSmem = kOffBar + 512 + 1024;
   using T = typename std::conditional<MODE == 3, bf16, float>::type;
 };
 
@@ -234,7 +238,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
     bias_grad_kernel(const BgArgs a, const __grid_constant__ CUtensorMap tmG,
                      const __grid_constant__ CUtensorMap tmB) {
   using S = Src<MODE>;
-  constexpr int kSA = S::kStagesA, kSB = S::kStagesB, kRaw = S::kRaw > 0 ? S::kRaw : 1;
+  constexpr int kSA = S::kSlotsA, kSB = S::kStagesB, kRaw = S::kRaw > 0 ? S::kRaw : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* raw = smem + S::kOffRaw;
@@ -251,13 +255,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
   uint64_t* rempty = rfull + kRaw;
   uint32_t* tbase = (uint32_t*)(rempty + kRaw);
   volatile int* stop = (volatile int*)(tbase + 1);
-  static_assert((2 * kSA + 2 * kSB + 4 + 2 * kRaw) * 8 + 8 <= 256, "barriers fit");
+  static_assert((2 * kSA + 2 * kSB + 4 + 2 * kRaw) * 8 + 8 <= 512, "barriers fit");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)cluster_rank(), pair = (int)blockIdx.x >> 1, pairs = (int)gridDim.x >> 1;
 
   if (tid == 0) {
     for (int i = 0; i < kSA; ++i) {
-      mbar_init(&afull[i], S::kTma ? 1 : 16);
+      mbar_init(&afull[i], S::kTma ? 1 : 8);
       mbar_init(&aempty[i], 1);
     }
     for (int i = 0; i < kSB; ++i) {
@@ -270,7 +274,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
     }
     for (int i = 0; i < kRaw; ++i) {
       mbar_init(&rfull[i], 1);
-      mbar_init(&rempty[i], 8);
+      mbar_init(&rempty[i], 4);
     }
     *stop = 0;
     fence_mbar_init();
@@ -323,7 +327,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
       bool ok = true;
       for (int i = pair; ok && i < a.items; i += pairs) {
         const Item t = item_of<WANT_A>(a, i, rank);
-        for (int s = t.k0; s < t.k1; ++s, ++g) {
+        for (int s = t.k0 * S::kHalves; s < t.k1 * S::kHalves; ++s, ++g) {
           const int slot = g % kS;
           if (g >= kS && !wait_or(S::kTma ? &aempty[slot] : &rempty[slot], (uint32_t)((g / kS - 1) & 1), stop)) {
             ok = false;
@@ -340,7 +344,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
                 tc::tma_load_2d_pair(st + b * kBox, &tmG, t.m0 + 64 * b, s * 64, bar, once);
           } else {
             mbar_expect_tx(&rfull[slot], kRawBytes);
-            tc::tma_load_2d(raw + slot * kRawBytes, &tmG, WANT_A ? s * 64 : t.m0, WANT_A ? t.m0 : s * 64,
+            tc::tma_load_2d(raw + slot * kRawBytes, &tmG, WANT_A ? s * 32 : t.m0, WANT_A ? t.m0 : s * 32,
                             &rfull[slot], once);
           }
         }
@@ -364,27 +368,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
           }
           const int s1 = min(t.k1, s0 + S::kRunStages);
           for (int s = s0; s < s1; ++s, ++g) {
-            const int sla = g % kSA, slb = g % kSB;
-            if (!wait_or(&bfull[slb], (uint32_t)((g / kSB) & 1), stop) ||
-                !wait_or(&afull[sla], (uint32_t)((g / kSA) & 1), stop)) {
+            const int slb = g % kSB;
+            if (!wait_or(&bfull[slb], (uint32_t)((g / kSB) & 1), stop)) {
               ok = false;
               break;
             }
-            tc::fence_after_sync();
-            const uint32_t sa = smem_u32(smem + sla * S::kStageA), sb = smem_u32(smem + S::kOffB + slb * kTileB);
+            const uint32_t sa = smem_u32(smem + (g % S::kStagesA) * S::kStageA);
+            const uint32_t sb = smem_u32(smem + S::kOffB + slb * kTileB);
             // K-major: 16 elements of K are 32 bytes along the rows; M- or N-major: 16 rows of 128 bytes
             const uint64_t bd = WANT_A && a.b_kmajor ? tc::sdesc_sw128(sb) : tc::sdesc_sw128_mn(sb, kBox);
             const uint64_t bstep = WANT_A && a.b_kmajor ? 2 : 128;
 #pragma unroll
-            for (int h = 0; h < S::kParts; ++h) {
-              const uint32_t at = sa + (uint32_t)h * kTileA;
-              const uint64_t ad = WANT_A ? tc::sdesc_sw128(at) : tc::sdesc_sw128_mn(at, kBox);
+            for (int half = 0; half < S::kHalves; ++half) {
+              const int ga = g * S::kHalves + half, sla = ga % kSA;
+              if (!wait_or(&afull[sla], (uint32_t)((ga / kSA) & 1), stop)) {
+                ok = false;
+                break;
+              }
+              tc::fence_after_sync();
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                tc::mma_bf16_pair(tmem + buf * kBN, ad + (WANT_A ? 2 : 128) * kk, bd + bstep * kk, idesc,
-                                  (s - s0) | h | kk);
+              for (int h = 0; h < S::kParts; ++h) {
+                const uint32_t at = sa + (uint32_t)h * kTileA;
+                const uint64_t ad = WANT_A ? tc::sdesc_sw128(at) : tc::sdesc_sw128_mn(at, kBox);
+#pragma unroll
+                for (int j = 0; j < 4 / S::kHalves; ++j) {
+                  const int kk = half * (4 / S::kHalves) + j;
+                  tc::mma_bf16_pair(tmem + buf * kBN, ad + (WANT_A ? 2 : 128) * kk, bd + bstep * kk, idesc,
+                                    (s - s0) | half | h | j);
+                }
+              }
+              tc::mma_commit_pair(&aempty[sla]);
             }
-            tc::mma_commit_pair(&aempty[sla]);
+            if (!ok) break;
             tc::mma_commit_pair(&bempty[slb]);
           }
           if (ok) {
@@ -431,7 +446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
           }
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive_cluster(cluster_addr(&tfree[buf], 0));
+        if (lane == 0) tc::mbar_arrive_cluster_relaxed(cluster_addr(&tfree[buf], 0));
       }
       const int row = t.m0 + 32 * q + lane;
       if (ok && row < (WANT_A ? a.N : a.V)) write_out<WANT_A>(a, t, row, c_lo, x);
@@ -441,45 +456,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsBring));
     using TG = typename S::T;
     const TG* G = (const TG*)a.G;
-    const int pt = tid - 384;
-    // a thread's eight quads of a stage: grad_a: row (16 u + pt / 16) of 128, quad pt % 16 of the 64
-    // entries; grad_W2: row (8 u + pt / 32) of 64, quad pt % 32 of the 128 entries
-    const int prow = WANT_A ? pt >> 4 : pt >> 5, pq = WANT_A ? pt & 15 : pt & 31;
-    constexpr int kRowStep = WANT_A ? 16 : 8;
-    int g = 0;
+    // Two groups of four warps take alternate half stages, so that one group's waits and fences pass
+    // beside the other's work.  A thread's eight quads of a half: grad_a: 128 rows of 8 quads (the rows
+    // of a warp are four apart in pairs: their swizzled stores meet all banks); grad_W2: 32 rows of 32.
+    const int half = (warp - 12) >> 2, pt = (tid - 384) & 127, j8 = pt >> 3;
+    const int prow = WANT_A ? (j8 & 1) * 4 + ((j8 >> 1) & 3) + (j8 & 8) : pt >> 5, pq = WANT_A ? pt & 7 : pt & 31;
+    constexpr int kRowStep = WANT_A ? 16 : 4, kRowQuads = WANT_A ? 8 : 32;
+    int g = 0;  // stages so far
     bool ok = true;
     for (int i = pair; ok && i < a.items; i += pairs) {
       const Item t = item_of<WANT_A>(a, i, rank);
       for (int s = t.k0; s < t.k1; ++s, ++g) {
-        const int slot = g % kSA;
+        const int ga = 2 * g + half, slot = ga % kSA;
+        if (lane == 0) {
+          if (S::kTmaRaw) ok = wait_or(&rfull[ga % kRaw], (uint32_t)((ga / kRaw) & 1), stop);
+          if (ok && ga >= kSA) ok = wait_or(&aempty[slot], (uint32_t)((ga / kSA - 1) & 1), stop);
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) {
+          if (lane == 0) atomicMax(a.status, kErrTimeout);
+          break;
+        }
         float4 r[8];
         if (S::kTmaRaw) {
-          if (lane == 0) ok = wait_or(&rfull[g % kRaw], (uint32_t)((g / kRaw) & 1), stop);
+          const float4* in = (const float4*)(raw + (ga % kRaw) * kRawBytes) + prow * kRowQuads + pq;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) r[u] = in[u * kRowStep * kRowQuads];
         } else {
-          const int row0 = (WANT_A ? t.m0 : s * 64) + prow;
-          const int col = (WANT_A ? s * 64 : t.m0) + 4 * pq, n = a.V - col;
+          const int row0 = (WANT_A ? t.m0 : s * 64 + 32 * half) + prow;
+          const int col = (WANT_A ? s * 64 + 32 * half : t.m0) + 4 * pq, n = a.V - col;
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
             const int row = row0 + u * kRowStep;
             r[u] = load_quad<TG>(G + (long long)row * a.V + col, row < a.N ? n : 0);
           }
         }
-        if (ok && g >= kSA && lane == 0) ok = wait_or(&aempty[slot], (uint32_t)((g / kSA - 1) & 1), stop);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) {
-          if (lane == 0) atomicMax(a.status, kErrTimeout);
-          break;
-        }
-        if (S::kTmaRaw) {
-          const float4* in = (const float4*)(raw + (g % kRaw) * kRawBytes) + pt;
-#pragma unroll
-          for (int u = 0; u < 8; ++u) r[u] = in[u * 256];
-        }
-        uint8_t* st = smem + slot * S::kStageA;
+        uint8_t* st = smem + (g % S::kStagesA) * S::kStageA;
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-          const int row = prow + u * kRowStep;
-          const int box = WANT_A ? row >> 6 : pq >> 4, y = row & 63, x = pq & 15;
+          const int row = prow + u * kRowStep + (WANT_A ? 0 : 32 * half);
+          const int box = WANT_A ? row >> 6 : pq >> 4, y = row & 63, x = WANT_A ? pq + 8 * half : pq & 15;
           const uint32_t at = (uint32_t)(box * kBox + y * 128 + (((x >> 1) ^ (y & 7)) << 4) + (x & 1) * 8);
 #pragma unroll
           for (int h = 0; h < S::kParts; ++h) *(uint2*)(st + h * kTileA + at) = take_bf16(r[u]);
@@ -487,7 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (S::kTmaRaw) mbar_arrive(&rempty[g % kRaw]);
+          if (S::kTmaRaw) mbar_arrive(&rempty[ga % kRaw]);
           tc::mbar_arrive_cluster(cluster_addr(&afull[slot], 0));
         }
       }
@@ -586,7 +602,7 @@ cudaError_t tensor(int N, int V, int r, int g_bf16, const void* G, const bf16* a
   cudaError_t e = cudaSuccess;
   if (gW) {
     if (!encode_bf16_2d(&tb, a, N, r, r, 64)) return cudaErrorInvalidValue;
-    if (mode == 1 && !encode_f32_2d(&tg, G, N, V, 128, 64)) return cudaErrorInvalidValue;
+    if (mode == 1 && !encode_f32_2d(&tg, G, N, V, 128, 32)) return cudaErrorInvalidValue;
     if (mode > 1) tg = tb;  // (not used)
     p.items = (V + kBM - 1) / kBM * p.nrb;
     p.nstage_k = (N + 63) / 64;
@@ -605,7 +621,7 @@ cudaError_t tensor(int N, int V, int r, int g_bf16, const void* G, const bf16* a
     }
     if (!(p.b_kmajor ? encode_bf16_2d(&tb, W, r, V, V, 64) : encode_bf16_2d(&tb, W, V, r, r, 64)))
       return cudaErrorInvalidValue;
-    if (mode == 1 && !encode_f32_2d(&tg, G, N, V, 64, 128)) return cudaErrorInvalidValue;
+    if (mode == 1 && !encode_f32_2d(&tg, G, N, V, 32, 128)) return cudaErrorInvalidValue;
     if (mode > 1) tg = tb;
     p.nmb = (N + kBM - 1) / kBM;
     p.nstage_k = (V + 63) / 64;
