@@ -10,14 +10,17 @@
 // The maximum is subtracted before the scale is applied: a row whose entries are all the type's
 // lowest number is a uniform row, not an overflow.
 //
-// Forward, one launch and one read of the logits: a block takes a 16-byte-aligned chunk of one row,
-// every thread holds its part of it in registers (all loads issued at once), and each warp forms
-// the maximum, then the sums relative to it.  The last block of a row to finish (a counter per row,
-// no waits) merges the chunks' partial results in their order and writes the row's outputs.
-// Alternatives: each warp also leaves the largest entry of its segment.  Any of the K largest
-// entries lies in one of the K segments that lead when ordered by (maximum, position): the K
-// leaders each hold an entry that precedes it otherwise.  So the last block ranks the segments and
-// re-reads K of them, 4 KB each and still in L2, instead of keeping lists during the pass.
+// Forward, one read of the logits: a warp takes a 16-byte-aligned segment of a row (4 KB; 1 KB in
+// small calls), holds it in registers (all loads issued at once), forms the maximum, then the sums
+// relative to it, and leaves them as one partial result.  A block per row merges the row's partial
+// results in their order: in large calls a second launch, so that a segment's warp ends with its
+// store; in small ones the row's last block to finish (a counter per row, no waits).
+// Alternatives: any of the K largest entries lies in one of the K segments that lead when ordered by
+// (maximum, position), since otherwise each of the K leaders holds an entry that precedes it.  So
+// that block ranks the segments and re-reads K of them, mostly from L2, and no lists are kept during
+// the pass.
+#include <cstddef>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -30,6 +33,8 @@ constexpr float kPL2e = 1.4426950408889634f;
 constexpr float kPLn2 = 0.6931471805599453f;
 constexpr int kPGroups = 256;   // segment groups ranked at most (one per thread)
 constexpr int kPKeep = 256;     // candidates kept before a cut to the K best
+constexpr int kPBuf = kPKeep + kPThr * 8;
+static_assert(kPBuf % kPThr == 0 && kPBuf / kPThr * 32 <= 2 * kPThr, "what a first cut leaves: two per thread");
 
 __device__ __forceinline__ float ex2p(float x) {
   float y;
@@ -185,8 +190,7 @@ __device__ __forceinline__ Part part_shfl(const Part& p, int o) {
 struct LpWs {
   WsHeader* hdr;
   unsigned* count;  // [N] blocks of the row done; zero between calls
-  Part* part;       // [N][nchunk]
-  float* seg;       // [N][nchunk][8] largest entry of each warp's segment (with alternatives)
+  float4* part;     // [N][nchunk][8] each segment's Part
 };
 
 struct LpArgs {
@@ -204,53 +208,94 @@ struct LpArgs {
 };
 
 // Shared memory of the alternatives' search.
-struct TopSm {
+struct alignas(16) TopSm {  // (gkey is read in 16-byte pieces)
   uint32_t gkey[kPGroups];                 // largest entry of each segment group, orderable
   int list[32];                            // the leading groups, best first
-  unsigned long long buf[kPKeep + kPThr * 8];
+  unsigned long long buf[kPBuf];
+  unsigned long long most[kPThr];          // each thread's largest candidate
   unsigned long long cut;                  // candidates below this are out
-  int n;
+  int n;                                   // candidates (all that passed: over kPBuf, not all are kept)
 };
 
-// Keeps the K largest of the n candidates, sorted, and raises the cut to the K-th.
+// Keeps the K largest of the candidates, sorted, and raises the cut to the K-th.  The candidates
+// differ, so their ranks do.  More than one per thread are first cut down: any of the K largest is no
+// less than the K-th largest of the threads' own maxima.
 __device__ __forceinline__ void top_prune(TopSm& t, int K) {
-  const int n = t.n;
-  constexpr int kPer = (kPKeep + kPThr * 8 + kPThr - 1) / kPThr;
-  unsigned long long k[kPer];
-  int r[kPer];
+  const int tid = (int)threadIdx.x;
+  int n = t.n;
+  if (n > kPThr) {
+    constexpr int kPer = kPBuf / kPThr;
+    unsigned long long k[kPer], m = 0ull;
 #pragma unroll
-  for (int u = 0; u < kPer; ++u) {
-    const int i = (int)threadIdx.x + u * kPThr;
+    for (int u = 0; u < kPer; ++u) {
+      const int i = tid + u * kPThr;
+      k[u] = i < n ? t.buf[i] : 0ull;
+      m = k[u] > m ? k[u] : m;
+    }
+    t.most[tid] = m;
+    __syncthreads();
+    if (tid == 0) t.n = 0;
+    int r = 0;
+    for (int j = 0; j < kPThr; ++j) r += t.most[j] > m ? 1 : 0;
+    if (r == K - 1) t.cut = m;
+    __syncthreads();
+    const unsigned long long cut = t.cut;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u)
+      if (k[u] >= cut) t.buf[atomicAdd(&t.n, 1)] = k[u];  // at most kPer K of them
+    __syncthreads();
+    n = t.n;
+  }
+  unsigned long long k[2];
+  int r[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int i = tid + u * kPThr;
     k[u] = i < n ? t.buf[i] : 0ull;
     r[u] = i < n ? 0 : K;
     if (u * kPThr < n)
-      for (int j = 0; j < n; ++j) r[u] += t.buf[j] > k[u] ? 1 : 0;  // (keys differ: ranks do too)
+      for (int j = 0; j < n; ++j) r[u] += t.buf[j] > k[u] ? 1 : 0;
   }
   __syncthreads();
 #pragma unroll
-  for (int u = 0; u < kPer; ++u)
+  for (int u = 0; u < 2; ++u)
     if (r[u] < K) {
       t.buf[r[u]] = k[u];
       if (r[u] == K - 1) t.cut = k[u];
     }
-  if (threadIdx.x == 0) t.n = min(n, K);
+  if (tid == 0) t.n = min(n, K);
   __syncthreads();
 }
 
-// The K alternatives of a row, by the whole block (the row's last one).
-template <typename T, int PER>
-__device__ __forceinline__ void top_search(TopSm& t, const LpArgs& a, const T* z, int head, long long row,
-                                           float m, float ls) {
+// The candidates among 16 bytes of a row whose first entry is v0.
+template <typename T>
+__device__ __forceinline__ void top_filter(TopSm& t, const uint4& q, int v0, unsigned long long cut) {
+#pragma unroll
+  for (int e = 0; e < Lg<T>::E / 2; ++e) {
+    const float2 f = un2(Lg<T>::pair(q, e));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float x = (h ? f.y : f.x) + 0.f;
+      if (x > -INFINITY) {
+        const unsigned long long k = make_key(x, (uint32_t)(v0 + 2 * e + h));
+        if (k >= cut) {
+          const int at = atomicAdd(&t.n, 1);
+          if (at < kPBuf) t.buf[at] = k;
+        }
+      }
+    }
+  }
+}
+
+// The K largest entries of a row, sorted, into t.buf (t.n of them), by a whole block.  mx: the largest
+// entry of the thread's group of g segments, -inf past the ng groups.  `beside` is run by the last
+// warp while the others read.
+template <typename T, int PER, typename F>
+__device__ __forceinline__ void top_search(TopSm& t, const LpArgs& a, const T* z, int head, float mx, int g, int ng,
+                                           F beside) {
   constexpr int E = Lg<T>::E;
   constexpr int kSeg = 32 * PER;  // 16-byte groups per segment
-  const int K = a.top, tid = (int)threadIdx.x;
-  const int nseg = a.nchunk * kPWarps;
-  const int g = (nseg + kPGroups - 1) / kPGroups;  // segments per group
-  const int ng = (nseg + g - 1) / g;
-  const float* seg = a.ws.seg + row * nseg;
-  float mx = -INFINITY;
-  if (tid < ng)
-    for (int i = tid * g; i < min(nseg, tid * g + g); ++i) mx = fmaxf(mx, __ldcg(seg + i));
+  const int K = a.top, tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t key = orderable(mx + 0.f);
   t.gkey[tid] = tid < ng ? key : 0u;
   if (tid < 32) t.list[tid] = -1;
@@ -262,7 +307,11 @@ __device__ __forceinline__ void top_search(TopSm& t, const LpArgs& a, const T* z
   // rank among the groups: larger maximum first, then the lower position
   if (tid < ng && mx != -INFINITY) {
     int r = 0;
-    for (int j = 0; j < ng; ++j) r += t.gkey[j] > key - (j < tid ? 1u : 0u) ? 1 : 0;
+    for (int j = 0; j < ng; j += 4) {
+      const uint4 o = *(const uint4*)(t.gkey + j);
+      r += (o.x > key - (j < tid ? 1u : 0u)) + (o.y > key - (j + 1 < tid ? 1u : 0u)) +
+           (o.z > key - (j + 2 < tid ? 1u : 0u)) + (o.w > key - (j + 3 < tid ? 1u : 0u));
+    }
     if (r < K) {
       t.list[r] = tid;
       // no entry below the K-th group's largest can be among the K (its index: not after the group)
@@ -270,52 +319,123 @@ __device__ __forceinline__ void top_search(TopSm& t, const LpArgs& a, const T* z
     }
   }
   __syncthreads();
-  const int steps = (g * kSeg + kPThr - 1) / kPThr;
-  for (int r0 = 0; r0 < K && t.list[r0] >= 0; ++r0) {
-    const int first = t.list[r0] * g * kSeg;
-    for (int s = 0; s < steps; ++s) {
-      const int i = s * kPThr + tid;
-      if (i < g * kSeg) {
-        const int v0 = (first + i) * E - head;
-        if (v0 < a.V) {
-          const uint4 q = load16<T>(z, v0, a.V);
-          const unsigned long long cut = t.cut;
+  const unsigned long long cut = t.cut;
+  const int vecs = g * kSeg;  // 16-byte vectors per group
+  // a warp per group; few entries but the K pass the cut
+  for (int r = warp; r < K && t.list[r] >= 0; r += kPWarps) {
+    const int first = t.list[r] * vecs;
+    for (int i0 = 0; i0 < vecs; i0 += 32 * 8) {
+      uint4 q[8];
 #pragma unroll
-          for (int e = 0; e < E / 2; ++e) {
-            const float2 f = un2(Lg<T>::pair(q, e));
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float x = (h ? f.y : f.x) + 0.f;
-              if (x > -INFINITY) {
-                const unsigned long long k = make_key(x, (uint32_t)(v0 + 2 * e + h));
-                if (k >= cut) t.buf[atomicAdd(&t.n, 1)] = k;
-              }
-            }
-          }
-        }
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + u * 32 + lane, v0 = (first + i) * E - head;
+        q[u] = i < vecs && v0 < a.V ? load16<T>(z, v0, a.V) : make_uint4(Lg<T>::kFill, Lg<T>::kFill, Lg<T>::kFill, Lg<T>::kFill);
       }
-      __syncthreads();
-      const bool full = t.n > kPKeep;
-      __syncthreads();  // (every thread has read the count before the next candidates add to it)
-      if (full) top_prune(t, K);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) top_filter<T>(t, q[u], (first + i0 + u * 32 + lane) * E - head, cut);
+    }
+  }
+  if (warp == kPWarps - 1) beside();
+  __syncthreads();
+  const bool all = t.n <= kPBuf;
+  __syncthreads();
+  if (!all) {
+    // Too many at once (sorted or constant rows): group by group, best first, cutting to the K best
+    // whenever kPKeep are exceeded, which raises the cut.
+    if (tid == 0) t.n = 0;
+    __syncthreads();
+    for (int r0 = 0; r0 < K && t.list[r0] >= 0; ++r0) {
+      const int first = t.list[r0] * vecs;
+      for (int i0 = 0; i0 < vecs; i0 += kPThr) {
+        const int i = i0 + tid, v0 = (first + i) * E - head;
+        if (i < vecs && v0 < a.V) top_filter<T>(t, load16<T>(z, v0, a.V), v0, t.cut);
+        __syncthreads();
+        const bool full = t.n > kPKeep;
+        __syncthreads();  // (every thread has read the count before the next candidates add to it)
+        if (full) top_prune(t, K);
+      }
     }
   }
   top_prune(t, K);
-  if (tid < K) {
-    const bool has = tid < t.n;
-    const unsigned long long k = has ? t.buf[tid] : 0ull;
-    a.top_ids[row * K + tid] = has ? (int32_t)key_token(k) : -1;
-    a.top_logp[row * K + tid] = has ? fmaf(key_score(k) - m, a.invT, -ls) : -INFINITY;
+}
+
+// Shared memory of a row's merge.
+template <bool TOP>
+struct RowSm {
+  TopSm top;
+  Part red[kPWarps];
+  float m, ls;
+};
+template <>
+struct RowSm<false> {
+  Part red[kPWarps];
+  float m, ls;
+};
+
+static_assert(offsetof(TopSm, gkey) == 0 && alignof(RowSm<true>) == 16, "gkey is 16-byte aligned");
+
+// A row's outputs from its segments' partial results, by a whole block.
+template <typename T, int PER, bool TOP>
+__device__ __forceinline__ void finish_row(RowSm<TOP>& sm, const LpArgs& a, const T* z, int head, long long row,
+                                           int x, float zx, float s2) {
+  const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nseg = a.nchunk * kPWarps, g = (nseg + kPGroups - 1) / kPGroups;  // segments per thread's group
+  const int ng = (nseg + g - 1) / g;
+  Part p{-INFINITY, 0.f, 0.f, 0};
+  const float4* part = a.ws.part + row * nseg;
+  for (int i = tid * g; i < min(nseg, tid * g + g); ++i) {
+    const float4 v = __ldcg(part + i);
+    part_merge(p, Part{v.x, v.y, v.z, __float_as_int(v.w)}, s2);
+  }
+  const float mx = p.m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) part_merge(p, part_shfl(p, o), s2);
+  if (lane == 0) sm.red[warp] = p;
+  auto outputs = [&]() {  // (one warp, after a barrier)
+    p = sm.red[lane & (kPWarps - 1)];
+#pragma unroll
+    for (int o = kPWarps / 2; o > 0; o >>= 1) part_merge(p, part_shfl(p, o), s2);
+    if (lane == 0) {
+      const bool bad = x < -1 || x >= a.V;
+      const bool none = p.S == 0.f;  // every entry -inf
+      const float ls = none ? 0.f : logf(p.S);
+      if (a.norm) a.norm[row] = make_float2(p.m, ls);
+      if (a.entropy) a.entropy[row] = none ? 0.f : fmaf(-kPLn2, p.A / p.S, ls);
+      if (a.logp)
+        a.logp[row] = x == -1 ? 0.f
+                      : bad || isnan(p.S) ? NAN
+                      : zx == -INFINITY   ? -INFINITY
+                                          : fmaf(zx - p.m, a.invT, -ls);
+      if (a.rank) a.rank[row] = bad ? -1 : x < 0 ? 0 : p.c + 1;
+      if (bad) atomicMax(&a.ws.hdr->status, kErrInvalid);
+      sm.m = p.m;
+      sm.ls = ls;
+    }
+  };
+  if constexpr (TOP) {
+    TopSm& t = sm.top;
+    top_search<T, PER>(t, a, z, head, mx, g, ng, outputs);
+    if (tid < a.top) {
+      const bool has = tid < t.n;
+      a.top_ids[row * a.top + tid] = has ? (int32_t)key_token(t.buf[tid]) : -1;
+      a.top_logp[row * a.top + tid] = has ? fmaf(key_score(t.buf[tid]) - sm.m, a.invT, -sm.ls) : -INFINITY;
+    }
+  } else {
+    __syncthreads();
+    if (warp == 0) outputs();
   }
 }
 
-template <typename T, int PER, bool TOP>
+// a row's token (-1: none) and its logit, +inf without one: nothing is above it
+template <typename T>
+__device__ __forceinline__ float token_logit(const LpArgs& a, const T* z, int x) {
+  return x >= 0 && x < a.V ? to_f<T>(z[x]) : INFINITY;
+}
+
+// ONE: the row's last block also merges it (small calls).
+template <typename T, int PER, bool TOP, bool ONE>
 __global__ void __launch_bounds__(kPThr) logprob_kernel(const T* __restrict__ logits, const LpArgs a) {
   constexpr int E = Lg<T>::E;
-  __shared__ Part red[kPWarps];
-  __shared__ float fin[2];
-  __shared__ int s_last;
-  __shared__ __align__(16) unsigned char top_raw[TOP ? sizeof(TopSm) : 16];
   const long long row = blockIdx.x / (unsigned)a.nchunk;
   const int ch = (int)(blockIdx.x % (unsigned)a.nchunk);
   const int lane = (int)(threadIdx.x & 31), warp = (int)(threadIdx.x >> 5);
@@ -331,8 +451,7 @@ __global__ void __launch_bounds__(kPThr) logprob_kernel(const T* __restrict__ lo
 #pragma unroll
     for (int u = 0; u < PER; ++u) q[u] = load16<T>(z, (g0 + u * 32 + lane) * E - head, V);
   }
-  const bool bad = x < -1 || x >= V;
-  const float zx = x >= 0 && !bad ? to_f<T>(z[x]) : INFINITY;
+  const float zx = token_logit<T>(a, z, x);
   const float s2 = a.invT * kPL2e;
   Part p;
   p.m = -INFINITY;
@@ -340,7 +459,6 @@ __global__ void __launch_bounds__(kPThr) logprob_kernel(const T* __restrict__ lo
   for (int u = 0; u < PER; ++u) p.m = Lg<T>::max16(p.m, q[u]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) p.m = fmaxf(p.m, __shfl_xor_sync(0xffffffffu, p.m, o));
-  if (TOP && lane == 0) a.ws.seg[(row * a.nchunk + ch) * kPWarps + warp] = p.m;
   const float mu = p.m == -INFINITY ? 0.f : p.m;
   const F2 nm = f2(-mu, -mu), ss = f2(s2, s2);
   F2 S = f2(0.f, 0.f), A = S;
@@ -363,59 +481,35 @@ __global__ void __launch_bounds__(kPThr) logprob_kernel(const T* __restrict__ lo
 #pragma unroll
   for (int u = 0; u < PER; ++u) Lg<T>::above(cnt, q[u], thr);
   p.c = __reduce_add_sync(0xffffffffu, Lg<T>::total(cnt));
-  if (lane == 0) red[warp] = p;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    p = red[0];
-#pragma unroll
-    for (int w = 1; w < kPWarps; ++w) part_merge(p, red[w], s2);
-    s_last = 1;
-    if (a.nchunk > 1) {
-      a.ws.part[row * a.nchunk + ch] = p;
-      __threadfence();
-      s_last = atomicAdd(&a.ws.count[row], 1u) == (unsigned)a.nchunk - 1u;
-    } else {
-      red[0] = p;
-    }
-  }
-  __syncthreads();
-  if (!s_last) return;
-  // ---- the row's last block
-  if (warp == 0) {
-    if (a.nchunk > 1) {
-      __threadfence();
-      p = Part{-INFINITY, 0.f, 0.f, 0};
-      for (int c = lane; c < a.nchunk; c += 32) {
-        const float4 v = __ldcg((const float4*)(a.ws.part + row * a.nchunk + c));
-        part_merge(p, Part{v.x, v.y, v.z, __float_as_int(v.w)}, s2);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) part_merge(p, part_shfl(p, o), s2);
-    } else {
-      p = red[0];
-    }
-    if (lane == 0) {
-      const bool none = p.S == 0.f;  // every entry -inf
-      const float ls = none ? 0.f : logf(p.S);
-      if (a.norm) a.norm[row] = make_float2(p.m, ls);
-      if (a.entropy) a.entropy[row] = none ? 0.f : fmaf(-kPLn2, p.A / p.S, ls);
-      if (a.logp)
-        a.logp[row] = x == -1 ? 0.f
-                      : bad || isnan(p.S) ? NAN
-                      : zx == -INFINITY   ? -INFINITY
-                                          : fmaf(zx - p.m, a.invT, -ls);
-      if (a.rank) a.rank[row] = bad ? -1 : x < 0 ? 0 : p.c + 1;
-      if (bad) atomicMax(&a.ws.hdr->status, kErrInvalid);
-      if (a.nchunk > 1) a.ws.count[row] = 0u;
-      fin[0] = p.m;
-      fin[1] = ls;
-    }
-  }
-  if (TOP) {
-    if (a.nchunk > 1) __threadfence();
+  if (lane == 0)
+    a.ws.part[(row * a.nchunk + ch) * kPWarps + warp] = make_float4(p.m, p.S, p.A, __int_as_float(p.c));
+  if constexpr (ONE) {
+    __shared__ __align__(16) RowSm<TOP> sm;
+    __shared__ int s_last;
     __syncthreads();
-    top_search<T, PER>(*(TopSm*)top_raw, a, z, head, row, fin[0], fin[1]);
+    if (threadIdx.x == 0) {
+      s_last = 1;
+      if (a.nchunk > 1) {
+        __threadfence();
+        s_last = atomicAdd(&a.ws.count[row], 1u) == (unsigned)a.nchunk - 1u;
+        if (s_last) {
+          __threadfence();
+          a.ws.count[row] = 0u;
+        }
+      }
+    }
+    __syncthreads();
+    if (s_last) finish_row<T, PER, TOP>(sm, a, z, head, row, x, zx, s2);
   }
+}
+
+template <typename T, int PER, bool TOP>
+__global__ void __launch_bounds__(kPThr) logprob_rows_kernel(const T* __restrict__ logits, const LpArgs a) {
+  __shared__ __align__(16) RowSm<TOP> sm;
+  const long long row = blockIdx.x;
+  const T* z = logits + row * a.ld;
+  const int x = a.tokens ? a.tokens[row] : -1;
+  finish_row<T, PER, TOP>(sm, a, z, row_head(z), row, x, token_logit<T>(a, z, x), a.invT * kPL2e);
 }
 
 // ------------------------------------------------------------------ gradient
@@ -513,30 +607,31 @@ int lp_chunks(int V, int E, int per, bool aligned_rows) {
   return (groups + kPThr * per - 1) / (kPThr * per);
 }
 
-template <typename T, int PER>
-cudaError_t lp_launch(int N, const T* logits, const LpArgs& a, cudaStream_t stream) {
-  const unsigned grid = (unsigned)N * (unsigned)a.nchunk;
-  if (a.top)
-    logprob_kernel<T, PER, true><<<grid, kPThr, 0, stream>>>(logits, a);
-  else
-    logprob_kernel<T, PER, false><<<grid, kPThr, 0, stream>>>(logits, a);
-  return cudaGetLastError();
-}
+// Sixteen-byte loads per thread: small problems take short segments, so that every SM has some, and
+// one launch.
+#ifndef LP_FEW
+#define LP_FEW 2
+#define LP_FEWB 8
+#define LP_MANY 8
+#endif
+constexpr int kPerMany = LP_MANY, kPerFew = LP_FEW;
+constexpr long long kFewBytes = (long long)LP_FEWB << 20;
 
-// Sixteen-byte loads per thread.  Small problems take short chunks so that every SM has some.
-constexpr int kPerMany = 8, kPerFew = 2;
-constexpr long long kFewBytes = 8ll << 20;
-
-template <typename T>
+template <typename T, bool TOP>
 cudaError_t lp_run(int N, const T* logits, LpArgs a, cudaStream_t stream) {
   constexpr int E = Lg<T>::E;
   const bool al = ((uintptr_t)logits % 16) == 0 && (a.ld * (long long)sizeof(T)) % 16 == 0;
   if ((long long)N * a.V * (long long)sizeof(T) <= kFewBytes) {
     a.nchunk = lp_chunks(a.V, E, kPerFew, al);
-    return lp_launch<T, kPerFew>(N, logits, a, stream);
+    logprob_kernel<T, kPerFew, TOP, true><<<(unsigned)N * (unsigned)a.nchunk, kPThr, 0, stream>>>(logits, a);
+    return cudaGetLastError();
   }
   a.nchunk = lp_chunks(a.V, E, kPerMany, al);
-  return lp_launch<T, kPerMany>(N, logits, a, stream);
+  logprob_kernel<T, kPerMany, TOP, false><<<(unsigned)N * (unsigned)a.nchunk, kPThr, 0, stream>>>(logits, a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  logprob_rows_kernel<T, kPerMany, TOP><<<N, kPThr, 0, stream>>>(logits, a);
+  return cudaGetLastError();
 }
 
 // Room for the chunks of N rows of at most V entries, whatever their type and alignment.  Short
@@ -550,11 +645,8 @@ size_t lp_slots(int N, int V) {
 
 }  // namespace
 
-size_t logprobs_workspace_bytes(int N, int V, int top) {
-  const size_t slots = lp_slots(N, V);
-  size_t o = sizeof(WsHeader) + lp_align((size_t)N * sizeof(unsigned)) + lp_align(slots * sizeof(Part));
-  if (top) o += lp_align(slots * kPWarps * sizeof(float));
-  return o;
+size_t logprobs_workspace_bytes(int N, int V, int) {
+  return sizeof(WsHeader) + lp_align((size_t)N * sizeof(unsigned)) + lp_align(lp_slots(N, V) * kPWarps * sizeof(float4));
 }
 
 cudaError_t launch_logprobs(int N, int V, float T, int bf16, const void* logits, long long ld,
@@ -578,11 +670,11 @@ cudaError_t launch_logprobs(int N, int V, float T, int bf16, const void* logits,
   w += sizeof(WsHeader);
   a.ws.count = (unsigned*)w;
   w += lp_align((size_t)N * sizeof(unsigned));
-  a.ws.part = (Part*)w;
-  w += lp_align(lp_slots(N, V) * sizeof(Part));
-  a.ws.seg = (float*)w;
-  return bf16 ? lp_run<__nv_bfloat16>(N, (const __nv_bfloat16*)logits, a, stream)
-              : lp_run<float>(N, (const float*)logits, a, stream);
+  a.ws.part = (float4*)w;
+  const __nv_bfloat16* zb = (const __nv_bfloat16*)logits;
+  const float* zf = (const float*)logits;
+  if (bf16) return top ? lp_run<__nv_bfloat16, true>(N, zb, a, stream) : lp_run<__nv_bfloat16, false>(N, zb, a, stream);
+  return top ? lp_run<float, true>(N, zf, a, stream) : lp_run<float, false>(N, zf, a, stream);
 }
 
 cudaError_t launch_logprobs_grad(int N, int V, float T, int bf16, const void* logits, long long ld,
