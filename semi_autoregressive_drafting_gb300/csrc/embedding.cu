@@ -218,6 +218,7 @@ __global__ void __launch_bounds__(kEThr) pairs_kernel(int N, int V, const int32_
                                                       int mark, int ncount, EgWs ws) {
   __shared__ __align__(16) uint32_t key[kPairs];
   __shared__ int cnt[kEThr / 32][32];
+  pdl_trigger();
   const int lane = (int)(threadIdx.x & 31), warp = (int)(threadIdx.x >> 5);
   const int n4 = (N + 3) & ~3;
   for (int i = threadIdx.x; i < n4; i += kEThr)
@@ -257,6 +258,7 @@ __global__ void __launch_bounds__(kSortThr) count_kernel(int N, int V, int per_b
                                                          const int32_t* __restrict__ tokens, int mark,
                                                          int ncount, EgWs ws) {
   __shared__ unsigned h[kBins];
+  pdl_trigger();
   for (int b = threadIdx.x; b < kBins; b += kSortThr) {
     h[b] = 0u;
     ws.hist[1][blockIdx.x * kBins + b] = 0u;
@@ -289,6 +291,8 @@ __global__ void __launch_bounds__(kSortThr) scatter_kernel(int N, int V, int per
   __shared__ unsigned wsum[kSortWarps];
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nb = (int)gridDim.x;
+  pdl_trigger();
+  pdl_wait();
   {  // base[d]: keys of lower digits, and of this digit in the blocks before
     unsigned below = 0u, all = 0u;
 #pragma unroll 8
@@ -354,6 +358,8 @@ __global__ void __launch_bounds__(kSortThr) scatter_kernel(int N, int V, int per
 }
 
 __global__ void __launch_bounds__(kSortThr) clear_kernel(unsigned* __restrict__ h) {
+  pdl_trigger();
+  pdl_wait();
   h[blockIdx.x * kBins + threadIdx.x] = 0u;
 }
 
@@ -435,6 +441,7 @@ __global__ void __launch_bounds__(kEThr) sum_kernel(const SumArgs a, const TG* _
                                                     TO* __restrict__ gW) {
   const int lane = (int)(threadIdx.x & 31);
   const int sum_blocks = (int)gridDim.x - a.fill_blocks;
+  pdl_wait();
   if ((int)blockIdx.x >= sum_blocks) {  // zero the rows of absent tokens, 32 rows at a time
     const int words = (a.V + 31) / 32;
     const unsigned per = (unsigned)a.D / E;
@@ -527,8 +534,7 @@ cudaError_t sums(SumArgs a, const TG* grad, TO* gW, cudaStream_t stream) {
   const long long warps = (long long)a.nslice * a.ntile;
   const unsigned grid = (unsigned)((warps + kEThr / 32 - 1) / (kEThr / 32)) + (unsigned)a.fill_blocks;
   if (grid == 0) return cudaSuccess;
-  sum_kernel<TG, TO, E><<<grid, kEThr, 0, stream>>>(a, grad, gW);
-  return cudaGetLastError();
+  return launch_pdl(sum_kernel<TG, TO, E>, grid, kEThr, 0, stream, a, grad, gW);
 }
 
 template <typename TG, typename TO>
@@ -582,14 +588,13 @@ cudaError_t launch_embedding_grad(int N, int V, int D, float scale, int g_bf16, 
     for (int p = 0; p < passes; ++p) {
       const int last = p == passes - 1;
       if (p >= 1 && !last) {  // (three passes: the counts of the first digit make room for the third's)
-        clear_kernel<<<nb, kSortThr, 0, stream>>>(a.ws.hist[(p + 1) & 1]);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = launch_pdl(clear_kernel, nb, kSortThr, 0, stream, a.ws.hist[(p + 1) & 1])) != cudaSuccess) return e;
       }
-      scatter_kernel<<<nb, kSortThr, 0, stream>>>(N, V, per_block, p * digit, digit, last,
-                                                  p == 0 ? tokens : nullptr, p ? a.ws.key[(p + 1) & 1] : nullptr,
-                                                  p ? a.ws.pos[(p + 1) & 1] : nullptr, a.ws.hist[p & 1],
-                                                  a.ws.hist[(p + 1) & 1], a.ws.key[p & 1], a.ws.pos[p & 1]);
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      if ((e = launch_pdl(scatter_kernel, nb, kSortThr, 0, stream, N, V, per_block, p * digit, digit, last,
+                          p == 0 ? tokens : nullptr, p ? a.ws.key[(p + 1) & 1] : nullptr,
+                          p ? a.ws.pos[(p + 1) & 1] : nullptr, a.ws.hist[p & 1], a.ws.hist[(p + 1) & 1],
+                          a.ws.key[p & 1], a.ws.pos[p & 1])) != cudaSuccess)
+        return e;
       at = p & 1;
     }
   }

@@ -307,6 +307,7 @@ __device__ __forceinline__ void top_search(TopSm& t, const LpArgs& a, const T* z
   // rank among the groups: larger maximum first, then the lower position
   if (tid < ng && mx != -INFINITY) {
     int r = 0;
+#pragma unroll 4
     for (int j = 0; j < ng; j += 4) {
       const uint4 o = *(const uint4*)(t.gkey + j);
       r += (o.x > key - (j < tid ? 1u : 0u)) + (o.y > key - (j + 1 < tid ? 1u : 0u)) +
@@ -337,9 +338,8 @@ __device__ __forceinline__ void top_search(TopSm& t, const LpArgs& a, const T* z
   }
   if (warp == kPWarps - 1) beside();
   __syncthreads();
-  const bool all = t.n <= kPBuf;
-  __syncthreads();
-  if (!all) {
+  if (t.n > kPBuf) {  // (in every thread or none: the count changes next behind a barrier)
+    __syncthreads();
     // Too many at once (sorted or constant rows): group by group, best first, cutting to the K best
     // whenever kPKeep are exceeded, which raises the cut.
     if (tid == 0) t.n = 0;
@@ -436,6 +436,7 @@ __device__ __forceinline__ float token_logit(const LpArgs& a, const T* z, int x)
 template <typename T, int PER, bool TOP, bool ONE>
 __global__ void __launch_bounds__(kPThr) logprob_kernel(const T* __restrict__ logits, const LpArgs a) {
   constexpr int E = Lg<T>::E;
+  if constexpr (!ONE) pdl_trigger();
   const long long row = blockIdx.x / (unsigned)a.nchunk;
   const int ch = (int)(blockIdx.x % (unsigned)a.nchunk);
   const int lane = (int)(threadIdx.x & 31), warp = (int)(threadIdx.x >> 5);
@@ -509,7 +510,9 @@ __global__ void __launch_bounds__(kPThr) logprob_rows_kernel(const T* __restrict
   const long long row = blockIdx.x;
   const T* z = logits + row * a.ld;
   const int x = a.tokens ? a.tokens[row] : -1;
-  finish_row<T, PER, TOP>(sm, a, z, row_head(z), row, x, token_logit<T>(a, z, x), a.invT * kPL2e);
+  const float zx = token_logit<T>(a, z, x);
+  pdl_wait();  // (above: only what the caller gave)
+  finish_row<T, PER, TOP>(sm, a, z, row_head(z), row, x, zx, a.invT * kPL2e);
 }
 
 // ------------------------------------------------------------------ gradient
@@ -609,13 +612,10 @@ int lp_chunks(int V, int E, int per, bool aligned_rows) {
 
 // Sixteen-byte loads per thread: small problems take short segments, so that every SM has some, and
 // one launch.
-#ifndef LP_FEW
-#define LP_FEW 2
-#define LP_FEWB 8
-#define LP_MANY 8
-#endif
-constexpr int kPerMany = LP_MANY, kPerFew = LP_FEW;
-constexpr long long kFewBytes = (long long)LP_FEWB << 20;
+// Measured: 16 MB of fp32 rows 8.4 us this way and 10.4 us the other, 64 MB with 20 alternatives the
+// other way round; segments of 4 KB against 2 KB in the largest call 288 and 348 us.
+constexpr int kPerMany = 8, kPerFew = 4;
+constexpr long long kFewBytes = 16ll << 20;
 
 template <typename T, bool TOP>
 cudaError_t lp_run(int N, const T* logits, LpArgs a, cudaStream_t stream) {
@@ -630,16 +630,15 @@ cudaError_t lp_run(int N, const T* logits, LpArgs a, cudaStream_t stream) {
   logprob_kernel<T, kPerMany, TOP, false><<<(unsigned)N * (unsigned)a.nchunk, kPThr, 0, stream>>>(logits, a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  logprob_rows_kernel<T, kPerMany, TOP><<<N, kPThr, 0, stream>>>(logits, a);
-  return cudaGetLastError();
+  return launch_pdl(logprob_rows_kernel<T, kPerMany, TOP>, (unsigned)N, kPThr, 0, stream, logits, a);
 }
 
 // Room for the chunks of N rows of at most V entries, whatever their type and alignment.  Short
-// chunks (problems of at most kFewBytes, so 2^22 entries, of 2^11 or more per chunk) are bounded by
-// their total: the room never shrinks as N or V grows, so a workspace serves smaller problems too.
+// chunks (problems of at most kFewBytes, of kPThr kPerFew 16 bytes per chunk) are bounded by their
+// total: the room never shrinks as N or V grows, so a workspace serves smaller problems too.
 size_t lp_slots(int N, int V) {
   const size_t many = (size_t)N * lp_chunks(V, 4, kPerMany, false);
-  const size_t few = (size_t)N * lp_chunks(V, 4, kPerFew, false), cap = 2048 + 2 * (size_t)N;
+  const size_t few = (size_t)N * lp_chunks(V, 4, kPerFew, false), cap = (size_t)kFewBytes / (kPThr * kPerFew * 16) + 2 * (size_t)N;
   return many > (few < cap ? few : cap) ? many : few < cap ? few : cap;
 }
 
