@@ -465,6 +465,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
     constexpr int kRowStep = WANT_A ? 16 : 4, kRowQuads = WANT_A ? 8 : 32;
     int g = 0;  // stages so far
     bool ok = true;
+    if constexpr (MODE == 3) {
+      // bf16 rows that start at any element: pairs of entries, consecutive along the lanes (half a warp
+      // per row of 32 in grad_a, two warps per row of 128 in grad_W2), from one 32-bit word, or from two
+      // where the row starts in the middle of one.  The next half stage's loads are in flight while this
+      // one waits for its place; nothing is done with a word before then.
+      const int row_of = WANT_A ? pt >> 4 : pt >> 6, x2 = WANT_A ? (pt & 15) * 2 : (pt & 63) * 2;
+      constexpr int kRows = WANT_A ? 8 : 2;  // rows per round (even: a thread's rows are all odd or all even)
+      const bool odd = (row_of & a.V & 1) != 0;
+      const long long total = (long long)a.N * a.V, words = total >> 1;
+      uint32_t w0[16], w1[16];
+      int left = 0;  // entries of the row from the thread's first one on
+      auto word = [&](long long k) {  // (the last one may be half a word)
+        return k < words ? __ldg((const uint32_t*)G + k) : (uint32_t)__ldg((const uint16_t*)G + 2 * k);
+      };
+      auto fetch = [&](const Item& t, int s) {
+        const int row0 = (WANT_A ? t.m0 : s * 64 + 32 * half) + row_of;
+        const int col = (WANT_A ? s * 64 + 32 * half : t.m0) + x2;
+        left = a.V - col;
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+          const int row = row0 + u * kRows;
+          const long long k = ((long long)row * a.V + col) >> 1;
+          w0[u] = w1[u] = 0u;
+          if (row < a.N && left > 0) w0[u] = word(k);
+          if (row < a.N && left > 1 && odd) w1[u] = word(k + 1);
+        }
+      };
+      int i = pair, s = 0;
+      Item t = {};
+      if (i < a.items) {
+        t = item_of<WANT_A>(a, i, rank);
+        s = t.k0;
+        fetch(t, s);
+      }
+      while (i < a.items) {
+        const int ga = 2 * g + half, slot = ga % kSA;
+        if (lane == 0 && ga >= kSA) ok = wait_or(&aempty[slot], (uint32_t)((ga / kSA - 1) & 1), stop);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) {
+          if (lane == 0) atomicMax(a.status, kErrTimeout);
+          break;
+        }
+        uint8_t* st = smem + (g % S::kStagesA) * S::kStageA;
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+          const int row = row_of + u * kRows + (WANT_A ? 0 : 32 * half), col = x2 + (WANT_A ? 32 * half : 0);
+          const int box = WANT_A ? row >> 6 : col >> 6, y = row & 63, x = col & 63;
+          uint32_t v = odd ? (w0[u] >> 16) | (w1[u] << 16) : w0[u];
+          if (left < 2) v = left < 1 ? 0u : v & 0xFFFFu;
+          *(uint32_t*)(st + box * kBox + y * 128 + (((x >> 3) ^ (y & 7)) << 4) + (x & 7) * 2) = v;
+        }
+        if (++s == t.k1) {
+          i += pairs;
+          if (i < a.items) {
+            t = item_of<WANT_A>(a, i, rank);
+            s = t.k0;
+          }
+        }
+        if (i < a.items) fetch(t, s);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_cluster(cluster_addr(&afull[slot], 0));
+        ++g;
+      }
+    } else
     for (int i = pair; ok && i < a.items; i += pairs) {
       const Item t = item_of<WANT_A>(a, i, rank);
       for (int s = t.k0; s < t.k1; ++s, ++g) {
