@@ -35,58 +35,77 @@ namespace {
 using bf16 = __nv_bfloat16;
 
 // ------------------------------------------------------------------ fp32 weights: CUDA cores
-// C[m][n] (+)= sum_k A(m, k) B(k, n) over 32 x 32 tiles; A and B by row and column strides.
-template <typename TA, typename TB>
-__global__ void __launch_bounds__(256) gemm_plain_kernel(int M, int Nn, int K, const TA* __restrict__ A,
-                                                         long long am, long long ak,
-                                                         const TB* __restrict__ B, long long bk,
-                                                         long long bn, float* __restrict__ C, long long cm,
-                                                         long long cn, int accumulate) {
-  __shared__ float sa[32][33], sb[32][33];
-  const int m0 = blockIdx.x * 32, n0 = blockIdx.y * 32;
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int k0 = 0; k0 < K; k0 += 32) {
-    for (int i = ty; i < 32; i += 8) {
-      // the tile index with unit stride goes along the lanes
-      const int ma = ak == 1 ? i : tx, ka = ak == 1 ? tx : i;
-      const bool oka = m0 + ma < M && k0 + ka < K;
-      sa[ka][ma] = oka ? to_f<TA>(A[(m0 + ma) * am + (k0 + ka) * ak]) : 0.f;
-      const int kb = bn == 1 ? i : tx, nb = bn == 1 ? tx : i;
-      const bool okb = k0 + kb < K && n0 + nb < Nn;
-      sb[kb][nb] = okb ? to_f<TB>(B[(k0 + kb) * bk + (n0 + nb) * bn]) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 32; ++k)
-#pragma unroll
-      for (int u = 0; u < 4; ++u) acc[u] = fmaf(sa[k][ty + 8 * u], sb[k][tx], acc[u]);
-    __syncthreads();
-  }
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int m = m0 + ty + 8 * u, n = n0 + tx;
-    if (m < M && n < Nn) {
-      float* c = C + m * cm + n * cn;
-      *c = accumulate ? *c + acc[u] : acc[u];
-    }
-  }
-}
+// C[share][m][n] (+)= sum over the share's k of A(m, k) B(k, n): 64 x 64 tiles, 16 products per thread
+// and step of K, the next 16 steps' elements in registers meanwhile.  A and B by row and column strides
+// (the index with unit stride goes along the lanes).
+constexpr int kFT = 64, kFK = 16;
 
-template <typename TG, typename TW>
-cudaError_t plain(int N, int V, int r, const TG* G, const TW* a, const TW* W2, int rv, float* ga, float* gW,
-                  int accumulate, cudaStream_t stream) {
-  const long long wv = rv ? 1 : r, wj = rv ? V : 1;
-  if (N > 0 && ga) {
-    gemm_plain_kernel<TG, TW><<<dim3((N + 31) / 32, (r + 31) / 32), 256, 0, stream>>>(
-        N, r, V, G, V, 1, W2, wv, wj, ga, r, 1, 0);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+template <typename TA, typename TB>
+__global__ void __launch_bounds__(256) gemm_f32_kernel(int M, int Nn, int K, int per, const TA* __restrict__ A,
+                                                       long long am, long long ak, const TB* __restrict__ B,
+                                                       long long bk, long long bn, float* __restrict__ C,
+                                                       long long cm, long long cn, long long cshare,
+                                                       int accumulate) {
+  __shared__ float sa[2][kFK][kFT + 4], sb[2][kFK][kFT + 4];
+  const int m0 = blockIdx.x * kFT, n0 = blockIdx.y * kFT, tid = threadIdx.x;
+  const int ka = blockIdx.z * per, kb = min(K, ka + per);
+  const int tx = tid & 15, ty = tid >> 4;
+  float ra[4], rb[4], acc[4][4] = {};
+  // element e of a thread: (k, m) by 256 e + tid, with k or m along the lanes
+  auto at_a = [&](int e, int& k, int& m) {
+    const int i = e * 256 + tid;
+    k = ak == 1 ? i % kFK : i / kFT;
+    m = ak == 1 ? i / kFK : i % kFT;
+  };
+  auto at_b = [&](int e, int& k, int& n) {
+    const int i = e * 256 + tid;
+    k = bn == 1 ? i / kFT : i % kFK;
+    n = bn == 1 ? i % kFT : i / kFK;
+  };
+  auto fetch = [&](int k0) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      int k, m;
+      at_a(e, k, m);
+      ra[e] = k0 + k < kb && m0 + m < M ? to_f<TA>(A[(m0 + m) * am + (k0 + k) * ak]) : 0.f;
+      at_b(e, k, m);
+      rb[e] = k0 + k < kb && n0 + m < Nn ? to_f<TB>(B[(k0 + k) * bk + (n0 + m) * bn]) : 0.f;
+    }
+  };
+  fetch(ka);
+  int p = 0;
+  for (int k0 = ka; k0 < kb; k0 += kFK, p ^= 1) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      int k, m;
+      at_a(e, k, m);
+      sa[p][k][m] = ra[e];
+      at_b(e, k, m);
+      sb[p][k][m] = rb[e];
+    }
+    __syncthreads();  // (the other buffer's readers passed this barrier's predecessor)
+    if (k0 + kFK < kb) fetch(k0 + kFK);
+#pragma unroll
+    for (int k = 0; k < kFK; ++k) {
+      const float4 x = *(const float4*)&sa[p][k][ty * 4], y = *(const float4*)&sb[p][k][tx * 4];
+      const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xs[i], ys[j], acc[i][j]);
+    }
   }
-  if (gW)
-    gemm_plain_kernel<TG, TW><<<dim3((V + 31) / 32, (r + 31) / 32), 256, 0, stream>>>(
-        V, r, N, G, 1, V, a, r, 1, gW, wv, wj, accumulate);
-  return cudaGetLastError();
+  C += blockIdx.z * cshare;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
+      if (m < M && n < Nn) {
+        float* c = C + m * cm + n * cn;
+        *c = accumulate ? *c + acc[i][j] : acc[i][j];
+      }
+    }
 }
 
 // ------------------------------------------------------------------ bf16 weights: tensor cores
@@ -623,6 +642,45 @@ __global__ void __launch_bounds__(256) share_sum_kernel(long long quads, int spl
   }
 }
 
+// fp32 weights: most blocks of a launch that shares the vocabulary out, and the floats of their results
+size_t plain_blocks(int nsm) { return 2 * (size_t)nsm; }
+size_t plain_floats(int N, int r, int nsm) {
+  const size_t all = plain_blocks(nsm) * N * r, tiles = plain_blocks(nsm) * kFT * kFT;
+  return all < tiles ? all : tiles;
+}
+
+template <typename TG, typename TW>
+cudaError_t plain(int N, int V, int r, const TG* G, const TW* a, const TW* W2, int rv, float* ga, float* gW,
+                  int accumulate, float* part, int nsm, cudaStream_t stream) {
+  const long long wv = rv ? 1 : r, wj = rv ? V : 1;
+  const unsigned nb = (unsigned)((r + kFT - 1) / kFT);
+  cudaError_t e = cudaSuccess;
+  if (ga) {
+    // shares of at least 64 entries, as many as fill the machine
+    const unsigned mb = (unsigned)((N + kFT - 1) / kFT);
+    int splits = (int)(plain_blocks(nsm) / ((size_t)mb * nb));
+    splits = splits > (V + 63) / 64 ? (V + 63) / 64 : splits < 1 ? 1 : splits;
+    const int per = ((V + splits - 1) / splits + kFK - 1) / kFK * kFK;
+    splits = (V + per - 1) / per;
+    float* out = splits > 1 ? part : ga;
+    gemm_f32_kernel<TG, TW><<<dim3(mb, nb, splits), 256, 0, stream>>>(N, r, V, per, G, V, 1, W2, wv, wj, out, r, 1,
+                                                                     (long long)N * r, 0);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (splits > 1) {
+      const long long quads = (long long)N * r / 4;
+      share_sum_kernel<<<(unsigned)((quads + 63) / 64), 256, 0, stream>>>(quads, splits, (const float4*)part,
+                                                                          (float4*)ga);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+  }
+  if (gW) {
+    gemm_f32_kernel<TG, TW><<<dim3((unsigned)((V + kFT - 1) / kFT), nb), 256, 0, stream>>>(
+        V, r, N, (N + kFK - 1) / kFK * kFK, G, 1, V, a, r, 1, gW, wv, wj, 0, accumulate);
+    e = cudaGetLastError();
+  }
+  return e;
+}
+
 size_t bg_align(size_t x) { return (x + 255) / 256 * 256; }
 
 // floats of shared-out results at most: kMaxItems work items of 256 x 256 per pair of SMs, and no more
@@ -737,7 +795,8 @@ __global__ void __launch_bounds__(256) zero_kernel(long long n4, float4* __restr
 
 size_t bias_grad_workspace_bytes(int N, int V, int r, int w_bf16, int nsm) {
   size_t o = sizeof(WsHeader);
-  if (w_bf16) o += bg_align(share_floats(N, r, nsm) * 4) + (V % 8 ? (size_t)V * r * 2 : 0);
+  o += w_bf16 ? bg_align(share_floats(N, r, nsm) * 4) + (V % 8 ? (size_t)V * r * 2 : 0)
+              : plain_floats(N, r, nsm) * 4;
   return o;
 }
 
@@ -752,9 +811,12 @@ cudaError_t launch_bias_grad(int N, int V, int r, int g_bf16, const void* G, int
   if (w_bf16)
     return tensor(N, V, r, g_bf16, G, (const bf16*)a, (const bf16*)W2, w2_rv, grad_a, grad_W2, accumulate,
                   (uint8_t*)workspace, nsm, stream);
+  float* part = (float*)((uint8_t*)workspace + sizeof(WsHeader));
   if (g_bf16)
-    return plain(N, V, r, (const bf16*)G, (const float*)a, (const float*)W2, w2_rv, grad_a, grad_W2, accumulate, stream);
-  return plain(N, V, r, (const float*)G, (const float*)a, (const float*)W2, w2_rv, grad_a, grad_W2, accumulate, stream);
+    return plain(N, V, r, (const bf16*)G, (const float*)a, (const float*)W2, w2_rv, grad_a, grad_W2, accumulate, part,
+                 nsm, stream);
+  return plain(N, V, r, (const float*)G, (const float*)a, (const float*)W2, w2_rv, grad_a, grad_W2, accumulate, part,
+               nsm, stream);
 }
 
 }  // namespace dspark
