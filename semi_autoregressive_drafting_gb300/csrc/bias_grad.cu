@@ -217,6 +217,9 @@ struct Src {
                        kOffBar = kOffRaw + kRaw * kRawBytes;
   static constexpr int kSmem = kOffBar + 512 + 1024;
   using T = typename std::conditional<MODE == 3, bf16, float>::type;
+  // The two groups of warps take alternate half stages: with an even number of slots a slot is always
+  // the same group's, which has then seen every phase of its barriers before the one it waits for.
+  static_assert(kTma || (kSlotsA % 2 == 0 && kRaw % 2 == 0), "a slot belongs to one group");
 };
 
 // A thread's part of a finished tile: columns c0 .. c0 + 127 of the item's, of one row.
@@ -300,7 +303,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
   }
   __syncthreads();
   cluster_sync_all();  // both CTAs are there
-  pdl_trigger();
+  if (WANT_A) pdl_trigger();  // (the sum of the shares follows)
   if (warp == 1) {
     tc::tmem_alloc_pair(tbase, 512);
     tc::tmem_relinquish_pair();
@@ -596,15 +599,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
   }
   tc::fence_before_sync();
   __syncthreads();
+  if (tid == 0 && !*stop) {
+    // The MMAs' signals that the last stages have been read come from the pair's other CTA too and are
+    // not waited for above: they arrive before this block ends, or they would find another's shared
+    // memory in its place.  (The phases before each slot's last use were waited for.)
+    int g = 0;
+    for (int i = pair; i < a.items; i += pairs) {
+      const Item t = item_of<WANT_A>(a, i, rank);
+      g += t.k1 - t.k0;
+    }
+    for (int j = max(0, g - kSB); j < g; ++j) mbar_wait(&bempty[j % kSB], (uint32_t)((j / kSB) & 1));
+    g *= S::kHalves;
+    for (int j = max(0, g - kSA); j < g; ++j) mbar_wait(&aempty[j % kSA], (uint32_t)((j / kSA) & 1));
+  }
   cluster_sync_all();  // the other CTA no longer reads this one's shared memory or arrives here
   if (warp == 1) {
     tc::fence_after_sync();
     tc::tmem_dealloc_pair(tmem, 512);
   }
   cluster_sync_all();  // neither CTA ends before both have freed
-  // grad_a's launch starts on the SMs that grad_W2's has left (neither reads what the other writes) but
-  // does not end before it, so that whatever waits for this launch finds both done.
-  if (WANT_A) pdl_wait();
 }
 
 // grad_a from the shares, in their order: four threads per 16 bytes, each a contiguous quarter.
@@ -691,25 +704,23 @@ size_t share_floats(int N, int r, int nsm) {
 }
 
 template <bool WANT_A, int MODE>
-cudaError_t bg_launch(const BgArgs& a, const CUtensorMap& tg, const CUtensorMap& tb, int nsm, bool behind,
-                      cudaStream_t stream) {
+cudaError_t bg_launch(const BgArgs& a, const CUtensorMap& tg, const CUtensorMap& tb, int nsm, cudaStream_t stream) {
   using S = Src<MODE>;
   cudaError_t e = cudaFuncSetAttribute(bias_grad_kernel<WANT_A, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        S::kSmem);
   if (e != cudaSuccess) return e;
   const int pairs = a.items < nsm / 2 ? a.items : nsm / 2;
-  if (behind) return launch_pdl(bias_grad_kernel<WANT_A, MODE>, 2 * pairs, S::kThreads, S::kSmem, stream, a, tg, tb);
   bias_grad_kernel<WANT_A, MODE><<<2 * pairs, S::kThreads, S::kSmem, stream>>>(a, tg, tb);
   return cudaGetLastError();
 }
 template <bool WANT_A>
-cudaError_t bg_mode(int mode, const BgArgs& a, const CUtensorMap& tg, const CUtensorMap& tb, int nsm, bool behind,
+cudaError_t bg_mode(int mode, const BgArgs& a, const CUtensorMap& tg, const CUtensorMap& tb, int nsm,
                     cudaStream_t stream) {
   switch (mode) {
-    case 0: return bg_launch<WANT_A, 0>(a, tg, tb, nsm, behind, stream);
-    case 1: return bg_launch<WANT_A, 1>(a, tg, tb, nsm, behind, stream);
-    case 2: return bg_launch<WANT_A, 2>(a, tg, tb, nsm, behind, stream);
-    default: return bg_launch<WANT_A, 3>(a, tg, tb, nsm, behind, stream);
+    case 0: return bg_launch<WANT_A, 0>(a, tg, tb, nsm, stream);
+    case 1: return bg_launch<WANT_A, 1>(a, tg, tb, nsm, stream);
+    case 2: return bg_launch<WANT_A, 2>(a, tg, tb, nsm, stream);
+    default: return bg_launch<WANT_A, 3>(a, tg, tb, nsm, stream);
   }
 }
 
@@ -738,17 +749,15 @@ cudaError_t tensor(int N, int V, int r, int g_bf16, const void* G, const bf16* a
     p.nstage_k = (N + 63) / 64;
     p.out = gW;
     p.wide = ((uintptr_t)gW % 32) == 0;
-    if ((e = bg_mode<false>(mode, p, tg, tb, nsm, false, stream)) != cudaSuccess) return e;
+    if ((e = bg_mode<false>(mode, p, tg, tb, nsm, stream)) != cudaSuccess) return e;
   }
   if (ga) {
     p.b_kmajor = rv;
     const bf16* W = W2;
-    bool behind = gW != nullptr;  // directly behind grad_W2's launch
     if (rv && V % 8 != 0) {  // rows that TMA cannot address: a [V][r] copy in the workspace
       bf16* t = (bf16*)(ws + sizeof(WsHeader) + bg_align(share_floats(N, r, nsm) * 4));
       if ((e = launch_transpose(W2, t, r, V, 2, stream)) != cudaSuccess) return e;
       W = t;
-      behind = false;
       p.b_kmajor = 0;
     }
     if (!(p.b_kmajor ? encode_bf16_2d(&tb, W, r, V, V, 64) : encode_bf16_2d(&tb, W, V, r, r, 64)))
@@ -776,7 +785,7 @@ cudaError_t tensor(int N, int V, int r, int g_bf16, const void* G, const bf16* a
     p.items = base * splits;
     p.out = splits > 1 ? part : ga;
     p.wide = ((uintptr_t)p.out % 32) == 0;
-    if ((e = bg_mode<true>(mode, p, tg, tb, nsm, behind, stream)) != cudaSuccess) return e;
+    if ((e = bg_mode<true>(mode, p, tg, tb, nsm, stream)) != cudaSuccess) return e;
     if (splits > 1) {
       const long long quads = (long long)N * r / 4;
       e = launch_pdl(share_sum_kernel, (unsigned)((quads + 63) / 64), 256, 0, stream, quads, splits,
