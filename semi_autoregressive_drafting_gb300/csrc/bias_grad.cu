@@ -36,9 +36,9 @@ using bf16 = __nv_bfloat16;
 
 // ------------------------------------------------------------------ fp32 weights: CUDA cores
 // C[share][m][n] (+)= sum over the share's k of A(m, k) B(k, n): 64 x 64 tiles, 16 products per thread
-// and step of K, the next 16 steps' elements in registers meanwhile.  A and B by row and column strides
+// and step of K, the next 32 steps' elements in registers meanwhile.  A and B by row and column strides
 // (the index with unit stride goes along the lanes).
-constexpr int kFT = 64, kFK = 16;
+constexpr int kFT = 64, kFK = 32, kFE = kFT * kFK / 256;  // kFE: elements of a tile per thread
 
 template <typename TA, typename TB>
 __global__ void __launch_bounds__(256) gemm_f32_kernel(int M, int Nn, int K, int per, const TA* __restrict__ A,
@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(256) gemm_f32_kernel(int M, int Nn, int K, int
   const int m0 = blockIdx.x * kFT, n0 = blockIdx.y * kFT, tid = threadIdx.x;
   const int ka = blockIdx.z * per, kb = min(K, ka + per);
   const int tx = tid & 15, ty = tid >> 4;
-  float ra[4], rb[4], acc[4][4] = {};
+  float ra[kFE], rb[kFE], acc[4][4] = {};
   // element e of a thread: (k, m) by 256 e + tid, with k or m along the lanes
   auto at_a = [&](int e, int& k, int& m) {
     const int i = e * 256 + tid;
@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(256) gemm_f32_kernel(int M, int Nn, int K, int
   };
   auto fetch = [&](int k0) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < kFE; ++e) {
       int k, m;
       at_a(e, k, m);
       ra[e] = k0 + k < kb && m0 + m < M ? to_f<TA>(A[(m0 + m) * am + (k0 + k) * ak]) : 0.f;
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(256) gemm_f32_kernel(int M, int Nn, int K, int
   int p = 0;
   for (int k0 = ka; k0 < kb; k0 += kFK, p ^= 1) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < kFE; ++e) {
       int k, m;
       at_a(e, k, m);
       sa[p][k][m] = ra[e];

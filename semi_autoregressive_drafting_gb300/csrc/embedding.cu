@@ -142,17 +142,48 @@ __global__ void __launch_bounds__(kEThr) embed_kernel(int N, int V, int D, float
   }
 }
 
+// Rows of any length and alignment: a warp per 256 elements of a row, consecutive along the lanes.
+template <typename TW, typename TO>
+__global__ void __launch_bounds__(kEThr) embed_any_kernel(int N, int V, int D, float scale, unsigned tiles,
+                                                          const TW* __restrict__ W,
+                                                          const int32_t* __restrict__ tokens,
+                                                          TO* __restrict__ out) {
+  const long long item = (long long)blockIdx.x * (kEThr / 32) + (threadIdx.x >> 5);
+  const long long row = item / tiles;
+  if (row >= N) return;
+  const int c0 = (int)(item - row * tiles) * 256 + (int)(threadIdx.x & 31);
+  const int t = tokens[row];
+  const bool in = t >= 0 && t < V;
+  const TW* w = W + (in ? (long long)t * D : 0);
+  TO* o = out + row * D;
+  float f[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int c = c0 + 32 * u;
+    f[u] = in ? (c < D ? to_f<TW>(w[c]) : 0.f) : t == -1 ? 0.f : NAN;
+  }
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int c = c0 + 32 * u;
+    const float x = in ? f[u] * scale : f[u];
+    if (c < D) store<1>(o + c, &x);
+  }
+}
+
 template <typename TW, typename TO>
 cudaError_t embed_run(int N, int V, int D, float scale, const TW* W, const int32_t* tokens, TO* out,
                       cudaStream_t stream) {
   constexpr int E = 16 / (int)sizeof(TW);
   const bool vec = D % E == 0 && ((uintptr_t)W % 16) == 0 && ((uintptr_t)out % (E * sizeof(TO))) == 0;
-  const long long pieces = (long long)N * (vec ? D / E : D);
-  const unsigned grid = (unsigned)((pieces + kEThr * kLook - 1) / (kEThr * kLook));
-  if (vec)
+  if (vec) {
+    const long long pieces = (long long)N * (D / E);
+    const unsigned grid = (unsigned)((pieces + kEThr * kLook - 1) / (kEThr * kLook));
     embed_kernel<TW, TO, E><<<grid, kEThr, 0, stream>>>(N, V, D, scale, W, tokens, out);
-  else
-    embed_kernel<TW, TO, 1><<<grid, kEThr, 0, stream>>>(N, V, D, scale, W, tokens, out);
+  } else {
+    const unsigned tiles = ((unsigned)D + 255) / 256;
+    const unsigned grid = (unsigned)(((long long)N * tiles + kEThr / 32 - 1) / (kEThr / 32));
+    embed_any_kernel<TW, TO><<<grid, kEThr, 0, stream>>>(N, V, D, scale, tiles, W, tokens, out);
+  }
   return cudaGetLastError();
 }
 

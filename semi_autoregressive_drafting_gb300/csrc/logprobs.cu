@@ -15,12 +15,11 @@
 // relative to it, and leaves them as one partial result.  A block per row merges the row's partial
 // results in their order: in large calls a second launch, so that a segment's warp ends with its
 // store; in small ones the row's last block to finish (a counter per row, no waits).
-// Alternatives: any of the K largest entries lies in one of the K segments that lead when ordered by
-// (maximum, position), since otherwise each of the K leaders holds an entry that precedes it.  So
-// that block ranks the segments and re-reads K of them, mostly from L2, and no lists are kept during
-// the pass.
-#include <cstddef>
-
+// Alternatives: the warps also leave the largest entry of each quarter of their segments.  The K-th
+// largest entry is no less than the K-th largest of these maxima.  So the block that merges the row
+// finds a bound just below that (of groups of quarters in long rows), re-reads the quarters that reach
+// it, mostly from L2, and sorts the entries that do; no lists are kept during the pass.  A row of fewer
+// than 2 K quarters, whose maxima say little, is read whole, with the threads' own maxima in their place.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -31,7 +30,7 @@ constexpr int kPThr = 256;
 constexpr int kPWarps = kPThr / 32;
 constexpr float kPL2e = 1.4426950408889634f;
 constexpr float kPLn2 = 0.6931471805599453f;
-constexpr int kPGroups = 256;   // segment groups ranked at most (one per thread)
+constexpr int kPGroups = 2 * kPThr;  // groups of quarter segments ranked at most (two per thread)
 constexpr int kPKeep = 256;     // candidates kept before a cut to the K best
 constexpr int kPBuf = kPKeep + kPThr * 8;
 static_assert(kPBuf % kPThr == 0 && kPBuf / kPThr * 32 <= 2 * kPThr, "what a first cut leaves: two per thread");
@@ -191,6 +190,7 @@ struct LpWs {
   WsHeader* hdr;
   unsigned* count;  // [N] blocks of the row done; zero between calls
   float4* part;     // [N][nchunk][8] each segment's Part
+  uint4* quart;     // [N][nchunk][8] the largest entries of its quarters, orderable (with alternatives)
 };
 
 struct LpArgs {
@@ -208,9 +208,9 @@ struct LpArgs {
 };
 
 // Shared memory of the alternatives' search.
-struct alignas(16) TopSm {  // (gkey is read in 16-byte pieces)
-  uint32_t gkey[kPGroups];                 // largest entry of each segment group, orderable
-  int list[32];                            // the leading groups, best first
+struct TopSm {
+  int list[kPGroups];                      // the groups to read, in any order
+  int pieces;
   unsigned long long buf[kPBuf];
   unsigned long long most[kPThr];          // each thread's largest candidate
   unsigned long long cut;                  // candidates below this are out
@@ -287,68 +287,84 @@ __device__ __forceinline__ void top_filter(TopSm& t, const uint4& q, int v0, uns
   }
 }
 
-// The K largest entries of a row, sorted, into t.buf (t.n of them), by a whole block.  mx: the largest
-// entry of the thread's group of g segments, -inf past the ng groups.  `beside` is run by the last
-// warp while the others read.
+// The K largest entries of a row, sorted, into t.buf (t.n of them), by a whole block.  `beside` is run
+// by the last warp while the others read.
 template <typename T, int PER, typename F>
-__device__ __forceinline__ void top_search(TopSm& t, const LpArgs& a, const T* z, int head, float mx, int g, int ng,
-                                           F beside) {
+__device__ __forceinline__ void top_search(TopSm& t, const LpArgs& a, const T* z, int head, long long row, F beside) {
   constexpr int E = Lg<T>::E;
-  constexpr int kSeg = 32 * PER;  // 16-byte groups per segment
+  constexpr int kQuart = 8 * PER;  // 16-byte vectors per quarter segment
   const int K = a.top, tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t key = orderable(mx + 0.f);
-  t.gkey[tid] = tid < ng ? key : 0u;
-  if (tid < 32) t.list[tid] = -1;
-  if (tid == 0) {
-    t.n = 0;
-    t.cut = 1ull;
+  const int nq = 4 * a.nchunk * kPWarps, g = (nq + kPGroups - 1) / kPGroups;  // quarters per group
+  const int ng = (nq + g - 1) / g;
+  const uint32_t* quart = (const uint32_t*)(a.ws.quart + row * a.nchunk * kPWarps);
+  constexpr uint32_t kNone = 0x007FFFFFu;  // -inf
+  uint32_t key[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int id = tid + h * kPThr;
+    key[h] = kNone;
+    for (int i = id * g; i < min(nq, id * g + g); ++i) key[h] = max(key[h], __ldcg(quart + i));
   }
-  __syncthreads();
-  // rank among the groups: larger maximum first, then the lower position
-  if (tid < ng && mx != -INFINITY) {
-    int r = 0;
-#pragma unroll 4
-    for (int j = 0; j < ng; j += 4) {
-      const uint4 o = *(const uint4*)(t.gkey + j);
-      r += (o.x > key - (j < tid ? 1u : 0u)) + (o.y > key - (j + 1 < tid ? 1u : 0u)) +
-           (o.z > key - (j + 2 < tid ? 1u : 0u)) + (o.w > key - (j + 3 < tid ? 1u : 0u));
-    }
-    if (r < K) {
-      t.list[r] = tid;
-      // no entry below the K-th group's largest can be among the K (its index: not after the group)
-      if (r == K - 1) t.cut = ((unsigned long long)key << 32) | (0xFFFFFFFFull - (uint32_t)min(a.V - 1, (tid + 1) * g * kSeg * E));
-    }
+  if (tid == 0) t.n = t.pieces = 0;
+  const bool whole = ng < 2 * K;
+  const int len = whole ? (a.V + head + E - 1) / E : g * kQuart;  // vectors per piece of the row
+  auto vec = [&](int i) {
+    const int v0 = i * E - head;
+    return v0 < a.V ? load16<T>(z, v0, a.V) : make_uint4(Lg<T>::kFill, Lg<T>::kFill, Lg<T>::kFill, Lg<T>::kFill);
+  };
+  if (whole) {
+    float m = -INFINITY;
+#pragma unroll 8
+    for (int i = tid; i < len; i += kPThr) m = Lg<T>::max16(m, vec(i));
+    key[0] = orderable(m + 0.f);
+    key[1] = kNone;
   }
+  // the largest bound, to 18 bits (sign, exponent, nine of the mantissa), that K maxima reach
+  uint32_t bound = 0u;
+  for (int bit = 31; bit >= 14; --bit) {
+    const uint32_t c = bound | (1u << bit);
+    int n = __syncthreads_count(key[0] >= c);
+    if (ng > kPThr) n += __syncthreads_count(key[1] >= c);
+    if (n >= K) bound = c;
+  }
+  if (whole) {
+    if (tid == 0) t.list[t.pieces++] = 0;
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (key[h] > kNone && key[h] >= bound) t.list[atomicAdd(&t.pieces, 1)] = tid + h * kPThr;
+  }
+  if (tid == 0) t.cut = max(1ull, (unsigned long long)bound << 32);
   __syncthreads();
   const unsigned long long cut = t.cut;
-  const int vecs = g * kSeg;  // 16-byte vectors per group
-  // a warp per group; few entries but the K pass the cut
-  for (int r = warp; r < K && t.list[r] >= 0; r += kPWarps) {
-    const int first = t.list[r] * vecs;
-    for (int i0 = 0; i0 < vecs; i0 += 32 * 8) {
-      uint4 q[8];
+  // The pieces (few entries but the K pass the cut) in runs of 32 vectors, eight in flight per warp.
+  const int runs = (len + 31) / 32, pieces = t.pieces;
+  for (int c0 = warp; c0 < pieces * runs; c0 += 8 * kPWarps) {
+    uint4 q[8];
+    int at[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int i = i0 + u * 32 + lane, v0 = (first + i) * E - head;
-        q[u] = i < vecs && v0 < a.V ? load16<T>(z, v0, a.V) : make_uint4(Lg<T>::kFill, Lg<T>::kFill, Lg<T>::kFill, Lg<T>::kFill);
-      }
-#pragma unroll
-      for (int u = 0; u < 8; ++u) top_filter<T>(t, q[u], (first + i0 + u * 32 + lane) * E - head, cut);
+    for (int u = 0; u < 8; ++u) {
+      const int c = c0 + u * kPWarps, r = c / runs, i = (c - r * runs) * 32 + lane;
+      const bool in = r < pieces && i < len;
+      at[u] = in ? t.list[r] * len + i : 0;
+      q[u] = in ? vec(at[u]) : make_uint4(Lg<T>::kFill, Lg<T>::kFill, Lg<T>::kFill, Lg<T>::kFill);
     }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) top_filter<T>(t, q[u], at[u] * E - head, cut);
   }
   if (warp == kPWarps - 1) beside();
   __syncthreads();
   if (t.n > kPBuf) {  // (in every thread or none: the count changes next behind a barrier)
     __syncthreads();
-    // Too many at once (sorted or constant rows): group by group, best first, cutting to the K best
-    // whenever kPKeep are exceeded, which raises the cut.
+    // Too many at once (sorted or constant rows): step by step, cutting to the K best whenever kPKeep are
+    // exceeded, which raises the cut.
     if (tid == 0) t.n = 0;
     __syncthreads();
-    for (int r0 = 0; r0 < K && t.list[r0] >= 0; ++r0) {
-      const int first = t.list[r0] * vecs;
-      for (int i0 = 0; i0 < vecs; i0 += kPThr) {
-        const int i = i0 + tid, v0 = (first + i) * E - head;
-        if (i < vecs && v0 < a.V) top_filter<T>(t, load16<T>(z, v0, a.V), v0, t.cut);
+    for (int r = 0; r < pieces; ++r) {
+      const int first = t.list[r] * len;
+      for (int i0 = 0; i0 < len; i0 += kPThr) {
+        const int i = i0 + tid;
+        if (i < len) top_filter<T>(t, vec(first + i), (first + i) * E - head, t.cut);
         __syncthreads();
         const bool full = t.n > kPKeep;
         __syncthreads();  // (every thread has read the count before the next candidates add to it)
@@ -372,22 +388,19 @@ struct RowSm<false> {
   float m, ls;
 };
 
-static_assert(offsetof(TopSm, gkey) == 0 && alignof(RowSm<true>) == 16, "gkey is 16-byte aligned");
 
 // A row's outputs from its segments' partial results, by a whole block.
 template <typename T, int PER, bool TOP>
 __device__ __forceinline__ void finish_row(RowSm<TOP>& sm, const LpArgs& a, const T* z, int head, long long row,
                                            int x, float zx, float s2) {
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int nseg = a.nchunk * kPWarps, g = (nseg + kPGroups - 1) / kPGroups;  // segments per thread's group
-  const int ng = (nseg + g - 1) / g;
+  const int nseg = a.nchunk * kPWarps;
   Part p{-INFINITY, 0.f, 0.f, 0};
   const float4* part = a.ws.part + row * nseg;
-  for (int i = tid * g; i < min(nseg, tid * g + g); ++i) {
+  for (int i = tid; i < nseg; i += kPThr) {
     const float4 v = __ldcg(part + i);
     part_merge(p, Part{v.x, v.y, v.z, __float_as_int(v.w)}, s2);
   }
-  const float mx = p.m;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) part_merge(p, part_shfl(p, o), s2);
   if (lane == 0) sm.red[warp] = p;
@@ -414,7 +427,7 @@ __device__ __forceinline__ void finish_row(RowSm<TOP>& sm, const LpArgs& a, cons
   };
   if constexpr (TOP) {
     TopSm& t = sm.top;
-    top_search<T, PER>(t, a, z, head, mx, g, ng, outputs);
+    top_search<T, PER>(t, a, z, head, row, outputs);
     if (tid < a.top) {
       const bool has = tid < t.n;
       a.top_ids[row * a.top + tid] = has ? (int32_t)key_token(t.buf[tid]) : -1;
@@ -456,10 +469,23 @@ __global__ void __launch_bounds__(kPThr) logprob_kernel(const T* __restrict__ lo
   const float s2 = a.invT * kPL2e;
   Part p;
   p.m = -INFINITY;
+  if constexpr (TOP) {
+    uint32_t k[4];
 #pragma unroll
-  for (int u = 0; u < PER; ++u) p.m = Lg<T>::max16(p.m, q[u]);
+    for (int j = 0; j < 4; ++j) {
+      float m = -INFINITY;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) p.m = fmaxf(p.m, __shfl_xor_sync(0xffffffffu, p.m, o));
+      for (int u = j * (PER / 4); u < (j + 1) * (PER / 4); ++u) m = Lg<T>::max16(m, q[u]);
+      k[j] = __reduce_max_sync(0xffffffffu, orderable(m + 0.f));
+    }
+    if (lane == 0) a.ws.quart[(row * a.nchunk + ch) * kPWarps + warp] = make_uint4(k[0], k[1], k[2], k[3]);
+    p.m = key_score((unsigned long long)max(max(k[0], k[1]), max(k[2], k[3])) << 32);
+  } else {
+#pragma unroll
+    for (int u = 0; u < PER; ++u) p.m = Lg<T>::max16(p.m, q[u]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) p.m = fmaxf(p.m, __shfl_xor_sync(0xffffffffu, p.m, o));
+  }
   const float mu = p.m == -INFINITY ? 0.f : p.m;
   const F2 nm = f2(-mu, -mu), ss = f2(s2, s2);
   F2 S = f2(0.f, 0.f), A = S;
@@ -644,8 +670,9 @@ size_t lp_slots(int N, int V) {
 
 }  // namespace
 
-size_t logprobs_workspace_bytes(int N, int V, int) {
-  return sizeof(WsHeader) + lp_align((size_t)N * sizeof(unsigned)) + lp_align(lp_slots(N, V) * kPWarps * sizeof(float4));
+size_t logprobs_workspace_bytes(int N, int V, int top) {
+  const size_t part = lp_align(lp_slots(N, V) * kPWarps * sizeof(float4));
+  return sizeof(WsHeader) + lp_align((size_t)N * sizeof(unsigned)) + (top ? 2 : 1) * part;
 }
 
 cudaError_t launch_logprobs(int N, int V, float T, int bf16, const void* logits, long long ld,
@@ -670,6 +697,7 @@ cudaError_t launch_logprobs(int N, int V, float T, int bf16, const void* logits,
   a.ws.count = (unsigned*)w;
   w += lp_align((size_t)N * sizeof(unsigned));
   a.ws.part = (float4*)w;
+  a.ws.quart = (uint4*)(w + lp_align(lp_slots(N, V) * kPWarps * sizeof(float4)));
   const __nv_bfloat16* zb = (const __nv_bfloat16*)logits;
   const float* zf = (const float*)logits;
   if (bf16) return top ? lp_run<__nv_bfloat16, true>(N, zb, a, stream) : lp_run<__nv_bfloat16, false>(N, zb, a, stream);
