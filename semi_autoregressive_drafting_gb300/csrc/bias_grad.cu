@@ -116,6 +116,8 @@ constexpr int kBM = 256;              // rows of a work item (a pair of CTAs)
 constexpr int kBN = 256;              // columns of a work item
 constexpr int kMaxItems = 2;          // work items per pair at most when the vocabulary is shared out
 constexpr int kRawBytes = 128 * 32 * 4;  // half a stage of an fp32 G as it lies
+constexpr int kWordBytes = 2 * 16 * 128 * 4;  // a half stage's words of G, those of unaligned rows twice
+constexpr int kDeep = 4;              // half stages of words in flight per group of four warps
 // Registers per thread where eight more warps bring G (640 threads, launched with 96 each): the
 // three shares, 128 x (48 + 2 x 160 + 2 x 56), are the launch's 640 x 96.
 constexpr int kRegsIssue = 48, kRegsSums = 160, kRegsBring = 56;
@@ -203,8 +205,8 @@ template <int MODE>
 struct Src {
   static constexpr bool kTma = MODE == 0, kTmaRaw = MODE == 1;
   static constexpr int kParts = MODE == 1 || MODE == 2 ? 3 : 1;
-  static constexpr int kStagesA = kParts == 3 ? 2 : 6;  // of G's parts
-  static constexpr int kStagesB = kParts == 3 ? 4 : 6;  // of W2 or a
+  static constexpr int kStagesA = kTma ? 6 : 2;  // of G's parts
+  static constexpr int kStagesB = kTma ? 6 : 4;  // of W2 or a
   // Where warps bring G, a stage is filled, multiplied and freed in halves of 32 of its K: twice the
   // steps in flight in the same memory (the chain of fill, MMAs and signals bounds this path).
   static constexpr int kHalves = kTma ? 1 : 2;
@@ -214,7 +216,7 @@ struct Src {
   static constexpr int kRunStages = kParts == 3 ? 2 : 8;  // 24 or 32 MMAs into one set of accumulators
   static constexpr int kThreads = kTma ? 384 : 640;
   static constexpr int kOffB = kStagesA * kStageA, kOffRaw = kOffB + kStagesB * kTileB,
-                       kOffBar = kOffRaw + kRaw * kRawBytes;
+                       kOffBar = kOffRaw + (MODE == 3 ? 2 * kDeep * kWordBytes : kRaw * kRawBytes);
   static constexpr int kSmem = kOffBar + 512 + 1024;
   using T = typename std::conditional<MODE == 3, bf16, float>::type;
   // The two groups of warps take alternate half stages: with an even number of slots a slot is always
@@ -490,54 +492,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
     if constexpr (MODE == 3) {
       // bf16 rows that start at any element: pairs of entries, consecutive along the lanes (half a warp
       // per row of 32 in grad_a, two warps per row of 128 in grad_W2), from one 32-bit word, or from two
-      // where the row starts in the middle of one.  The next half stage's loads are in flight while this
-      // one waits for its place; nothing is done with a word before then.
+      // where the row starts in the middle of one.  Every thread copies its own words ahead
+      // (asynchronously, kDeep half stages) and puts them in place when their turn comes.
       const int row_of = WANT_A ? pt >> 4 : pt >> 6, x2 = WANT_A ? (pt & 15) * 2 : (pt & 63) * 2;
       constexpr int kRows = WANT_A ? 8 : 2;  // rows per round (even: a thread's rows are all odd or all even)
       const bool odd = (row_of & a.V & 1) != 0;
-      const long long total = (long long)a.N * a.V, words = total >> 1;
-      uint32_t w0[16], w1[16];
-      int left = 0;  // entries of the row from the thread's first one on
-      auto word = [&](long long k) {  // (the last one may be half a word)
-        return k < words ? __ldg((const uint32_t*)G + k) : (uint32_t)__ldg((const uint16_t*)G + 2 * k);
-      };
-      auto fetch = [&](const Item& t, int s) {
+      const long long words = ((long long)a.N * a.V) >> 1;  // (then perhaps half of one)
+      uint32_t* mine = (uint32_t*)(raw + half * kDeep * kWordBytes) + pt;
+      const long long dk = (long long)kRows * a.V / 2;  // words from one of a thread's rows to its next
+      auto copy = [&](const Item& t, int s, int slot) {
         const int row0 = (WANT_A ? t.m0 : s * 64 + 32 * half) + row_of;
-        const int col = (WANT_A ? s * 64 + 32 * half : t.m0) + x2;
-        left = a.V - col;
+        const int col = (WANT_A ? s * 64 + 32 * half : t.m0) + x2, left = a.V - col;
+        const int rows = left > 0 && row0 < a.N ? min(16, (a.N - row0 + kRows - 1) / kRows) : 0;
+        const long long k0 = ((long long)row0 * a.V + col) >> 1;
+        const uint32_t* src = (const uint32_t*)a.G + k0;
+        uint32_t dst = smem_u32(mine + slot * (kWordBytes / 4));
+        // the word that only half exists, if it is one of these: a thread's last row's first or second
+        const int half0 = k0 + (rows - 1) * dk == words ? rows - 1 : -1;
+        const int half1 = k0 + 1 + (rows - 1) * dk == words ? rows - 1 : -1;
 #pragma unroll
         for (int u = 0; u < 16; ++u) {
-          const int row = row0 + u * kRows;
-          const long long k = ((long long)row * a.V + col) >> 1;
-          w0[u] = w1[u] = 0u;
-          if (row < a.N && left > 0) w0[u] = word(k);
-          if (row < a.N && left > 1 && odd) w1[u] = word(k + 1);
+          const bool in = u < rows;  // zeros where there is nothing to copy
+          const uint32_t* p = in ? src : (const uint32_t*)a.G;
+          const uint32_t n0 = !in ? 0u : u == half0 ? 2u : 4u;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(p), "r"(n0) : "memory");
+          if (odd) {
+            const bool in1 = in && left > 1;
+            const uint32_t n1 = !in1 ? 0u : u == half1 ? 2u : 4u;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 16 * 512), "l"(in1 ? p + 1 : p),
+                         "r"(n1)
+                         : "memory");
+          }
+          src += dk;
+          dst += 512;
         }
       };
-      int i = pair, s = 0;
-      Item t = {};
-      if (i < a.items) {
-        t = item_of<WANT_A>(a, i, rank);
-        s = t.k0;
-        fetch(t, s);
-      }
-      while (i < a.items) {
-        const int ga = 2 * g + half, slot = ga % kSA;
-        if (lane == 0 && ga >= kSA) ok = wait_or(&aempty[slot], (uint32_t)((ga / kSA - 1) & 1), stop);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) {
-          if (lane == 0) atomicMax(a.status, kErrTimeout);
-          break;
-        }
-        uint8_t* st = smem + (g % S::kStagesA) * S::kStageA;
-#pragma unroll
-        for (int u = 0; u < 16; ++u) {
-          const int row = row_of + u * kRows + (WANT_A ? 0 : 32 * half), col = x2 + (WANT_A ? 32 * half : 0);
-          const int box = WANT_A ? row >> 6 : col >> 6, y = row & 63, x = col & 63;
-          uint32_t v = odd ? (w0[u] >> 16) | (w1[u] << 16) : w0[u];
-          if (left < 2) v = left < 1 ? 0u : v & 0xFFFFu;
-          *(uint32_t*)(st + box * kBox + y * 128 + (((x >> 3) ^ (y & 7)) << 4) + (x & 7) * 2) = v;
-        }
+      auto step = [&](int& i, Item& t, int& s) {
         if (++s == t.k1) {
           i += pairs;
           if (i < a.items) {
@@ -545,12 +535,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
             s = t.k0;
           }
         }
-        if (i < a.items) fetch(t, s);
+      };
+      int i = pair, s = 0;
+      Item t = {};
+      if (i < a.items) {
+        t = item_of<WANT_A>(a, i, rank);
+        s = t.k0;
+      }
+      int ni = i, ns = s;  // the half stage to copy next
+      Item nt = t;
+      for (int d = 0; d < kDeep; ++d) {
+        if (ni < a.items) {
+          copy(nt, ns, d);
+          step(ni, nt, ns);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      }
+      while (i < a.items) {
+        const int ga = 2 * g + half, slot = ga % kSA;
+        asm volatile("cp.async.wait_group %0;" ::"n"(kDeep - 1) : "memory");
+        if (lane == 0 && ga >= kSA) ok = wait_or(&aempty[slot], (uint32_t)((ga / kSA - 1) & 1), stop);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) {
+          if (lane == 0) atomicMax(a.status, kErrTimeout);
+          break;
+        }
+        const uint32_t* w = mine + (g % kDeep) * (kWordBytes / 4);
+        const int left = a.V - ((WANT_A ? s * 64 + 32 * half : t.m0) + x2);
+        uint8_t* st = smem + (g % S::kStagesA) * S::kStageA;
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+          const int row = row_of + u * kRows + (WANT_A ? 0 : 32 * half), col = x2 + (WANT_A ? 32 * half : 0);
+          const int box = WANT_A ? row >> 6 : col >> 6, y = row & 63, x = col & 63;
+          uint32_t v = w[u * 128];
+          if (odd) v = (v >> 16) | (w[(16 + u) * 128] << 16);
+          if (left < 2) v = left < 1 ? 0u : v & 0xFFFFu;
+          *(uint32_t*)(st + box * kBox + y * 128 + (((x >> 3) ^ (y & 7)) << 4) + (x & 7) * 2) = v;
+        }
+        if (ni < a.items) {
+          copy(nt, ns, g % kDeep);
+          step(ni, nt, ns);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        step(i, t, s);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive_cluster(cluster_addr(&afull[slot], 0));
         ++g;
       }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
     } else
     for (int i = pair; ok && i < a.items; i += pairs) {
       const Item t = item_of<WANT_A>(a, i, rank);
