@@ -267,9 +267,18 @@ __device__ __forceinline__ void top_prune(TopSm& t, int K) {
   __syncthreads();
 }
 
-// The candidates among 16 bytes of a row whose first entry is v0.
+constexpr uint32_t kNone = 0x007FFFFFu;  // orderable(-inf)
+
+// the logit of a cut
+__device__ __forceinline__ float cut_score(unsigned long long cut) {
+  return (uint32_t)(cut >> 32) > kNone ? key_score(cut) : -INFINITY;
+}
+
+// The candidates among 16 bytes of a row whose first entry is v0 (few have one: their maximum is looked
+// at first).
 template <typename T>
 __device__ __forceinline__ void top_filter(TopSm& t, const uint4& q, int v0, unsigned long long cut) {
+  if (!(Lg<T>::max16(-INFINITY, q) >= cut_score(cut))) return;
 #pragma unroll
   for (int e = 0; e < Lg<T>::E / 2; ++e) {
     const float2 f = un2(Lg<T>::pair(q, e));
@@ -297,7 +306,6 @@ __device__ __forceinline__ void top_search(TopSm& t, const LpArgs& a, const T* z
   const int nq = 4 * a.nchunk * kPWarps, g = (nq + kPGroups - 1) / kPGroups;  // quarters per group
   const int ng = (nq + g - 1) / g;
   const uint32_t* quart = (const uint32_t*)(a.ws.quart + row * a.nchunk * kPWarps);
-  constexpr uint32_t kNone = 0x007FFFFFu;  // -inf
   uint32_t key[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -339,12 +347,13 @@ __device__ __forceinline__ void top_search(TopSm& t, const LpArgs& a, const T* z
   const unsigned long long cut = t.cut;
   // The pieces (few entries but the K pass the cut) in runs of 32 vectors, eight in flight per warp.
   const int runs = (len + 31) / 32, pieces = t.pieces;
+  const uint32_t inv = 0xFFFFFFFFu / (uint32_t)runs + 1u;  // c / runs = high half of c inv (c runs < 2^32)
   for (int c0 = warp; c0 < pieces * runs; c0 += 8 * kPWarps) {
     uint4 q[8];
     int at[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const int c = c0 + u * kPWarps, r = c / runs, i = (c - r * runs) * 32 + lane;
+      const int c = c0 + u * kPWarps, r = runs == 1 ? c : (int)__umulhi((uint32_t)c, inv), i = (c - r * runs) * 32 + lane;
       const bool in = r < pieces && i < len;
       at[u] = in ? t.list[r] * len + i : 0;
       q[u] = in ? vec(at[u]) : make_uint4(Lg<T>::kFill, Lg<T>::kFill, Lg<T>::kFill, Lg<T>::kFill);
