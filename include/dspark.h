@@ -325,7 +325,7 @@ dspark_status dspark_markov_draft_noalloc(int B, int gamma, int V, int r, int d,
  * norm (-inf, 0), entropy 0 and logp -inf.  NaN or +inf logits make their row's norm[1], logp and
  * entropy NaN; NaN entries are not alternatives and count in no rank.  Sums run in a fixed order: the
  * same inputs give the same bits.  Limits: 0 <= N <= 2^24 (N = 0 does nothing), 2 <= V <= 2^24,
- * N (V / 4096 + 2) < 2^31.  One launch.
+ * N (V / 4096 + 2) < 2^31.  One launch for up to 16 MB of logits, else two.
  */
 size_t dspark_token_logprobs_workspace_bytes(int N, int V, int top);
 dspark_status dspark_token_logprobs(int N, int V, float T, dspark_dtype zdt, const void* logits, int64_t ld,
@@ -384,8 +384,11 @@ dspark_status dspark_embedding_grad(int N, int V, int D, float scale, dspark_dty
  * dspark_token_logprobs_grad's); a [N][r] and W2 ([V][r] or [r][V], w2_layout) of type wdt; grad_a
  * [N][r] and grad_W2 (W2's layout) fp32, each optional (at least one).  accumulate != 0 adds to
  * grad_W2 (not to grad_a) instead of writing it.  All arrays 16-byte aligned.  Sums in fp32 in a fixed
- * order.  workspace: dspark_bias_grad_workspace_bytes(N, V, r, wdt) bytes, 256-byte aligned, zeroed
- * once.  Limits: r a multiple of 8 in 8..512, 2 <= V <= 2^24, 0 <= N <= 2^24 (N = 0: zero gradients).
+ * order.  bf16 weights run on the tensor cores (an fp32 G in three bf16 parts, all its 24 bits), fp32
+ * weights on the CUDA cores.  workspace: dspark_bias_grad_workspace_bytes(N, V, r, wdt) bytes, 256-byte
+ * aligned, zeroed once; a wait inside the kernel that exceeds about one second sets DSPARK_ERR_TIMEOUT
+ * in its status.  One launch per output, one more where grad_a's sum is shared out, and one for W2 as
+ * [r][V] in bf16 when V is not a multiple of 8.  Limits: r a multiple of 8 in 8..512, 2 <= V <= 2^24, 0 <= N <= 2^24 (N = 0: zero gradients).
  */
 size_t dspark_bias_grad_workspace_bytes(int N, int V, int r, dspark_dtype wdt);
 dspark_status dspark_bias_grad(int N, int V, int r, dspark_dtype gdt, const void* G, dspark_dtype wdt,

@@ -10,6 +10,12 @@ temperature T; W1 (embedding, [V][r]), W2 (logit projection: [r][V] as the pages
 ``w2_layout="rv"``, or a linear layer's [V][r] weight with the default ``"vr"``), w (confidence
 weight [d + r]), Wj (RNN joint projection [3r][2r + d]), U (base logits [B][gamma][V]),
 h (hidden states [B][gamma][d]), x0 (anchors [B]).
+
+Beside the draft block: ``token_logprobs`` scores given tokens (log probability, entropy, rank,
+alternatives), ``embedding`` looks rows of a table up, and ``token_logprobs_grad``, ``bias_grad`` and
+``embedding_grad`` are the gradients that lead from a likelihood back to W1 and W2
+(``examples/train_markov_head.py`` runs them together).  Each has a ``...Plan`` that checks and
+marshals its arguments once.
 """
 from __future__ import annotations
 
@@ -588,7 +594,7 @@ def embedding_grad(grad, tokens, V, *, scale=1.0, dtype=torch.float32, accumulat
 
 
 class BiasGradWorkspace(Workspace):
-    """Zero-initialised device scratch for ``bias_grad`` (shapes up to N rows, V, r)."""
+    """Zero-initialised device scratch for ``bias_grad`` of this shape (or fewer rows)."""
 
     def __init__(self, N: int, V: int, r: int, bf16: bool = True, device=None):
         n = _lib.load().dspark_bias_grad_workspace_bytes(N, V, r, _BF16 if bf16 else _F32)

@@ -22,6 +22,14 @@
 // 2e-8 of themselves per MMA (measured: 1.5e-5 after 784).  So a run of 24 or 32 MMAs goes to one half
 // of TMEM, and while the next run goes to the other half, the eight warps add the first to sums in
 // their registers (128 columns of a row per thread), rounded to nearest.
+//
+// 3584 x 262144 x 256 from bf16: 820 us in a row of calls (370 us per product alone; a library bf16
+// product of the same operands 357 and 313).  Streaming G bounds it: with 16 columns in place of 256 a
+// product still takes 340 us (5.5 TB/s), the tensor pipe is active half the time.  448 x 151936 x 256 from
+// fp32: 207 us, bound by the chain of steps per half stage (copy, split, signal, MMAs, signal) that the
+// shared memory left for slots cannot hide: no single step taken out saves more than 14 of 95 us per
+// product.  One CTA per tile instead of a pair took 925 and 179 us, the latter with two parts; fences at
+// cluster scope in the signals cost 60 us of the latter.
 // fp32 weights (small heads): CUDA-core tiles.
 #include <cuda.h>
 

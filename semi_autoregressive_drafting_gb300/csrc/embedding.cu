@@ -12,6 +12,12 @@
 // bitmap names.  A run inside one slice is written at once; of a longer one every slice's warp leaves
 // an fp32 partial sum, and the last of them to arrive (a counter per run and columns, no waits) adds
 // those up in their order.
+//
+// Bound by HBM once the table is large: 448 tokens x 256 over 151936 rows of fp32 take 26.7 us (the 156 MB
+// written, 0.86 of a copy's rate; 5 us are the sort), 32768 bf16 rows of 2560 into 1.56 GB 272 us (0.94).
+// The join in the sum launch replaced a launch of its own that took 27 us in the second case; 16-byte
+// stores two apart, half a sector each, had made the zeroing take 390 us.  The lookup of 32768 rows of
+// 4096 bf16 takes 64 us (5.8 TB/s).
 #include "common.cuh"
 #include "kernels.h"
 
