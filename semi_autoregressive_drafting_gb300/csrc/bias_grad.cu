@@ -6,17 +6,19 @@
 //
 // bf16 weights: two tensor-core products (tcgen05, kind::f16, fp32 accumulation in TMEM), each with
 // G as the M-side operand and 256 columns of the other one:
-//   grad_W2: M = 256 vocabulary entries (G as it lies is M-major), K = N; one tile per work item;
-//   grad_a:  M = 256 rows, K = a share of the vocabulary (G as it lies is K-major); the shares'
-//            fp32 results are added in order by a second launch.
-// A pair of CTAs (cta_group::2) takes a work item: each holds 128 of the rows and half the columns,
-// so that W2 or a reaches each SM's shared memory once per 256 rows of G.  One block per SM walks
-// over its pair's items: TMA threads, one thread of the pair that issues the MMAs, eight warps that
+//   grad_W2: M = vocabulary entries (G as it lies is M-major), K = N; one tile per work item;
+//   grad_a:  M = rows, K = a share of the vocabulary (G as it lies is K-major); the shares' fp32 results
+//            are added in order by a second launch.
+// One block per SM walks over work items: TMA threads, one thread that issues the MMAs, eight warps that
 // read the accumulators out of TMEM.
+// A bf16 G comes by TMA, and a pair of CTAs (cta_group::2) takes an item of 256 rows: each holds 128 of
+// them and half the columns, so that W2 or a reaches each SM's shared memory once per 256 rows of G.
 // An fp32 G enters as three bf16 parts, hi = bf16(G), mid = bf16(G - hi), lo = bf16(G - hi - mid): all
 // 24 bits (two parts measured 2.5e-6 of the result off, an fp32 product 1e-6).  TMA brings it as it
 // lies, and eight warps split it from one shared-memory buffer into another.  A G whose rows TMA
-// cannot address is read by the same warps, element by element.
+// cannot address is brought by the same warps: fp32 element by element, bf16 by copied words.  These
+// paths take items of 128 rows, one CTA each (a pair gained nothing there: the signals between its CTAs
+// cost what the halved operand saved).
 //
 // The tensor cores add into fp32 accumulators with truncation: over a long K the sums shrink by about
 // 2e-8 of themselves per MMA (measured: 1.5e-5 after 784).  So a run of 24 or 32 MMAs goes to one half
@@ -24,12 +26,11 @@
 // their registers (128 columns of a row per thread), rounded to nearest.
 //
 // 3584 x 262144 x 256 from bf16: 820 us in a row of calls (370 us per product alone; a library bf16
-// product of the same operands 357 and 313).  Streaming G bounds it: with 16 columns in place of 256 a
-// product still takes 340 us (5.5 TB/s), the tensor pipe is active half the time.  448 x 151936 x 256 from
-// fp32: 207 us, bound by the chain of steps per half stage (copy, split, signal, MMAs, signal) that the
-// shared memory left for slots cannot hide: no single step taken out saves more than 14 of 95 us per
-// product.  One CTA per tile instead of a pair took 925 and 179 us, the latter with two parts; fences at
-// cluster scope in the signals cost 60 us of the latter.
+// product of the same operands 357 and 313).  With 16 columns in place of 256 a product still takes
+// 340 us: G's stream (5.5 TB/s) and the MMAs, which cost about 200 cycles each whatever their columns, are
+// both near their limits.  448 x 151936 x 256 from fp32: 207 us, 94 and 104 per product, of which the
+// twelve MMAs of a 64-deep stage are 67 (170 cycles each); the split, in their shadow, adds 13.
+// Fences at cluster scope in a pair's signals had cost 60 us, two bf16 parts would save 25.
 // fp32 weights (small heads): CUDA-core tiles.
 #include <cuda.h>
 
@@ -118,11 +119,9 @@ __global__ void __launch_bounds__(256) gemm_f32_kernel(int M, int Nn, int K, int
 
 // ------------------------------------------------------------------ bf16 weights: tensor cores
 constexpr int kBox = 64 * 128;        // bytes of one shared-memory box: 64 rows of 64 bf16
-constexpr int kTileA = 2 * kBox;      // 128 (M) x 64 (K) of G: a CTA's half of a pair's tile
-constexpr int kTileB = 2 * kBox;      // 64 (K) x 128 of W2 or a: a CTA's half of the columns
-constexpr int kBM = 256;              // rows of a work item (a pair of CTAs)
+constexpr int kTileA = 2 * kBox;      // 128 (M) x 64 (K) of G
 constexpr int kBN = 256;              // columns of a work item
-constexpr int kMaxItems = 2;          // work items per pair at most when the vocabulary is shared out
+constexpr int kMaxItems = 2;          // work items per CTA or pair at most when the vocabulary is shared out
 constexpr int kRawBytes = 128 * 32 * 4;  // half a stage of an fp32 G as it lies
 constexpr int kWordBytes = 2 * 16 * 128 * 4;  // a half stage's words of G, those of unaligned rows twice
 constexpr int kDeep = 4;              // half stages of words in flight per group of four warps
@@ -133,7 +132,7 @@ constexpr int kRegsIssue = 48, kRegsSums = 160, kRegsBring = 56;
 struct BgArgs {
   int N, V, r;
   int items, nrb;       // work items; blocks of 256 columns of r
-  int nmb;              // grad_a: blocks of 256 rows
+  int nmb;              // grad_a: blocks of 128 rows (a pair: 256)
   int per_split;        // grad_a: K stages per share of the vocabulary
   int nstage_k;         // K stages in all
   int b_kmajor;         // grad_a: W2 is [r][V]
@@ -159,12 +158,12 @@ __device__ __forceinline__ bool wait_or(uint64_t* bar, uint32_t parity, volatile
   return true;
 }
 
-// One work item as a CTA of the pair sees it: its 128 rows, the K stages, the columns; the columns
-// that the MMA takes (a multiple of 16) and this CTA's half of them.
+// One work item as a CTA sees it: its 128 rows, the K stages, the columns; the columns that the MMA takes
+// (a multiple of 16), and those of them that this CTA brings (half of them in a pair): first, number.
 struct Item {
-  int m0, k0, k1, c0, cols, split, n, half0;
+  int m0, k0, k1, c0, cols, split, n, b0, nb;
 };
-template <bool WANT_A>
+template <bool WANT_A, bool PAIR>
 __device__ __forceinline__ Item item_of(const BgArgs& a, int i, int rank) {
   Item t;
   const int rb = i % a.nrb;
@@ -172,14 +171,15 @@ __device__ __forceinline__ Item item_of(const BgArgs& a, int i, int rank) {
   t.c0 = rb * kBN;
   t.cols = min(kBN, a.r - t.c0);
   t.n = (t.cols + 15) / 16 * 16;
-  t.half0 = t.c0 + rank * (t.n / 2);
+  t.nb = PAIR ? t.n / 2 : t.n;
+  t.b0 = t.c0 + rank * t.nb;
   if (WANT_A) {
-    t.m0 = (i % a.nmb) * kBM + rank * 128;
+    t.m0 = (i % a.nmb) * (PAIR ? 256 : 128) + rank * 128;
     t.split = i / a.nmb;
     t.k0 = t.split * a.per_split;
     t.k1 = min(a.nstage_k, t.k0 + a.per_split);
   } else {
-    t.m0 = i * kBM + rank * 128;
+    t.m0 = i * (PAIR ? 256 : 128) + rank * 128;
     t.split = 0;
     t.k0 = 0;
     t.k1 = a.nstage_k;
@@ -212,9 +212,12 @@ __device__ __forceinline__ uint2 take_bf16(float4& f) {
 template <int MODE>
 struct Src {
   static constexpr bool kTma = MODE == 0, kTmaRaw = MODE == 1;
+  static constexpr bool kPair = kTma;
+  static constexpr int kBM = kPair ? 256 : 128;
+  static constexpr int kTileB = (kPair ? 2 : 4) * kBox;  // 64 (K) x 128 or 256 of W2 or a
   static constexpr int kParts = MODE == 1 || MODE == 2 ? 3 : 1;
   static constexpr int kStagesA = kTma ? 6 : 2;  // of G's parts
-  static constexpr int kStagesB = kTma ? 6 : 4;  // of W2 or a
+  static constexpr int kStagesB = kTma ? 6 : 2;  // of W2 or a
   // Where warps bring G, a stage is filled, multiplied and freed in halves of 32 of its K: twice the
   // steps in flight in the same memory (the chain of fill, MMAs and signals bounds this path).
   static constexpr int kHalves = kTma ? 1 : 2;
@@ -266,15 +269,16 @@ __device__ __forceinline__ void write_out(const BgArgs& a, const Item& t, int ro
 }
 
 template <bool WANT_A, int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads, 1)
+__global__ void __cluster_dims__(Src<MODE>::kPair ? 2 : 1, 1, 1) __launch_bounds__(Src<MODE>::kThreads, 1)
     bias_grad_kernel(const BgArgs a, const __grid_constant__ CUtensorMap tmG,
                      const __grid_constant__ CUtensorMap tmB) {
   using S = Src<MODE>;
-  constexpr int kSA = S::kSlotsA, kSB = S::kStagesB, kRaw = S::kRaw > 0 ? S::kRaw : 1;
+  constexpr bool kPair = S::kPair;
+  constexpr int kTileB = S::kTileB, kSA = S::kSlotsA, kSB = S::kStagesB, kRaw = S::kRaw > 0 ? S::kRaw : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* raw = smem + S::kOffRaw;
-  // Of the pair's two copies, rank 0's count: G's parts in place (afull), W2 or a in place (bfull),
+  // Of a pair's two copies, rank 0's count: G's parts in place (afull), W2 or a in place (bfull),
   // accumulators read (tfree).  Both ranks' own: MMAs have read a stage (aempty, bempty), a run's MMAs
   // are complete (done), an fp32 G has arrived or been split (rfull, rempty).
   uint64_t* afull = (uint64_t*)(smem + S::kOffBar);
@@ -289,11 +293,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
   volatile int* stop = (volatile int*)(tbase + 1);
   static_assert((2 * kSA + 2 * kSB + 4 + 2 * kRaw) * 8 + 8 <= 512, "barriers fit");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = (int)cluster_rank(), pair = (int)blockIdx.x >> 1, pairs = (int)gridDim.x >> 1;
+  const int rank = kPair ? (int)cluster_rank() : 0;
+  const int pair = (int)blockIdx.x >> (kPair ? 1 : 0), pairs = (int)gridDim.x >> (kPair ? 1 : 0);
 
   if (tid == 0) {
     for (int i = 0; i < kSA; ++i) {
-      mbar_init(&afull[i], S::kTma ? 1 : 8);
+      mbar_init(&afull[i], S::kTma ? 1 : 4);
       mbar_init(&aempty[i], 1);
     }
     for (int i = 0; i < kSB; ++i) {
@@ -302,7 +307,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&done[i], 1);
-      mbar_init(&tfree[i], 16);
+      mbar_init(&tfree[i], kPair ? 16 : 8);
     }
     for (int i = 0; i < kRaw; ++i) {
       mbar_init(&rfull[i], 1);
@@ -312,15 +317,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
     fence_mbar_init();
   }
   __syncthreads();
-  cluster_sync_all();  // both CTAs are there
+  if (kPair) cluster_sync_all();  // both CTAs are there
   if (WANT_A) pdl_trigger();  // (the sum of the shares follows)
   if (warp == 1) {
-    tc::tmem_alloc_pair(tbase, 512);
-    tc::tmem_relinquish_pair();
+    if (kPair) {
+      tc::tmem_alloc_pair(tbase, 512);
+      tc::tmem_relinquish_pair();
+    } else {
+      tc::tmem_alloc(tbase, 512);
+      tc::tmem_relinquish();
+    }
   }
   tc::fence_before_sync();
   __syncthreads();
-  cluster_sync_all();  // both CTAs' barriers and TMEM are ready
+  if (kPair) cluster_sync_all();  // both CTAs' barriers and TMEM are ready
   tc::fence_after_sync();
   const uint32_t tmem = *tbase;
 
@@ -331,22 +341,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
       int g = 0;
       bool ok = true;
       for (int i = pair; ok && i < a.items; i += pairs) {
-        const Item t = item_of<WANT_A>(a, i, rank);
-        const int nb = (t.n / 2 + 63) / 64;
+        const Item t = item_of<WANT_A, kPair>(a, i, rank);
+        const int nb = (t.nb + 63) / 64;
         for (int s = t.k0; s < t.k1; ++s, ++g) {
           const int slot = g % kSB;
           if (g >= kSB && !wait_or(&bempty[slot], (uint32_t)((g / kSB - 1) & 1), stop)) {
             ok = false;
             break;
           }
-          if (rank == 0) mbar_expect_tx(&bfull[slot], (uint32_t)(2 * nb * kBox));  // both CTAs' boxes
-          const uint32_t bar = cluster_addr(&bfull[slot], 0);
           uint8_t* st = smem + S::kOffB + slot * kTileB;
-          for (int b = 0; b < nb; ++b)
-            if (WANT_A && a.b_kmajor)
-              tc::tma_load_2d_pair(st + b * kBox, &tmB, s * 64, t.half0 + 64 * b, bar, keep);
+          if (rank == 0) mbar_expect_tx(&bfull[slot], (uint32_t)((kPair ? 2 : 1) * nb * kBox));  // both CTAs' boxes
+          for (int b = 0; b < nb; ++b) {
+            const int c = t.b0 + 64 * b;
+            const bool km = WANT_A && a.b_kmajor;
+            if (kPair)
+              tc::tma_load_2d_pair(st + b * kBox, &tmB, km ? s * 64 : c, km ? c : s * 64, cluster_addr(&bfull[slot], 0),
+                                   keep);
             else
-              tc::tma_load_2d_pair(st + b * kBox, &tmB, t.half0 + 64 * b, s * 64, bar, keep);
+              tc::tma_load_2d(st + b * kBox, &tmB, km ? s * 64 : c, km ? c : s * 64, &bfull[slot], keep);
+          }
         }
       }
       if (!ok) atomicMax(a.status, kErrTimeout);
@@ -359,7 +372,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
       int g = 0;
       bool ok = true;
       for (int i = pair; ok && i < a.items; i += pairs) {
-        const Item t = item_of<WANT_A>(a, i, rank);
+        const Item t = item_of<WANT_A, kPair>(a, i, rank);
         for (int s = t.k0 * S::kHalves; s < t.k1 * S::kHalves; ++s, ++g) {
           const int slot = g % kS;
           if (g >= kS && !wait_or(S::kTma ? &aempty[slot] : &rempty[slot], (uint32_t)((g / kS - 1) & 1), stop)) {
@@ -387,11 +400,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
         for (int j = max(0, g - kS); j < g; ++j)
           mbar_wait(S::kTma ? &afull[j % kS] : &rfull[j % kS], (uint32_t)((j / kS) & 1));
     } else if (warp == 1 && lane == 0 && rank == 0) {  // ---- MMA, for both CTAs
+      auto commit = [](uint64_t* bar) {
+        if (kPair)
+          tc::mma_commit_pair(bar);
+        else
+          tc::mma_commit(bar);
+      };
       int g = 0, n = 0;  // stages and runs so far
       bool ok = true;
       for (int i = pair; ok && i < a.items; i += pairs) {
-        const Item t = item_of<WANT_A>(a, i, 0);
-        const uint32_t idesc = tc::idesc_bf16_f32(kBM, t.n) | (WANT_A ? 0u : tc::kIdescAMajorMN) |
+        const Item t = item_of<WANT_A, kPair>(a, i, 0);
+        const uint32_t idesc = tc::idesc_bf16_f32(S::kBM, t.n) | (WANT_A ? 0u : tc::kIdescAMajorMN) |
                                (WANT_A && a.b_kmajor ? 0u : tc::kIdescBMajorMN);
         for (int s0 = t.k0; ok && s0 < t.k1; s0 += S::kRunStages) {
           const int buf = n & 1;
@@ -426,17 +445,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
 #pragma unroll
                 for (int j = 0; j < 4 / S::kHalves; ++j) {
                   const int kk = half * (4 / S::kHalves) + j;
-                  tc::mma_bf16_pair(tmem + buf * kBN, ad + (WANT_A ? 2 : 128) * kk, bd + bstep * kk, idesc,
-                                    (s - s0) | half | h | j);
+                  if (kPair)
+                    tc::mma_bf16_pair(tmem + buf * kBN, ad + (WANT_A ? 2 : 128) * kk, bd + bstep * kk, idesc,
+                                      (s - s0) | half | h | j);
+                  else
+                    tc::mma_bf16(tmem + buf * kBN, ad + (WANT_A ? 2 : 128) * kk, bd + bstep * kk, idesc,
+                                 (s - s0) | half | h | j);
                 }
               }
-              tc::mma_commit_pair(&aempty[sla]);
+              commit(&aempty[sla]);
             }
             if (!ok) break;
-            tc::mma_commit_pair(&bempty[slb]);
+            commit(&bempty[slb]);
           }
           if (ok) {
-            tc::mma_commit_pair(&done[buf]);
+            commit(&done[buf]);
             ++n;
           }
         }
@@ -444,7 +467,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
       if (!ok) {
         atomicMax(a.status, kErrTimeout);
         // what was issued completes before TMEM is freed
-        tc::mma_commit_pair(&done[n & 1]);
+        commit(&done[n & 1]);
         mbar_wait(&done[n & 1], (uint32_t)((n / 2) & 1));
       }
     }
@@ -456,7 +479,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
     int n = 0;
     bool ok = true;
     for (int i = pair; ok && i < a.items; i += pairs) {
-      const Item t = item_of<WANT_A>(a, i, rank);
+      const Item t = item_of<WANT_A, kPair>(a, i, rank);
       float x[kBN / 2];
 #pragma unroll
       for (int j = 0; j < kBN / 2; ++j) x[j] = 0.f;
@@ -479,7 +502,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
           }
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive_cluster_relaxed(cluster_addr(&tfree[buf], 0));
+        if (lane == 0) {
+          if (kPair)
+            tc::mbar_arrive_cluster_relaxed(cluster_addr(&tfree[buf], 0));
+          else
+            mbar_arrive(&tfree[buf]);
+        }
       }
       const int row = t.m0 + 32 * q + lane;
       if (ok && row < (WANT_A ? a.N : a.V)) write_out<WANT_A>(a, t, row, c_lo, x);
@@ -539,7 +567,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
         if (++s == t.k1) {
           i += pairs;
           if (i < a.items) {
-            t = item_of<WANT_A>(a, i, rank);
+            t = item_of<WANT_A, kPair>(a, i, rank);
             s = t.k0;
           }
         }
@@ -547,7 +575,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
       int i = pair, s = 0;
       Item t = {};
       if (i < a.items) {
-        t = item_of<WANT_A>(a, i, rank);
+        t = item_of<WANT_A, kPair>(a, i, rank);
         s = t.k0;
       }
       int ni = i, ns = s;  // the half stage to copy next
@@ -588,13 +616,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
         step(i, t, s);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive_cluster(cluster_addr(&afull[slot], 0));
+        if (lane == 0) mbar_arrive(&afull[slot]);
         ++g;
       }
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     } else
     for (int i = pair; ok && i < a.items; i += pairs) {
-      const Item t = item_of<WANT_A>(a, i, rank);
+      const Item t = item_of<WANT_A, kPair>(a, i, rank);
       for (int s = t.k0; s < t.k1; ++s, ++g) {
         const int ga = 2 * g + half, slot = ga % kSA;
         if (lane == 0) {
@@ -633,7 +661,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
         __syncwarp();
         if (lane == 0) {
           if (S::kTmaRaw) mbar_arrive(&rempty[ga % kRaw]);
-          tc::mbar_arrive_cluster(cluster_addr(&afull[slot], 0));
+          mbar_arrive(&afull[slot]);
         }
       }
     }
@@ -641,24 +669,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Src<MODE>::kThreads,
   tc::fence_before_sync();
   __syncthreads();
   if (tid == 0 && !*stop) {
-    // The MMAs' signals that the last stages have been read come from the pair's other CTA too and are
-    // not waited for above: they arrive before this block ends, or they would find another's shared
+    // The MMAs' signals that the last stages have been read are not waited for above, and in a pair come
+    // from the other CTA too: they arrive before this block ends, or they would find another's shared
     // memory in its place.  (The phases before each slot's last use were waited for.)
     int g = 0;
     for (int i = pair; i < a.items; i += pairs) {
-      const Item t = item_of<WANT_A>(a, i, rank);
+      const Item t = item_of<WANT_A, kPair>(a, i, rank);
       g += t.k1 - t.k0;
     }
     for (int j = max(0, g - kSB); j < g; ++j) mbar_wait(&bempty[j % kSB], (uint32_t)((j / kSB) & 1));
     g *= S::kHalves;
     for (int j = max(0, g - kSA); j < g; ++j) mbar_wait(&aempty[j % kSA], (uint32_t)((j / kSA) & 1));
   }
-  cluster_sync_all();  // the other CTA no longer reads this one's shared memory or arrives here
+  if (kPair) cluster_sync_all();  // the other CTA no longer reads this one's shared memory or arrives here
   if (warp == 1) {
     tc::fence_after_sync();
-    tc::tmem_dealloc_pair(tmem, 512);
+    if (kPair)
+      tc::tmem_dealloc_pair(tmem, 512);
+    else
+      tc::tmem_dealloc(tmem, 512);
   }
-  cluster_sync_all();  // neither CTA ends before both have freed
+  if (kPair) cluster_sync_all();  // neither CTA ends before both have freed
 }
 
 // grad_a from the shares, in their order: four threads per 16 bytes, each a contiguous quarter.
@@ -737,10 +768,10 @@ cudaError_t plain(int N, int V, int r, const TG* G, const TW* a, const TW* W2, i
 
 size_t bg_align(size_t x) { return (x + 255) / 256 * 256; }
 
-// floats of shared-out results at most: kMaxItems work items of 256 x 256 per pair of SMs, and no more
-// shares than that many work items
+// floats of shared-out results at most: kMaxItems work items of 128 x 256 per SM (of 256 x 256 per pair),
+// and no more shares than that many work items
 size_t share_floats(int N, int r, int nsm) {
-  const size_t cap = (size_t)kMaxItems * (nsm / 2), all = cap * N * r, tiles = cap * kBM * kBN;
+  const size_t cap = (size_t)kMaxItems * nsm, all = cap * N * r, tiles = cap * 128 * kBN;
   return all < tiles ? all : tiles;
 }
 
@@ -750,8 +781,9 @@ cudaError_t bg_launch(const BgArgs& a, const CUtensorMap& tg, const CUtensorMap&
   cudaError_t e = cudaFuncSetAttribute(bias_grad_kernel<WANT_A, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        S::kSmem);
   if (e != cudaSuccess) return e;
-  const int pairs = a.items < nsm / 2 ? a.items : nsm / 2;
-  bias_grad_kernel<WANT_A, MODE><<<2 * pairs, S::kThreads, S::kSmem, stream>>>(a, tg, tb);
+  constexpr int kCtas = S::kPair ? 2 : 1;
+  const int units = a.items < nsm / kCtas ? a.items : nsm / kCtas;
+  bias_grad_kernel<WANT_A, MODE><<<kCtas * units, S::kThreads, S::kSmem, stream>>>(a, tg, tb);
   return cudaGetLastError();
 }
 template <bool WANT_A>
@@ -768,6 +800,7 @@ cudaError_t bg_mode(int mode, const BgArgs& a, const CUtensorMap& tg, const CUte
 cudaError_t tensor(int N, int V, int r, int g_bf16, const void* G, const bf16* a, const bf16* W2, int rv,
                    float* ga, float* gW, int accumulate, uint8_t* ws, int nsm, cudaStream_t stream) {
   const int mode = g_bf16 ? (V % 8 == 0 ? 0 : 3) : (V % 4 == 0 ? 1 : 2);
+  const int bm = mode == 0 ? 256 : 128;  // rows of a work item: a pair's or a CTA's
   float* part = (float*)(ws + sizeof(WsHeader));
   BgArgs p;
   p.N = N;
@@ -786,7 +819,7 @@ cudaError_t tensor(int N, int V, int r, int g_bf16, const void* G, const bf16* a
     if (!encode_bf16_2d(&tb, a, N, r, r, 64)) return cudaErrorInvalidValue;
     if (mode == 1 && !encode_f32_2d(&tg, G, N, V, 128, 32)) return cudaErrorInvalidValue;
     if (mode > 1) tg = tb;  // (not used)
-    p.items = (V + kBM - 1) / kBM * p.nrb;
+    p.items = (V + bm - 1) / bm * p.nrb;
     p.nstage_k = (N + 63) / 64;
     p.out = gW;
     p.wide = ((uintptr_t)gW % 32) == 0;
@@ -805,17 +838,17 @@ cudaError_t tensor(int N, int V, int r, int g_bf16, const void* G, const bf16* a
       return cudaErrorInvalidValue;
     if (mode == 1 && !encode_f32_2d(&tg, G, N, V, 32, 128)) return cudaErrorInvalidValue;
     if (mode > 1) tg = tb;
-    p.nmb = (N + kBM - 1) / kBM;
+    p.nmb = (N + bm - 1) / bm;
     p.nstage_k = (V + 63) / 64;
     // Shares of the vocabulary: the rounds of work items times the stages of one, against writing and
     // reading the shares' results (microseconds: a stage of 128 x 64 at the memory's rate per SM)
-    const int base = p.nmb * p.nrb, pairs = nsm / 2;
+    const int base = p.nmb * p.nrb, units = mode == 0 ? nsm / 2 : nsm;
     const double stage = (g_bf16 ? 0.38 : 0.75), io = (double)N * r * 8 / 6.7e6;
     int splits = 1;
     double best = 1e300;
-    for (int s = 1; s <= p.nstage_k && (long long)base * s <= (long long)kMaxItems * pairs; ++s) {
+    for (int s = 1; s <= p.nstage_k && (long long)base * s <= (long long)kMaxItems * units; ++s) {
       const int per = (p.nstage_k + s - 1) / s;
-      const double t = (double)((base * s + pairs - 1) / pairs) * per * stage + (s > 1 ? s * io + 2.0 : 0.0);
+      const double t = (double)((base * s + units - 1) / units) * per * stage + (s > 1 ? s * io + 2.0 : 0.0);
       if (t < best) {
         best = t;
         splits = s;

@@ -94,6 +94,26 @@ def test_bias_grad_repeat_identical_and_other_stream():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("gdt,V", [(torch.float32, 4096), (torch.bfloat16, 4096), (torch.bfloat16, 4099)])
+def test_bias_grad_in_a_graph(gdt, V):
+    G, a, W2 = [x.cuda() for x in make(300, V, 128, gdt, torch.bfloat16, "vr", 8)]
+    plan = ds.BiasGradPlan(G, a, W2)
+    plan.run()
+    torch.cuda.synchronize()
+    want = [x.clone() for x in plan.out]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        plan.run(torch.cuda.current_stream())
+    for _ in range(3):
+        for x in plan.out:
+            x.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(plan.out, want))
+    assert plan.workspace.status() == 0
+
+
+@pytest.mark.gpu
 def test_bias_grad_keeps_infinities_and_nan():
     # what is not finite reaches the rows that it touches and no others
     G, a, W2 = make(40, 3000, 64, torch.float32, torch.bfloat16, "vr", 5)

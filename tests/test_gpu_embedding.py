@@ -158,6 +158,25 @@ def test_embedding_grad_order_and_workspace_reuse():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("N", [500, 9000])
+def test_embedding_grad_in_a_graph(N):
+    V, D = 3000, 72
+    g = torch.randn(N, D, generator=torch.Generator().manual_seed(N)).cuda()
+    plan = ds.EmbeddingGradPlan(g, tokens(N, V, 11, "text").cuda(), V)
+    plan.run()
+    torch.cuda.synchronize()
+    want = plan.out.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan.run(torch.cuda.current_stream())
+    for _ in range(3):
+        plan.out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(plan.out, want)
+
+
+@pytest.mark.gpu
 def test_embedding_grad_no_tokens_and_all_padding():
     out = ds.embedding_grad(torch.empty(0, 12, device="cuda"),
                             torch.empty(0, dtype=torch.int32, device="cuda"), 30)
