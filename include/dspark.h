@@ -364,7 +364,7 @@ dspark_status dspark_embedding(int N, int V, int D, float scale, dspark_dtype wd
  * The table's gradient for dspark_embedding:
  *   grad_W[v] = scale * sum_{i : tokens[i] = v} grad[i],
  * every sum in fp32 and in an order that depends on the tokens alone (the same inputs give the same
- * bits; no floating-point atomics).  grad [N][D] of type gdt, grad_W [V][D] of type odt (rounded
+ * bits).  grad [N][D] of type gdt, grad_W [V][D] of type odt (rounded
  * once).  accumulate = 0 writes every row (zero for tokens that do not occur); otherwise the sums are
  * added to grad_W and other rows are neither read nor written.  tokens[i] = -1 adds nothing; another
  * token outside [0, V) adds nothing and sets DSPARK_ERR_INVALID in the workspace status.

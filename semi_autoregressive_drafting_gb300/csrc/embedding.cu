@@ -79,11 +79,6 @@ __device__ __forceinline__ void store(bf16* p, const float* f) {
   }
 }
 template <int E>
-__device__ __forceinline__ void load_out(const float* p, float* f) {
-#pragma unroll
-  for (int i = 0; i < E; ++i) f[i] = p[i];
-}
-template <int E>
 __device__ __forceinline__ void load_out(const bf16* p, float* f) {
 #pragma unroll
   for (int i = 0; i < E; ++i) f[i] = __bfloat162float(p[i]);
@@ -194,7 +189,9 @@ cudaError_t embed_run(int N, int V, int D, float scale, const TW* W, const int32
 }
 
 // ------------------------------------------------------------------ gradient: workspace
-constexpr int kPairs = 4096;      // most tokens that are sorted by counting all pairs
+// Most tokens that are sorted by counting all pairs: measured, the whole gradient of 4000 tokens takes
+// 28.8 us this way, of 8192 39.0, and 31.8 with the radix sort.
+constexpr int kPairs = 4096;
 constexpr int kBinBits = 9, kBins = 1 << kBinBits;
 constexpr int kSortThr = 512, kSortWarps = kSortThr / 32;
 constexpr int kTile = 1024;       // keys per tile of a sort block
@@ -412,18 +409,38 @@ struct SumArgs {
   EgWs ws;
 };
 
+// A finished row.  Added to the output, it is added by the memory (fp32), so that no warp waits for what
+// is there; each element gets one addition, so its order is not in question.
+template <int E>
+__device__ __forceinline__ void add_out(float* o, const float* f) {
+  if (E == 1) {
+    asm volatile("red.global.add.f32 [%0], %1;" ::"l"(o), "f"(f[0]) : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; i += 4)
+      asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(o + i), "f"(f[i]), "f"(f[(i + 1) % E]),
+                   "f"(f[(i + 2) % E]), "f"(f[(i + 3) % E])
+                   : "memory");
+  }
+}
+template <int E>
+__device__ __forceinline__ void add_out(bf16* o, const float* f) {
+  float g[E];
+  load_out<E>(o, g);
+#pragma unroll
+  for (int e = 0; e < E; ++e) g[e] += f[e];
+  store<E>(o, g);
+}
+
 template <typename TO, int E>
 __device__ __forceinline__ void put_row(TO* o, const float* s, float scale, int accumulate) {
   float f[E];
-  if (accumulate) {
-    load_out<E>(o, f);
 #pragma unroll
-    for (int e = 0; e < E; ++e) f[e] = fmaf(scale, s[e], f[e]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; ++e) f[e] = scale * s[e];
-  }
-  store<E>(o, f);
+  for (int e = 0; e < E; ++e) f[e] = scale * s[e];
+  if (accumulate)
+    add_out<E>(o, f);
+  else
+    store<E>(o, f);
 }
 
 // One slice's part of a run that crosses slices has been stored (part 1 of the slice in which it
