@@ -26,11 +26,12 @@
 // their registers (128 columns of a row per thread), rounded to nearest.
 //
 // 3584 x 262144 x 256 from bf16: 820 us in a row of calls (370 us per product alone; a library bf16
-// product of the same operands 357 and 313).  With 16 columns in place of 256 a product still takes
-// 340 us: G's stream (5.5 TB/s) and the MMAs, which cost about 200 cycles each whatever their columns, are
-// both near their limits.  448 x 151936 x 256 from fp32: 207 us, 94 and 104 per product, of which the
-// twelve MMAs of a 64-deep stage are 67 (170 cycles each); the split, in their shadow, adds 13.
-// Fences at cluster scope in a pair's signals had cost 60 us, two bf16 parts would save 25.
+// product of the same operands 357 and 313; one CTA per item 385 and 400).  G's stream bounds it: with 16
+// columns in place of 256 a product still takes 335 us (5.6 TB/s).  448 x 151936 x 256 from fp32: 207 us,
+// 94 and 104 per product.  Copies with a step taken out took, of the 95 of grad_a: the split 82, two
+// thirds of the MMAs 88, W2 88, reading the accumulators 89, all of them 50: the chain of the steps bounds
+// it, through shared memory that moves 288 KB per 64-deep stage (2250 cycles of about 2430).  Fences at
+// cluster scope in a pair's signals had cost 60 us.
 // fp32 weights (small heads): CUDA-core tiles.
 #include <cuda.h>
 
