@@ -24,9 +24,9 @@
 // Bound by HBM once the rows are many: 3584 x 262144 bf16 rows take 285 us (6.6 TB/s, 0.97 of a copy's
 // rate), the fp32 gradient of 448 x 151936 rows 82 us (6.7 TB/s).  With the merge in the pass itself
 // the first took 340 us: a block that waits for its fence and counter holds registers that loads could
-// use.  512 x 151936 fp32 rows with 20 alternatives take 62 us, 50 of them the pass; ranking the segments
+// use.  512 x 151936 fp32 rows with 20 alternatives take 60 us, 50 of them the pass; ranking the segments
 // by all pairs instead of the counted bound cost 13 us more.  Small calls are a chain of latencies (launch,
-// loads, fence and counter, bound, quarters, sort): 8 x 151936 bf16 rows 6.3 us, 10.5 with 5 alternatives.
+// loads, fence and counter, bound, quarters, sort): 8 x 151936 bf16 rows 6.3 us, 10.3 with 5 alternatives.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -303,23 +303,41 @@ __device__ __forceinline__ void top_filter(TopSm& t, const uint4& q, int v0, uns
   }
 }
 
+// The groups of a row's quarter segments: g quarters each, ng of them, at most two per thread.
+struct Groups {
+  int g, ng;
+  uint32_t key[2];  // the largest entries of the thread's groups, orderable
+};
+__device__ __forceinline__ Groups load_groups(const LpArgs& a, long long row) {
+  Groups q;
+  const int nq = 4 * a.nchunk * kPWarps;
+  q.g = (nq + kPGroups - 1) / kPGroups;
+  q.ng = (nq + q.g - 1) / q.g;
+  const uint32_t* quart = (const uint32_t*)(a.ws.quart + row * a.nchunk * kPWarps);
+  const int id = (int)threadIdx.x;
+  if (q.g == 1) {
+    q.key[0] = id < nq ? __ldcg(quart + id) : kNone;
+    q.key[1] = id + kPThr < nq ? __ldcg(quart + id + kPThr) : kNone;
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int first = (id + h * kPThr) * q.g;
+      q.key[h] = kNone;
+      for (int i = first; i < min(nq, first + q.g); ++i) q.key[h] = max(q.key[h], __ldcg(quart + i));
+    }
+  }
+  return q;
+}
+
 // The K largest entries of a row, sorted, into t.buf (t.n of them), by a whole block.  `beside` is run
 // by the last warp while the others read.
 template <typename T, int PER, typename F>
-__device__ __forceinline__ void top_search(TopSm& t, const LpArgs& a, const T* z, int head, long long row, F beside) {
+__device__ __forceinline__ void top_search(TopSm& t, const LpArgs& a, const T* z, int head, const Groups& q4, F beside) {
   constexpr int E = Lg<T>::E;
   constexpr int kQuart = 8 * PER;  // 16-byte vectors per quarter segment
   const int K = a.top, tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int nq = 4 * a.nchunk * kPWarps, g = (nq + kPGroups - 1) / kPGroups;  // quarters per group
-  const int ng = (nq + g - 1) / g;
-  const uint32_t* quart = (const uint32_t*)(a.ws.quart + row * a.nchunk * kPWarps);
-  uint32_t key[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int id = tid + h * kPThr;
-    key[h] = kNone;
-    for (int i = id * g; i < min(nq, id * g + g); ++i) key[h] = max(key[h], __ldcg(quart + i));
-  }
+  const int g = q4.g, ng = q4.ng;
+  uint32_t key[2] = {q4.key[0], q4.key[1]};
   if (tid == 0) t.n = t.pieces = 0;
   const bool whole = ng < 2 * K;
   const int len = whole ? (a.V + head + E - 1) / E : g * kQuart;  // vectors per piece of the row
@@ -334,13 +352,12 @@ __device__ __forceinline__ void top_search(TopSm& t, const LpArgs& a, const T* z
     key[0] = orderable(m + 0.f);
     key[1] = kNone;
   }
-  // the largest bound, to 18 bits (sign, exponent, nine of the mantissa), that K maxima reach
+  // the largest bound, to 15 bits (sign, exponent, six of the mantissa), that K threads' maxima reach
+  const uint32_t most = max(key[0], key[1]);
   uint32_t bound = 0u;
-  for (int bit = 31; bit >= 14; --bit) {
+  for (int bit = 31; bit >= 17; --bit) {
     const uint32_t c = bound | (1u << bit);
-    int n = __syncthreads_count(key[0] >= c);
-    if (ng > kPThr) n += __syncthreads_count(key[1] >= c);
-    if (n >= K) bound = c;
+    if (__syncthreads_count(most >= c) >= K) bound = c;
   }
   if (whole) {
     if (tid == 0) t.list[t.pieces++] = 0;
@@ -411,6 +428,8 @@ __device__ __forceinline__ void finish_row(RowSm<TOP>& sm, const LpArgs& a, cons
                                            int x, float zx, float s2) {
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nseg = a.nchunk * kPWarps;
+  Groups q4;
+  if constexpr (TOP) q4 = load_groups(a, row);  // (in flight beside the partial results)
   Part p{-INFINITY, 0.f, 0.f, 0};
   const float4* part = a.ws.part + row * nseg;
   for (int i = tid; i < nseg; i += kPThr) {
@@ -443,7 +462,7 @@ __device__ __forceinline__ void finish_row(RowSm<TOP>& sm, const LpArgs& a, cons
   };
   if constexpr (TOP) {
     TopSm& t = sm.top;
-    top_search<T, PER>(t, a, z, head, row, outputs);
+    top_search<T, PER>(t, a, z, head, q4, outputs);
     if (tid < a.top) {
       const bool has = tid < t.n;
       a.top_ids[row * a.top + tid] = has ? (int32_t)key_token(t.buf[tid]) : -1;
