@@ -57,6 +57,7 @@ __global__ void __launch_bounds__(256) gemm_f32_kernel(int M, int Nn, int K, int
                                                        long long cm, long long cn, long long cshare,
                                                        int accumulate) {
   __shared__ float sa[2][kFK][kFT + 4], sb[2][kFK][kFT + 4];
+  pdl_trigger();
   const int m0 = blockIdx.x * kFT, n0 = blockIdx.y * kFT, tid = threadIdx.x;
   const int ka = blockIdx.z * per, kb = min(K, ka + per);
   const int tx = tid & 15, ty = tid >> 4;
@@ -116,6 +117,9 @@ __global__ void __launch_bounds__(256) gemm_f32_kernel(int M, int Nn, int K, int
         *c = accumulate ? *c + acc[i][j] : acc[i][j];
       }
     }
+  // grad_a's launch runs beside grad_W2's (neither reads what the other writes) but does not end before
+  // it, so that whatever waits for this launch finds both done.
+  pdl_wait();
 }
 
 // ------------------------------------------------------------------ bf16 weights: tensor cores
@@ -741,6 +745,11 @@ cudaError_t plain(int N, int V, int r, const TG* G, const TW* a, const TW* W2, i
   const long long wv = rv ? 1 : r, wj = rv ? V : 1;
   const unsigned nb = (unsigned)((r + kFT - 1) / kFT);
   cudaError_t e = cudaSuccess;
+  if (gW) {
+    gemm_f32_kernel<TG, TW><<<dim3((unsigned)((V + kFT - 1) / kFT), nb), 256, 0, stream>>>(
+        V, r, N, (N + kFK - 1) / kFK * kFK, G, 1, V, a, r, 1, gW, wv, wj, 0, accumulate);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
   if (ga) {
     // shares of at least 64 entries, as many as fill the machine
     const unsigned mb = (unsigned)((N + kFT - 1) / kFT);
@@ -749,20 +758,20 @@ cudaError_t plain(int N, int V, int r, const TG* G, const TW* a, const TW* W2, i
     const int per = ((V + splits - 1) / splits + kFK - 1) / kFK * kFK;
     splits = (V + per - 1) / per;
     float* out = splits > 1 ? part : ga;
-    gemm_f32_kernel<TG, TW><<<dim3(mb, nb, splits), 256, 0, stream>>>(N, r, V, per, G, V, 1, W2, wv, wj, out, r, 1,
-                                                                     (long long)N * r, 0);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const dim3 grid(mb, nb, splits);
+    if (gW)
+      e = launch_pdl(gemm_f32_kernel<TG, TW>, grid, 256, 0, stream, N, r, V, per, G, V, 1, W2, wv, wj, out, r, 1,
+                     (long long)N * r, 0);
+    else
+      gemm_f32_kernel<TG, TW><<<grid, 256, 0, stream>>>(N, r, V, per, G, V, 1, W2, wv, wj, out, r, 1,
+                                                        (long long)N * r, 0);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
     if (splits > 1) {
       const long long quads = (long long)N * r / 4;
-      share_sum_kernel<<<(unsigned)((quads + 63) / 64), 256, 0, stream>>>(quads, splits, (const float4*)part,
-                                                                          (float4*)ga);
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      e = launch_pdl(share_sum_kernel, (unsigned)((quads + 63) / 64), 256, 0, stream, quads, splits,
+                     (const float4*)part, (float4*)ga);
     }
-  }
-  if (gW) {
-    gemm_f32_kernel<TG, TW><<<dim3((unsigned)((V + kFT - 1) / kFT), nb), 256, 0, stream>>>(
-        V, r, N, (N + kFK - 1) / kFK * kFK, G, 1, V, a, r, 1, gW, wv, wj, 0, accumulate);
-    e = cudaGetLastError();
   }
   return e;
 }
