@@ -323,7 +323,7 @@ __global__ void __cluster_dims__(Src<MODE>::kPair ? 2 : 1, 1, 1) __launch_bounds
   }
   __syncthreads();
   if (kPair) cluster_sync_all();  // both CTAs are there
-  if (WANT_A) pdl_trigger();  // (the sum of the shares follows)
+  pdl_trigger();  // (grad_a's launch, or the sum of its shares, may follow)
   if (warp == 1) {
     if (kPair) {
       tc::tmem_alloc_pair(tbase, 512);
@@ -695,6 +695,9 @@ __global__ void __cluster_dims__(Src<MODE>::kPair ? 2 : 1, 1, 1) __launch_bounds
       tc::tmem_dealloc(tmem, 512);
   }
   if (kPair) cluster_sync_all();  // neither CTA ends before both have freed
+  // grad_a's launch starts on the SMs that grad_W2's has left (neither reads what the other writes) but
+  // does not end before it, so that whatever waits for this launch finds both done.
+  if (WANT_A) pdl_wait();
 }
 
 // grad_a from the shares, in their order: four threads per 16 bytes, each a contiguous quarter.
@@ -786,24 +789,27 @@ size_t share_floats(int N, int r, int nsm) {
 }
 
 template <bool WANT_A, int MODE>
-cudaError_t bg_launch(const BgArgs& a, const CUtensorMap& tg, const CUtensorMap& tb, int nsm, cudaStream_t stream) {
+cudaError_t bg_launch(const BgArgs& a, const CUtensorMap& tg, const CUtensorMap& tb, int nsm, bool behind,
+                      cudaStream_t stream) {
   using S = Src<MODE>;
   cudaError_t e = cudaFuncSetAttribute(bias_grad_kernel<WANT_A, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        S::kSmem);
   if (e != cudaSuccess) return e;
   constexpr int kCtas = S::kPair ? 2 : 1;
   const int units = a.items < nsm / kCtas ? a.items : nsm / kCtas;
+  if (behind)
+    return launch_pdl(bias_grad_kernel<WANT_A, MODE>, kCtas * units, S::kThreads, S::kSmem, stream, a, tg, tb);
   bias_grad_kernel<WANT_A, MODE><<<kCtas * units, S::kThreads, S::kSmem, stream>>>(a, tg, tb);
   return cudaGetLastError();
 }
 template <bool WANT_A>
-cudaError_t bg_mode(int mode, const BgArgs& a, const CUtensorMap& tg, const CUtensorMap& tb, int nsm,
+cudaError_t bg_mode(int mode, const BgArgs& a, const CUtensorMap& tg, const CUtensorMap& tb, int nsm, bool behind,
                     cudaStream_t stream) {
   switch (mode) {
-    case 0: return bg_launch<WANT_A, 0>(a, tg, tb, nsm, stream);
-    case 1: return bg_launch<WANT_A, 1>(a, tg, tb, nsm, stream);
-    case 2: return bg_launch<WANT_A, 2>(a, tg, tb, nsm, stream);
-    default: return bg_launch<WANT_A, 3>(a, tg, tb, nsm, stream);
+    case 0: return bg_launch<WANT_A, 0>(a, tg, tb, nsm, behind, stream);
+    case 1: return bg_launch<WANT_A, 1>(a, tg, tb, nsm, behind, stream);
+    case 2: return bg_launch<WANT_A, 2>(a, tg, tb, nsm, behind, stream);
+    default: return bg_launch<WANT_A, 3>(a, tg, tb, nsm, behind, stream);
   }
 }
 
@@ -833,15 +839,17 @@ cudaError_t tensor(int N, int V, int r, int g_bf16, const void* G, const bf16* a
     p.nstage_k = (N + 63) / 64;
     p.out = gW;
     p.wide = ((uintptr_t)gW % 32) == 0;
-    if ((e = bg_mode<false>(mode, p, tg, tb, nsm, stream)) != cudaSuccess) return e;
+    if ((e = bg_mode<false>(mode, p, tg, tb, nsm, false, stream)) != cudaSuccess) return e;
   }
   if (ga) {
     p.b_kmajor = rv;
     const bf16* W = W2;
+    bool behind = gW != nullptr;  // directly behind grad_W2's launch
     if (rv && V % 8 != 0) {  // rows that TMA cannot address: a [V][r] copy in the workspace
       bf16* t = (bf16*)(ws + sizeof(WsHeader) + bg_align(share_floats(N, r, nsm) * 4));
       if ((e = launch_transpose(W2, t, r, V, 2, stream)) != cudaSuccess) return e;
       W = t;
+      behind = false;
       p.b_kmajor = 0;
     }
     if (!(p.b_kmajor ? encode_bf16_2d(&tb, W, r, V, V, 64) : encode_bf16_2d(&tb, W, V, r, r, 64)))
@@ -869,7 +877,7 @@ cudaError_t tensor(int N, int V, int r, int g_bf16, const void* G, const bf16* a
     p.items = base * splits;
     p.out = splits > 1 ? part : ga;
     p.wide = ((uintptr_t)p.out % 32) == 0;
-    if ((e = bg_mode<true>(mode, p, tg, tb, nsm, stream)) != cudaSuccess) return e;
+    if ((e = bg_mode<true>(mode, p, tg, tb, nsm, behind, stream)) != cudaSuccess) return e;
     if (splits > 1) {
       const long long quads = (long long)N * r / 4;
       e = launch_pdl(share_sum_kernel, (unsigned)((quads + 63) / 64), 256, 0, stream, quads, splits,
