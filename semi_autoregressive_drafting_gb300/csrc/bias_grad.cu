@@ -27,7 +27,7 @@
 //
 // 3584 x 262144 x 256 from bf16: 820 us in a row of calls (370 us per product alone; a library bf16
 // product of the same operands 357 and 313; one CTA per item 385 and 400).  G's stream bounds it: with 16
-// columns in place of 256 a product still takes 335 us (5.6 TB/s).  448 x 151936 x 256 from fp32: 207 us,
+// columns in place of 256 a product still takes 335 us (5.6 TB/s).  448 x 151936 x 256 from fp32: 205 us,
 // 94 and 104 per product.  Copies with a step taken out took, of the 95 of grad_a: the split 82, two
 // thirds of the MMAs 88, W2 88, reading the accumulators 89, all of them 50: the chain of the steps bounds
 // it, through shared memory that moves 288 KB per 64-deep stage (2250 cycles of about 2430).  Fences at
@@ -831,6 +831,12 @@ cudaError_t tensor(int N, int V, int r, int g_bf16, const void* G, const bf16* a
   CUtensorMap tg, tb;
   if (mode == 0 && !encode_bf16_2d(&tg, G, N, V, V, 64)) return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
+  const bf16* W = W2;
+  if (ga && rv && V % 8 != 0) {  // rows that TMA cannot address: a [V][r] copy in the workspace
+    bf16* t = (bf16*)(ws + sizeof(WsHeader) + bg_align(share_floats(N, r, nsm) * 4));
+    if ((e = launch_transpose(W2, t, r, V, 2, stream)) != cudaSuccess) return e;
+    W = t;
+  }
   if (gW) {
     if (!encode_bf16_2d(&tb, a, N, r, r, 64)) return cudaErrorInvalidValue;
     if (mode == 1 && !encode_f32_2d(&tg, G, N, V, 128, 32)) return cudaErrorInvalidValue;
@@ -842,16 +848,7 @@ cudaError_t tensor(int N, int V, int r, int g_bf16, const void* G, const bf16* a
     if ((e = bg_mode<false>(mode, p, tg, tb, nsm, false, stream)) != cudaSuccess) return e;
   }
   if (ga) {
-    p.b_kmajor = rv;
-    const bf16* W = W2;
-    bool behind = gW != nullptr;  // directly behind grad_W2's launch
-    if (rv && V % 8 != 0) {  // rows that TMA cannot address: a [V][r] copy in the workspace
-      bf16* t = (bf16*)(ws + sizeof(WsHeader) + bg_align(share_floats(N, r, nsm) * 4));
-      if ((e = launch_transpose(W2, t, r, V, 2, stream)) != cudaSuccess) return e;
-      W = t;
-      behind = false;
-      p.b_kmajor = 0;
-    }
+    p.b_kmajor = rv && W == W2;
     if (!(p.b_kmajor ? encode_bf16_2d(&tb, W, r, V, V, 64) : encode_bf16_2d(&tb, W, V, r, r, 64)))
       return cudaErrorInvalidValue;
     if (mode == 1 && !encode_f32_2d(&tg, G, N, V, 32, 128)) return cudaErrorInvalidValue;
@@ -877,7 +874,7 @@ cudaError_t tensor(int N, int V, int r, int g_bf16, const void* G, const bf16* a
     p.items = base * splits;
     p.out = splits > 1 ? part : ga;
     p.wide = ((uintptr_t)p.out % 32) == 0;
-    if ((e = bg_mode<true>(mode, p, tg, tb, nsm, behind, stream)) != cudaSuccess) return e;
+    if ((e = bg_mode<true>(mode, p, tg, tb, nsm, gW != nullptr, stream)) != cudaSuccess) return e;
     if (splits > 1) {
       const long long quads = (long long)N * r / 4;
       e = launch_pdl(share_sum_kernel, (unsigned)((quads + 63) / 64), 256, 0, stream, quads, splits,
