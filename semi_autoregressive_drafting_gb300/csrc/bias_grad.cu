@@ -164,7 +164,8 @@ __device__ __forceinline__ bool wait_or(uint64_t* bar, uint32_t parity, volatile
 }
 
 // One work item as a CTA sees it: its 128 rows, the K stages, the columns; the columns that the MMA takes
-// (a multiple of 16), and those of them that this CTA brings (half of them in a pair): first, number.
+// (a multiple of 16, in a pair of 32: the MMA of two CTAs takes no others), and those of them that this
+// CTA brings (half of them in a pair): first, number.
 struct Item {
   int m0, k0, k1, c0, cols, split, n, b0, nb;
 };
@@ -175,7 +176,7 @@ __device__ __forceinline__ Item item_of(const BgArgs& a, int i, int rank) {
   i /= a.nrb;
   t.c0 = rb * kBN;
   t.cols = min(kBN, a.r - t.c0);
-  t.n = (t.cols + 15) / 16 * 16;
+  t.n = PAIR ? (t.cols + 31) / 32 * 32 : (t.cols + 15) / 16 * 16;  // (the columns past r are zeros)
   t.nb = PAIR ? t.n / 2 : t.n;
   t.b0 = t.c0 + rank * t.nb;
   if (WANT_A) {
