@@ -195,7 +195,7 @@ __device__ __forceinline__ Part part_shfl(const Part& p, int o) {
 
 struct LpWs {
   WsHeader* hdr;
-  unsigned* count;  // [N] blocks of the row done; zero between calls
+  unsigned* count;  // [kCountRows] blocks of the row done; zero between calls
   float4* part;     // [N][nchunk][8] each segment's Part
   uint4* quart;     // [N][nchunk][8] the largest entries of its quarters, orderable (with alternatives)
 };
@@ -677,6 +677,10 @@ int lp_chunks(int V, int E, int per, bool aligned_rows) {
 // other way round; segments of 4 KB against 2 KB in the largest call 288 and 348 us.
 constexpr int kPerMany = 8, kPerFew = 4;
 constexpr long long kFewBytes = 16ll << 20;
+// Rows that are counted at most: only small calls count, and only rows of more than one chunk, that is of
+// more than kPThr kPerFew - 1 whole groups.  The counters have this room in every workspace, whatever N:
+// what a call of other sizes leaves in the workspace is never in their place.
+constexpr int kCountRows = (int)(kFewBytes / ((kPThr * kPerFew - 1) * 16)) + 1;
 
 template <typename T, bool TOP>
 cudaError_t lp_run(int N, const T* logits, LpArgs a, cudaStream_t stream) {
@@ -707,7 +711,7 @@ size_t lp_slots(int N, int V) {
 
 size_t logprobs_workspace_bytes(int N, int V, int top) {
   const size_t part = lp_align(lp_slots(N, V) * kPWarps * sizeof(float4));
-  return sizeof(WsHeader) + lp_align((size_t)N * sizeof(unsigned)) + (top ? 2 : 1) * part;
+  return sizeof(WsHeader) + lp_align(kCountRows * sizeof(unsigned)) + (top ? 2 : 1) * part;
 }
 
 cudaError_t launch_logprobs(int N, int V, float T, int bf16, const void* logits, long long ld,
@@ -730,7 +734,7 @@ cudaError_t launch_logprobs(int N, int V, float T, int bf16, const void* logits,
   a.ws.hdr = (WsHeader*)w;
   w += sizeof(WsHeader);
   a.ws.count = (unsigned*)w;
-  w += lp_align((size_t)N * sizeof(unsigned));
+  w += lp_align(kCountRows * sizeof(unsigned));
   a.ws.part = (float4*)w;
   a.ws.quart = (uint4*)(w + lp_align(lp_slots(N, V) * kPWarps * sizeof(float4)));
   const __nv_bfloat16* zb = (const __nv_bfloat16*)logits;
