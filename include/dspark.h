@@ -384,8 +384,9 @@ dspark_status dspark_embedding_grad(int N, int V, int D, float scale, dspark_dty
  * dspark_token_logprobs_grad's); a [N][r] and W2 ([V][r] or [r][V], w2_layout) of type wdt; grad_a
  * [N][r] and grad_W2 (W2's layout) fp32, each optional (at least one).  accumulate != 0 adds to
  * grad_W2 (not to grad_a) instead of writing it.  All arrays 16-byte aligned.  Sums in fp32 in a fixed
- * order.  bf16 weights run on the tensor cores (an fp32 G in three bf16 parts, all its 24 bits), fp32
- * weights on the CUDA cores.  workspace: dspark_bias_grad_workspace_bytes(N, V, r, wdt) bytes, 256-byte
+ * order.  bf16 weights run on the tensor cores (an fp32 G in three bf16 parts, all its 24 bits down to
+ * 2^-133), fp32 weights on the CUDA cores.  Infinities and NaN in G give what a plain product gives; an
+ * infinity in bf16 a or W2 makes what it meets of an fp32 G infinite or NaN.  workspace: dspark_bias_grad_workspace_bytes(N, V, r, wdt) bytes, 256-byte
  * aligned, zeroed once; a wait inside the kernel that exceeds about one second sets DSPARK_ERR_TIMEOUT
  * in its status.  One launch per output, one more where grad_a's sum is shared out, and one for W2 as
  * [r][V] in bf16 when V is not a multiple of 8.  Limits: r a multiple of 8 in 8..512, 2 <= V <= 2^24, 0 <= N <= 2^24 (N = 0: zero gradients).

@@ -14,7 +14,8 @@
 // A bf16 G comes by TMA, and a pair of CTAs (cta_group::2) takes an item of 256 rows: each holds 128 of
 // them and half the columns, so that W2 or a reaches each SM's shared memory once per 256 rows of G.
 // An fp32 G enters as three bf16 parts, hi = bf16(G), mid = bf16(G - hi), lo = bf16(G - hi - mid): all
-// 24 bits (two parts measured 2.5e-6 of the result off, an fp32 product 1e-6).  TMA brings it as it
+// 24 bits (two parts measured 2.5e-6 of the result off, an fp32 product 1e-6); where |G| is above bf16's
+// largest number, as parts cut off and not rounded, so that they are finite.  TMA brings it as it
 // lies, and eight warps split it from one shared-memory buffer into another.  A G whose rows TMA
 // cannot address is brought by the same warps: fp32 element by element, bf16 by copied words.  These
 // paths take items of 128 rows, one CTA each (a pair gained nothing there: the signals between its CTAs
@@ -200,7 +201,7 @@ __device__ __forceinline__ float4 load_quad(const TG* p, int n) {
   return make_float4(to_f<TG>(p[0]), n > 1 ? to_f<TG>(p[1]) : 0.f, n > 2 ? to_f<TG>(p[2]) : 0.f,
                      n > 3 ? to_f<TG>(p[3]) : 0.f);
 }
-// bf16 of four values, and what it leaves of them (exactly)
+// bf16 of four values, and what it leaves of them (exactly): numbers up to bf16's largest, NaN
 __device__ __forceinline__ uint2 take_bf16(float4& f) {
   const __nv_bfloat162 a = __floats2bfloat162_rn(f.x, f.y), b = __floats2bfloat162_rn(f.z, f.w);
   uint2 w;
@@ -212,6 +213,22 @@ __device__ __forceinline__ uint2 take_bf16(float4& f) {
   f.w -= __uint_as_float(w.y & 0xFFFF0000u);
   return w;
 }
+// The same of any numbers, by cutting off and not rounding, so that the part of a finite number is finite.
+// An infinity leaves nothing.
+__device__ __forceinline__ float left_of(float x) {
+  const float part = __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
+  return x == part ? 0.f : x - part;
+}
+__device__ __forceinline__ uint2 cut_bf16(float4& f) {
+  const uint2 w = make_uint2(__byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632),
+                             __byte_perm(__float_as_uint(f.z), __float_as_uint(f.w), 0x7632));
+  f = make_float4(left_of(f.x), left_of(f.y), left_of(f.z), left_of(f.w));
+  return w;
+}
+__device__ __forceinline__ float abs_max(const float4& f) {
+  return fmaxf(fmaxf(fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(f.z), fabsf(f.w)));
+}
+constexpr float kBf16Most = 3.3895313892515355e38f;  // bf16's largest finite number
 
 // MODE 0: bf16 G by TMA.  1: fp32 G by TMA, split into three parts.  2: fp32 G element by element.
 // 3: bf16 G element by element (one part).
@@ -655,14 +672,23 @@ __global__ void __cluster_dims__(Src<MODE>::kPair ? 2 : 1, 1, 1) __launch_bounds
           }
         }
         uint8_t* st = smem + (g % S::kStagesA) * S::kStageA;
+        auto split = [&](auto take) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int row = prow + u * kRowStep + (WANT_A ? 0 : 32 * half);
-          const int box = WANT_A ? row >> 6 : pq >> 4, y = row & 63, x = WANT_A ? pq + 8 * half : pq & 15;
-          const uint32_t at = (uint32_t)(box * kBox + y * 128 + (((x >> 1) ^ (y & 7)) << 4) + (x & 1) * 8);
+          for (int u = 0; u < 8; ++u) {
+            const int row = prow + u * kRowStep + (WANT_A ? 0 : 32 * half);
+            const int box = WANT_A ? row >> 6 : pq >> 4, y = row & 63, x = WANT_A ? pq + 8 * half : pq & 15;
+            const uint32_t at = (uint32_t)(box * kBox + y * 128 + (((x >> 1) ^ (y & 7)) << 4) + (x & 1) * 8);
 #pragma unroll
-          for (int h = 0; h < S::kParts; ++h) *(uint2*)(st + h * kTileA + at) = take_bf16(r[u]);
-        }
+            for (int h = 0; h < S::kParts; ++h) *(uint2*)(st + h * kTileA + at) = take(r[u]);
+          }
+        };
+        float most = abs_max(r[0]);
+#pragma unroll
+        for (int u = 1; u < 8; ++u) most = fmaxf(most, abs_max(r[u]));
+        if (most <= kBf16Most)
+          split([](float4& f) { return take_bf16(f); });
+        else
+          split([](float4& f) { return cut_bf16(f); });
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
