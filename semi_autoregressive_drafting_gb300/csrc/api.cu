@@ -101,6 +101,10 @@ bool dev_info(DevInfo* out) {
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+// the kernels scale by 1 / T and by log2(e) / T, the larger one
+bool usable_temperature(float T) {
+  return T > 0.f && std::isfinite(T) && std::isfinite(1.4426950408889634f * (1.f / T));
+}
 
 struct WsLayout {
   size_t keys, hdot, ml, mlt, l1p, rnn_s, rnn_a, rnn_gh, rnn_flag, ybuf, w2t, total;
@@ -518,8 +522,7 @@ dspark_status dspark_token_logprobs(int N, int V, float T, dspark_dtype zdt, con
   if (N < 0 || N > (1 << 24) || V < 2 || V > (1 << 24) || (long long)N * (V / 4096 + 2) >= (1ll << 31))
     return fail(DSPARK_ERR_INVALID, "bad shape N=%d V=%d", N, V);
   if (top < 0 || top > 32 || top > V) return fail(DSPARK_ERR_INVALID, "top must be 0..min(32, V), not %d", top);
-  if (!(T > 0.f) || !std::isfinite(T) || !std::isfinite(1.f / T))
-    return fail(DSPARK_ERR_INVALID, "T must be finite and > 0");
+  if (!usable_temperature(T)) return fail(DSPARK_ERR_INVALID, "T must be finite and log2(e) / T too");
   if (zdt != DSPARK_F32 && zdt != DSPARK_BF16) return fail(DSPARK_ERR_INVALID, "unknown dtype");
   if (ld < V) return fail(DSPARK_ERR_INVALID, "row stride %lld is below V=%d", (long long)ld, V);
   if (!logp && !norm && !entropy && !rank && !top) return fail(DSPARK_ERR_INVALID, "no output requested");
@@ -546,8 +549,7 @@ dspark_status dspark_token_logprobs_grad(int N, int V, float T, dspark_dtype zdt
   g_err.clear();
   if (N < 0 || N > (1 << 24) || V < 2 || V > (1 << 24) || (long long)N * (V / 4096 + 2) >= (1ll << 31))
     return fail(DSPARK_ERR_INVALID, "bad shape N=%d V=%d", N, V);
-  if (!(T > 0.f) || !std::isfinite(T) || !std::isfinite(1.f / T))
-    return fail(DSPARK_ERR_INVALID, "T must be finite and > 0");
+  if (!usable_temperature(T)) return fail(DSPARK_ERR_INVALID, "T must be finite and log2(e) / T too");
   if (zdt != DSPARK_F32 && zdt != DSPARK_BF16) return fail(DSPARK_ERR_INVALID, "unknown dtype");
   if (ld < V || grad_ld < V) return fail(DSPARK_ERR_INVALID, "a row stride is below V=%d", V);
   if (N == 0) return DSPARK_OK;
