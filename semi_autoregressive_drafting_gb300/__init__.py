@@ -345,25 +345,57 @@ class _Plan:
     ``out``.  ``stream`` (a torch stream) overrides the one given at construction.
 
     What a plan allocates (outputs, workspace) belongs to its stream: given ``stream``, it is
-    allocated and cleared there, and the inputs are recorded as in use on it."""
+    allocated and cleared there.  Everything that the call reads or writes, a caller's outputs and
+    workspace among it, is recorded as in use on a stream that was given.  The first run on a stream other
+    than the plan's waits for what the plan's has enqueued so far (the clearing of the workspace); later
+    ones are ordered by the caller, and so is a run that a graph captures."""
 
     def _set(self, name, args, stream, out, keep, device):
-        if stream is not None:
-            for t in keep:
-                if isinstance(t, torch.Tensor):
-                    t.record_stream(stream)
         self._fn = getattr(_lib.load(), name)
         self._where = name
-        self._args = (*args, _stream(stream, device))
+        self._stream = stream if stream is not None else torch.cuda.current_stream(device)
+        self._args = (*args, self._stream.cuda_stream)
+        self._others = {}   # streams of other runs, by handle
         self.out = out
-        self._keep = keep   # every tensor whose address is baked into the arguments stays alive
+        self._keep = (keep, out)   # everything whose address is baked into the arguments stays alive
+        if stream is not None:
+            self._record(stream)
+
+    def _record(self, stream):
+        for t in _tensors(self._keep):
+            t.record_stream(stream)
+
+    def _elsewhere(self, stream):
+        with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return
+        stream.wait_stream(self._stream)
+        self._record(stream)
+        self._others[stream.cuda_stream] = stream
 
     def run(self, stream=None):
-        args = self._args if stream is None else self._args[:-1] + (stream.cuda_stream,)
+        args = self._args
+        if stream is not None and stream.cuda_stream != args[-1]:
+            if stream.cuda_stream not in self._others:
+                self._elsewhere(stream)
+            args = args[:-1] + (stream.cuda_stream,)
         code = self._fn(*args)
         if code != 0:
             _lib.check(code, self._where)
         return self.out
+
+
+def _tensors(items):
+    """The tensors of nested tuples, workspaces and outputs."""
+    for x in items:
+        if isinstance(x, torch.Tensor):
+            yield x
+        elif isinstance(x, Workspace):
+            yield x.buf
+        elif isinstance(x, tuple):
+            yield from _tensors(x)
+        elif isinstance(x, LogprobOutput):
+            yield from _tensors(vars(x).values())
 
 
 def _on(stream):

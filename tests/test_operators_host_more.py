@@ -24,3 +24,64 @@ def test_temperature_whose_scale_overflows(lib, T, ok):
     want = 0 if ok else 1
     assert lib.dspark_token_logprobs(0, 100, T, 0, P, 100, P, 2, P, P, P, P, P, P, P, BIG, None) == want
     assert lib.dspark_token_logprobs_grad(0, 100, T, 0, P, 100, P, P, P, P, P, P, 100, None) == want
+
+
+class _Stream:
+    def __init__(self, handle):
+        self.cuda_stream, self.waits = handle, []
+
+    def wait_stream(self, other):
+        self.waits.append(other.cuda_stream)
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    """Recorded uses of tensors by stream, with stand-ins for the streams themselves."""
+    from contextlib import nullcontext
+    uses = []
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: uses.append((t.data_ptr(), s.cuda_stream)))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: nullcontext())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    return uses
+
+
+def _plan(stream):
+    """A plan as the constructors leave it: an input, a caller's workspace, a caller's output."""
+    x, y, z = torch.zeros(4), torch.zeros(5), torch.zeros(6)
+    ws = ds.Workspace.__new__(ds.Workspace)
+    ws.buf, ws.nbytes = torch.zeros(256, dtype=torch.uint8), 256
+    out = ds.LogprobOutput(y, z, y, y, None, None)
+    plan = ds._Plan()
+    plan._set("dspark_embedding", (0,), stream, out, (x, ws), torch.device("cpu"))
+    calls = []
+    plan._fn = lambda *a: calls.append(a) or 0
+    return plan, calls, {t.data_ptr() for t in (x, y, z, ws.buf)}
+
+
+def test_what_a_plan_uses_is_recorded_on_its_stream(lib, streams):
+    plan, _, used = _plan(_Stream(7))
+    assert {p for p, s in streams if s == 7} == used
+
+
+def test_a_run_on_another_stream_follows_the_plans_and_is_recorded(lib, streams):
+    own, other = _Stream(7), _Stream(9)
+    plan, calls, used = _plan(own)
+    plan.run()
+    plan.run(own)
+    assert not own.waits and [c[-1] for c in calls] == [7, 7]
+    plan.run(other)
+    plan.run(other)
+    assert [c[-1] for c in calls] == [7, 7, 9, 9]
+    assert other.waits == [7]                       # the workspace was cleared on the plan's stream
+    assert {p for p, s in streams if s == 9} == used
+
+
+def test_a_captured_run_waits_for_nothing_outside_the_graph(lib, streams, monkeypatch):
+    plan, calls, _ = _plan(_Stream(7))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    other = _Stream(9)
+    plan.run(other)
+    assert not other.waits and calls[-1][-1] == 9
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    plan.run(other)
+    assert other.waits == [7]
