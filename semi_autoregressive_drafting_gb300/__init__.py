@@ -353,6 +353,7 @@ class _Plan:
     def _set(self, name, args, stream, out, keep, device):
         self._fn = getattr(_lib.load(), name)
         self._where = name
+        self._index = device.index
         self._stream = stream if stream is not None else torch.cuda.current_stream(device)
         self._args = (*args, self._stream.cuda_stream)
         self._others = {}   # streams of other runs, by handle
@@ -374,6 +375,7 @@ class _Plan:
         self._others[stream.cuda_stream] = stream
 
     def run(self, stream=None):
+        _check_current(self._index)
         args = self._args
         if stream is not None and stream.cuda_stream != args[-1]:
             if stream.cuda_stream not in self._others:
@@ -404,16 +406,26 @@ def _on(stream):
 
 
 def _same_device(*tensors):
+    """The device of all these tensors (and workspaces), which is the current one: the library
+    launches there."""
     dev = None
     for t in tensors:
         if t is None:
             continue
+        if isinstance(t, Workspace):
+            t = t.buf
         if not t.is_cuda:
             raise ValueError("libdspark takes device tensors")
         if dev is not None and t.device != dev:
             raise ValueError("all tensors are on one device")
         dev = t.device
+    _check_current(dev.index)
     return dev
+
+
+def _check_current(index):
+    if torch.cuda.current_device() != index:
+        raise ValueError(f"the tensors are on cuda:{index}, which is not the current device")
 
 
 def _ints(t, shape, name):
@@ -490,7 +502,7 @@ class LogprobPlan(_Plan):
     """``token_logprobs`` with its arguments marshalled once (see ``_Plan``)."""
 
     def __init__(self, logits, tokens, *, T=1.0, top=0, workspace=None, stream=None, out=None):
-        dev = _same_device(logits, tokens)
+        dev = _same_device(logits, tokens, workspace)
         zdt = _dtype_code(logits)
         lead, N, V, ld, zp = _logit_rows(logits, "logits")
         if not 0 <= top <= min(32, V):
@@ -528,10 +540,10 @@ class LogprobGradPlan(_Plan):
 
     def __init__(self, logits, tokens, norm, *, T=1.0, grad_logp=None, grad_entropy=None, entropy=None,
                  stream=None, out=None):
+        dev = _same_device(logits, tokens, norm, entropy, grad_logp, grad_entropy, out)
         if out is None:
             with _on(stream):
-                out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-        dev = _same_device(logits, tokens, norm, entropy, grad_logp, grad_entropy, out)
+                out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
         zdt = _dtype_code(logits)
         lead, N, V, ld, zp = _logit_rows(logits, "logits")
         if out.dtype != logits.dtype or out.shape != logits.shape:
@@ -597,7 +609,7 @@ class EmbeddingGradPlan(_Plan):
 
     def __init__(self, grad, tokens, V, *, scale=1.0, dtype=torch.float32, accumulate=False, out=None,
                  workspace=None, stream=None):
-        dev = _same_device(grad, tokens, out)
+        dev = _same_device(grad, tokens, out, workspace)
         lead, D = tuple(tokens.shape), grad.shape[-1]
         if tuple(grad.shape) != (*lead, D):
             raise ValueError("grad must be [..., D] for tokens [...]")
@@ -641,7 +653,7 @@ class BiasGradPlan(_Plan):
 
     def __init__(self, grad_logits, a, W2, *, w2_layout="vr", accumulate=False, out=None, workspace=None,
                  stream=None):
-        dev = _same_device(grad_logits, a, W2)
+        dev = _same_device(grad_logits, a, W2, workspace)
         V, r = grad_logits.shape[-1], a.shape[-1]
         lead = tuple(grad_logits.shape[:-1])
         w2c = _w2_code(w2_layout)
