@@ -429,6 +429,8 @@ def _check_current(index):
 
 
 def _ints(t, shape, name):
+    if t is None:
+        raise ValueError(f"{name} is required")
     if t.dtype != torch.int32:
         raise TypeError(f"{name} is int32")
     if tuple(t.shape) != tuple(shape):
@@ -512,7 +514,7 @@ class LogprobPlan(_Plan):
             ws = workspace or LogprobWorkspace(N, V, top, device=dev)
             if out is None:
                 def new(*shape, dtype=torch.float32):
-                    return torch.empty(*lead, *shape, dtype=dtype, device=dev)
+                    return torch.empty((*lead, *shape), dtype=dtype, device=dev)
                 out = LogprobOutput(new(), new(2), new(), new(dtype=torch.int32),
                                     new(top, dtype=torch.int32) if top else None, new(top) if top else None)
         _same_device(logits, out.logp, out.norm, out.entropy, out.rank, out.top_ids, out.top_logp)
