@@ -324,8 +324,9 @@ dspark_status dspark_markov_draft_noalloc(int B, int gamma, int V, int r, int d,
  * -inf; positions past the last alternative hold -1 and -inf.  A row that is -inf everywhere has
  * norm (-inf, 0), entropy 0 and logp -inf.  NaN or +inf logits make their row's norm[1], logp and
  * entropy NaN; NaN entries are not alternatives and count in no rank.  Sums run in a fixed order: the
- * same inputs give the same bits.  Limits: T > 0 with T and log2(e) / T finite, 0 <= N <= 2^24 (N = 0
- * does nothing), 2 <= V <= 2^24, N (V / 4096 + 2) < 2^31.  One launch for up to 16 MB of logits, else two.
+ * same row, at the same place within 16 bytes, gives the same bits in calls of any N.  Limits: T > 0 with
+ * T and log2(e) / T finite, 0 <= N <= 2^24 (N = 0 does nothing), 2 <= V <= 2^24,
+ * N (V / 4096 + 2) < 2^31.  One launch for up to 16 MB of logits, else two.
  */
 size_t dspark_token_logprobs_workspace_bytes(int N, int V, int top);
 dspark_status dspark_token_logprobs(int N, int V, float T, dspark_dtype zdt, const void* logits, int64_t ld,

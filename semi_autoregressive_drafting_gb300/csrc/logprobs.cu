@@ -10,11 +10,12 @@
 // The maximum is subtracted before the scale is applied: a row whose entries are all the type's
 // lowest number is a uniform row, not an overflow.
 //
-// Forward, one read of the logits: a warp takes a 16-byte-aligned segment of a row (4 KB; 1 KB in
-// small calls), holds it in registers (all loads issued at once), forms the maximum, then the sums
-// relative to it, and leaves them as one partial result.  A block per row merges the row's partial
-// results in their order: in large calls a second launch, so that a segment's warp ends with its
-// store; in small ones the row's last block to finish (a counter per row, no waits).
+// Forward, one read of the logits: a warp (two in small calls) takes a 16-byte-aligned segment of a row
+// (4 KB), holds it in registers (all loads issued at once), forms the maximum, then the sums relative to
+// it, and leaves them as one partial result.  A block per row merges the row's partial results in their
+// order: in large calls a second launch, so that a segment's warp ends with its store; in small ones the
+// row's last block to finish (a counter per row, no waits).  One warp or two add a segment's halves in the
+// same order: a row has the same bits in calls of any number of rows.
 // Alternatives: the warps also leave the largest entry of each quarter of their segments.  The K-th
 // largest entry is no less than the K-th largest of these maxima.  So the block that merges the row
 // finds a bound just below that (of groups of quarters in long rows), re-reads the quarters that reach
@@ -30,6 +31,8 @@
 #include "common.cuh"
 #include "kernels.h"
 
+#include <type_traits>
+
 namespace dspark {
 namespace {
 
@@ -38,6 +41,7 @@ constexpr int kPWarps = kPThr / 32;
 constexpr float kPL2e = 1.4426950408889634f;
 constexpr float kPLn2 = 0.6931471805599453f;
 constexpr int kPGroups = 2 * kPThr;  // groups of quarter segments ranked at most (two per thread)
+constexpr int kSegment = 8;     // 16-byte loads per lane of a segment (4 KB)
 constexpr int kPKeep = 256;     // candidates kept before a cut to the K best
 constexpr int kPBuf = kPKeep + kPThr * 8;
 static_assert(kPBuf % kPThr == 0 && kPBuf / kPThr * 32 <= 2 * kPThr, "what a first cut leaves: two per thread");
@@ -178,9 +182,9 @@ __device__ __forceinline__ void part_merge(Part& a, const Part& b, float s2) {
   const float da = a.m == -INFINITY ? -256.f : fmaxf((a.m - m) * s2, -256.f);
   const float db = b.m == -INFINITY ? -256.f : fmaxf((b.m - m) * s2, -256.f);
   const float wa = ex2p(da), wb = ex2p(db);
-  const float S = a.S * wa + b.S * wb;
-  a.A = fmaf(a.S, da, a.A) * wa + fmaf(b.S, db, b.A) * wb;
-  a.S = S;
+  // (fused as written, so that every kernel rounds alike; an empty side changes nothing)
+  a.A = fmaf(fmaf(a.S, da, a.A), wa, __fmul_rn(fmaf(b.S, db, b.A), wb));
+  a.S = fmaf(a.S, wa, __fmul_rn(b.S, wb));
   a.m = m;
   a.c += b.c;
 }
@@ -193,11 +197,18 @@ __device__ __forceinline__ Part part_shfl(const Part& p, int o) {
   return q;
 }
 
+// What the warps that share a segment tell one another: maxima and counts, the second one's sums.
+struct PairSm {
+  float m[kPWarps];
+  int c[kPWarps];
+  float S[kPWarps / 2][32], A[kPWarps / 2][32];
+};
+
 struct LpWs {
   WsHeader* hdr;
   unsigned* count;  // [kCountRows] blocks of the row done; zero between calls
-  float4* part;     // [N][nchunk][8] each segment's Part
-  uint4* quart;     // [N][nchunk][8] the largest entries of its quarters, orderable (with alternatives)
+  float4* part;     // [N][nchunk][segments of a chunk] each segment's Part
+  uint4* quart;     // [N][nchunk][8] the largest entries of a warp's quarters, orderable (with alternatives)
 };
 
 struct LpArgs {
@@ -427,7 +438,7 @@ template <typename T, int PER, bool TOP>
 __device__ __forceinline__ void finish_row(RowSm<TOP>& sm, const LpArgs& a, const T* z, int head, long long row,
                                            int x, float zx, float s2) {
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int nseg = a.nchunk * kPWarps;
+  const int nseg = a.nchunk * (kPWarps * PER / kSegment);
   Groups q4;
   if constexpr (TOP) q4 = load_groups(a, row);  // (in flight beside the partial results)
   Part p{-INFINITY, 0.f, 0.f, 0};
@@ -480,9 +491,10 @@ __device__ __forceinline__ float token_logit(const LpArgs& a, const T* z, int x)
   return x >= 0 && x < a.V ? to_f<T>(z[x]) : INFINITY;
 }
 
-// ONE: the row's last block also merges it (small calls).
+// ONE: the row's last block also merges it (small calls).  Large calls keep five blocks per SM: with four,
+// at 52 registers, the largest call took 294 us, against 287.
 template <typename T, int PER, bool TOP, bool ONE>
-__global__ void __launch_bounds__(kPThr) logprob_kernel(const T* __restrict__ logits, const LpArgs a) {
+__global__ void __launch_bounds__(kPThr, ONE ? 0 : 5) logprob_kernel(const T* __restrict__ logits, const LpArgs a) {
   constexpr int E = Lg<T>::E;
   if constexpr (!ONE) pdl_trigger();
   const long long row = blockIdx.x / (unsigned)a.nchunk;
@@ -521,30 +533,71 @@ __global__ void __launch_bounds__(kPThr) logprob_kernel(const T* __restrict__ lo
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) p.m = fmaxf(p.m, __shfl_xor_sync(0xffffffffu, p.m, o));
   }
-  const float mu = p.m == -INFINITY ? 0.f : p.m;
-  const F2 nm = f2(-mu, -mu), ss = f2(s2, s2);
-  F2 S = f2(0.f, 0.f), A = S;
-#pragma unroll
-  for (int u = 0; u < PER; ++u)
-#pragma unroll
-    for (int e = 0; e < E / 2; ++e) {
-      float2 y = un2(mul2(add2(Lg<T>::pair(q[u], e), nm), ss));
-      // 2^y is zero from -150 down: -inf becomes a finite factor of a zero.  (A NaN passes through
-      // the exponential, not through this maximum.)
-      const F2 ex = f2(ex2p(y.x), ex2p(y.y));
-      S = add2(S, ex);
-      A = fma2(ex, f2(fmaxf(y.x, -256.f), fmaxf(y.y, -256.f)), A);
-    }
-  const float2 S1 = un2(S), A1 = un2(A);
-  p.S = warp_sum(S1.x + S1.y);
-  p.A = warp_sum(A1.x + A1.y);
   typename Lg<T>::Cnt cnt = Lg<T>::zero();
   const typename Lg<T>::Thr thr = Lg<T>::thr(zx);
+  constexpr bool kPaired = PER < kSegment;  // two warps share a segment
+  __shared__ typename std::conditional<kPaired, PairSm, int>::type pair;
+  if constexpr (kPaired) {
 #pragma unroll
-  for (int u = 0; u < PER; ++u) Lg<T>::above(cnt, q[u], thr);
-  p.c = __reduce_add_sync(0xffffffffu, Lg<T>::total(cnt));
-  if (lane == 0)
-    a.ws.part[(row * a.nchunk + ch) * kPWarps + warp] = make_float4(p.m, p.S, p.A, __int_as_float(p.c));
+    for (int u = 0; u < PER; ++u) Lg<T>::above(cnt, q[u], thr);
+    p.c = __reduce_add_sync(0xffffffffu, Lg<T>::total(cnt));
+    if (lane == 0) {
+      pair.m[warp] = p.m;
+      pair.c[warp] = p.c;
+    }
+    __syncthreads();
+    p.m = fmaxf(p.m, pair.m[warp ^ 1]);
+    p.c += pair.c[warp ^ 1];
+  }
+  const float mu = p.m == -INFINITY ? 0.f : p.m;
+  const F2 nm = f2(-mu, -mu), ss = f2(s2, s2);
+  // S and A of vectors u0 to u0 + 3
+  auto sums = [&](int u0, float& s, float& a1) {
+    F2 S = f2(0.f, 0.f), A = S;
+#pragma unroll
+    for (int u = 0; u < kSegment / 2; ++u)
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) {
+        float2 y = un2(mul2(add2(Lg<T>::pair(q[u0 + u], e), nm), ss));
+        // 2^y is zero from -150 down: -inf becomes a finite factor of a zero.  (A NaN passes through
+        // the exponential, not through this maximum.)
+        const F2 ex = f2(ex2p(y.x), ex2p(y.y));
+        S = add2(S, ex);
+        A = fma2(ex, f2(fmaxf(y.x, -256.f), fmaxf(y.y, -256.f)), A);
+      }
+    const float2 S1 = un2(S), A1 = un2(A);
+    s = S1.x + S1.y;
+    a1 = A1.x + A1.y;
+  };
+  sums(0, p.S, p.A);
+  if constexpr (kPaired) {
+    if (warp & 1) {
+      pair.S[warp >> 1][lane] = p.S;
+      pair.A[warp >> 1][lane] = p.A;
+    }
+    __syncthreads();
+    if (!(warp & 1)) {
+      p.S += pair.S[warp >> 1][lane];
+      p.A += pair.A[warp >> 1][lane];
+    }
+  } else {
+    float S, A;
+    sums(kSegment / 2, S, A);
+    p.S += S;
+    p.A += A;
+  }
+  if (!kPaired || !(warp & 1)) {
+    p.S = warp_sum(p.S);
+    p.A = warp_sum(p.A);
+    if constexpr (!kPaired) {
+#pragma unroll
+      for (int u = 0; u < PER; ++u) Lg<T>::above(cnt, q[u], thr);
+      p.c = __reduce_add_sync(0xffffffffu, Lg<T>::total(cnt));
+    }
+    if (lane == 0)
+      a.ws.part[(row * a.nchunk + ch) * (kPWarps * PER / kSegment) + warp * PER / kSegment] =
+          make_float4(p.m, p.S, p.A, __int_as_float(p.c));
+  }
   if constexpr (ONE) {
     __shared__ __align__(16) RowSm<TOP> sm;
     __shared__ int s_last;
@@ -671,11 +724,12 @@ int lp_chunks(int V, int E, int per, bool aligned_rows) {
   return (groups + kPThr * per - 1) / (kPThr * per);
 }
 
-// Sixteen-byte loads per thread: small problems take short segments, so that every SM has some, and
-// one launch.
-// Measured: 16 MB of fp32 rows 8.4 us this way and 10.4 us the other, 64 MB with 20 alternatives the
-// other way round; segments of 4 KB against 2 KB in the largest call 288 and 348 us.
-constexpr int kPerMany = 8, kPerFew = 4;
+// Sixteen-byte loads per thread.  Small calls take one launch (measured: 16 MB of fp32 rows 8.4 us this way
+// and 10.4 us the other, 64 MB with 20 alternatives the other way round).  They give a segment to two warps
+// where whole chunks would be fewer than the SMs (8 x 151936 bf16 rows 4.3 us, against 5.1 with one warp)
+// or a row fits in half a chunk; else to one (77 x 50021 fp32 rows, 8 alternatives: 11.6 us against 12.7).
+constexpr int kPerMany = kSegment, kPerFew = kSegment / 2;
+constexpr int kFill = 152;  // chunks for every SM
 constexpr long long kFewBytes = 16ll << 20;
 // Rows that are counted at most: only small calls count, and only rows of more than one chunk, that is of
 // more than kPThr kPerFew - 1 whole groups.  The counters have this room in every workspace, whatever N:
@@ -687,6 +741,11 @@ cudaError_t lp_run(int N, const T* logits, LpArgs a, cudaStream_t stream) {
   constexpr int E = Lg<T>::E;
   const bool al = ((uintptr_t)logits % 16) == 0 && (a.ld * (long long)sizeof(T)) % 16 == 0;
   if ((long long)N * a.V * (long long)sizeof(T) <= kFewBytes) {
+    a.nchunk = lp_chunks(a.V, E, kPerMany, al);
+    if (lp_chunks(a.V, E, kPerFew, al) > 1 && (long long)N * a.nchunk >= kFill) {
+      logprob_kernel<T, kPerMany, TOP, true><<<(unsigned)N * (unsigned)a.nchunk, kPThr, 0, stream>>>(logits, a);
+      return cudaGetLastError();
+    }
     a.nchunk = lp_chunks(a.V, E, kPerFew, al);
     logprob_kernel<T, kPerFew, TOP, true><<<(unsigned)N * (unsigned)a.nchunk, kPThr, 0, stream>>>(logits, a);
     return cudaGetLastError();
