@@ -636,8 +636,13 @@ dspark_status dspark_bias_grad(int N, int V, int r, dspark_dtype gdt, const void
   const size_t need = bias_grad_workspace_bytes(N, V, r, wdt == DSPARK_BF16, di.sms);
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < need)
     return fail(DSPARK_ERR_WORKSPACE, "workspace must be 256-byte aligned and >= %zu bytes", need);
+  // Failure-path test hook, as for the draft kernels: DSPARK_TEST_STUCK_WAIT = mbar | mma makes a wait of
+  // the warps that read the accumulators, or of the thread that issues the MMAs, run out after 20 us.
+  int stuck = 0;
+  if (const char* f = std::getenv("DSPARK_TEST_STUCK_WAIT"))
+    stuck = !std::strcmp(f, "mbar") ? 1 : !std::strcmp(f, "mma") ? 2 : 0;
   cudaError_t e = launch_bias_grad(N, V, r, gdt == DSPARK_BF16, G, wdt == DSPARK_BF16, a, W2,
-                                   w2_layout == DSPARK_W2_RV, grad_a, grad_W2, accumulate != 0, workspace,
+                                   w2_layout == DSPARK_W2_RV, grad_a, grad_W2, accumulate != 0, stuck, workspace,
                                    di.sms, (cudaStream_t)stream);
   return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, "bias gradient launch");
 }

@@ -130,6 +130,7 @@ constexpr int kBN = 256;              // columns of a work item
 constexpr int kMaxItems = 2;          // work items per CTA or pair at most when the vocabulary is shared out
 constexpr int kRawBytes = 128 * 32 * 4;  // half a stage of an fp32 G as it lies
 constexpr int kWordBytes = 2 * 16 * 128 * 4;  // a half stage's words of G, those of unaligned rows twice
+constexpr unsigned long long kStuckNs = 20000, kSettleNs = 1000000;
 constexpr int kDeep = 4;              // half stages of words in flight per group of four warps
 // Registers per thread where eight more warps bring G (640 threads, launched with 96 each): the
 // three shares, 128 x (48 + 2 x 160 + 2 x 56), are the launch's 640 x 96.
@@ -145,19 +146,30 @@ struct BgArgs {
   int out_rv;           // grad_W2 is [r][V]
   int accumulate;
   int wide;             // out is 32-byte aligned
+  int stuck;            // failure-path test hook: a wait of the sums (1) or of the MMA thread (2) runs out
   float* out;           // grad_W2, or grad_a's shares [split][N][r]
   const void* G;
   unsigned* status;
 };
 
-// A bounded wait of one thread that also ends when another role of the block gave up.
-__device__ __forceinline__ bool wait_or(uint64_t* bar, uint32_t parity, volatile int* stop) {
+// How a block gives up: a flag that its roles look at while they wait, and in a pair the other CTA's flag.
+struct Stop {
+  volatile int* mine;
+  uint32_t other;  // shared::cluster address, 0 without a pair
+};
+__device__ __forceinline__ void give_up(Stop stop) {
+  *stop.mine = 1;
+  if (stop.other) asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(stop.other), "r"(1) : "memory");
+}
+// A bounded wait of one thread that also ends when another role of the block, or of the pair, gave up.
+__device__ __forceinline__ bool wait_or(uint64_t* bar, uint32_t parity, Stop stop,
+                                        unsigned long long limit_ns = kWaitLimitNs) {
   if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = globaltimer();
   while (!mbar_try_wait_sleep(bar, parity, kSuspendHintNs)) {
-    if (*stop) return false;
-    if (globaltimer() - t0 > kWaitLimitNs) {
-      *stop = 1;
+    if (*stop.mine) return false;
+    if (globaltimer() - t0 > limit_ns) {
+      give_up(stop);
       return false;
     }
   }
@@ -313,10 +325,11 @@ __global__ void __cluster_dims__(Src<MODE>::kPair ? 2 : 1, 1, 1) __launch_bounds
   uint64_t* rfull = tfree + 2;
   uint64_t* rempty = rfull + kRaw;
   uint32_t* tbase = (uint32_t*)(rempty + kRaw);
-  volatile int* stop = (volatile int*)(tbase + 1);
-  static_assert((2 * kSA + 2 * kSB + 4 + 2 * kRaw) * 8 + 8 <= 512, "barriers fit");
+  uint64_t* never = (uint64_t*)(tbase + 2);  // nothing arrives here
+  static_assert((2 * kSA + 2 * kSB + 4 + 2 * kRaw) * 8 + 16 <= 512, "barriers fit");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = kPair ? (int)cluster_rank() : 0;
+  const Stop stop{(volatile int*)(tbase + 1), kPair ? cluster_addr(tbase + 1, rank ^ 1) : 0u};
   const int pair = (int)blockIdx.x >> (kPair ? 1 : 0), pairs = (int)gridDim.x >> (kPair ? 1 : 0);
 
   if (tid == 0) {
@@ -336,7 +349,8 @@ __global__ void __cluster_dims__(Src<MODE>::kPair ? 2 : 1, 1, 1) __launch_bounds
       mbar_init(&rfull[i], 1);
       mbar_init(&rempty[i], 4);
     }
-    *stop = 0;
+    mbar_init(never, 1);
+    *stop.mine = 0;
     fence_mbar_init();
   }
   __syncthreads();
@@ -388,7 +402,7 @@ __global__ void __cluster_dims__(Src<MODE>::kPair ? 2 : 1, 1, 1) __launch_bounds
       if (!ok) atomicMax(a.status, kErrTimeout);
       // every copy lands before the pair ends (the phase of each slot's last use)
       if (rank == 0)
-        for (int j = max(0, g - kSB); j < g; ++j) mbar_wait(&bfull[j % kSB], (uint32_t)((j / kSB) & 1));
+        for (int j = max(0, g - kSB); j < g && mbar_wait(&bfull[j % kSB], (uint32_t)((j / kSB) & 1)); ++j) {}
     } else if ((S::kTma || S::kTmaRaw) && warp == 2 && lane == 0) {  // ---- TMA: G
       const uint64_t once = policy_evict_first();
       constexpr int kS = S::kTma ? kSA : kRaw;
@@ -420,8 +434,8 @@ __global__ void __cluster_dims__(Src<MODE>::kPair ? 2 : 1, 1, 1) __launch_bounds
       }
       if (!ok) atomicMax(a.status, kErrTimeout);
       if (!S::kTma || rank == 0)
-        for (int j = max(0, g - kS); j < g; ++j)
-          mbar_wait(S::kTma ? &afull[j % kS] : &rfull[j % kS], (uint32_t)((j / kS) & 1));
+        for (int j = max(0, g - kS);
+             j < g && mbar_wait(S::kTma ? &afull[j % kS] : &rfull[j % kS], (uint32_t)((j / kS) & 1)); ++j) {}
     } else if (warp == 1 && lane == 0 && rank == 0) {  // ---- MMA, for both CTAs
       auto commit = [](uint64_t* bar) {
         if (kPair)
@@ -430,7 +444,7 @@ __global__ void __cluster_dims__(Src<MODE>::kPair ? 2 : 1, 1, 1) __launch_bounds
           tc::mma_commit(bar);
       };
       int g = 0, n = 0;  // stages and runs so far
-      bool ok = true;
+      bool ok = a.stuck != 2 || wait_or(never, 0, stop, kStuckNs);
       for (int i = pair; ok && i < a.items; i += pairs) {
         const Item t = item_of<WANT_A, kPair>(a, i, 0);
         const uint32_t idesc = tc::idesc_bf16_f32(S::kBM, t.n) | (WANT_A ? 0u : tc::kIdescAMajorMN) |
@@ -489,10 +503,11 @@ __global__ void __cluster_dims__(Src<MODE>::kPair ? 2 : 1, 1, 1) __launch_bounds
       }
       if (!ok) {
         atomicMax(a.status, kErrTimeout);
-        // what was issued completes before TMEM is freed
         commit(&done[n & 1]);
-        mbar_wait(&done[n & 1], (uint32_t)((n / 2) & 1));
+        ++n;
       }
+      // what was issued completes before TMEM is freed, whether or not anything else waits for it
+      if (n > 0) mbar_wait(&done[(n - 1) & 1], (uint32_t)(((n - 1) / 2) & 1));
     }
     __syncwarp();
   } else if (warp < 12) {  // ---- accumulators to the sums, sums to global memory
@@ -501,6 +516,11 @@ __global__ void __cluster_dims__(Src<MODE>::kPair ? 2 : 1, 1, 1) __launch_bounds
     const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + c_lo;
     int n = 0;
     bool ok = true;
+    if (a.stuck == 1) {
+      if (lane == 0 && !wait_or(never, 0, stop, kStuckNs)) atomicMax(a.status, kErrTimeout);
+      __syncwarp();
+      ok = false;
+    }
     for (int i = pair; ok && i < a.items; i += pairs) {
       const Item t = item_of<WANT_A, kPair>(a, i, rank);
       float x[kBN / 2];
@@ -700,7 +720,7 @@ __global__ void __cluster_dims__(Src<MODE>::kPair ? 2 : 1, 1, 1) __launch_bounds
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (tid == 0 && !*stop) {
+  if (tid == 0 && !*stop.mine) {
     // The MMAs' signals that the last stages have been read are not waited for above, and in a pair come
     // from the other CTA too: they arrive before this block ends, or they would find another's shared
     // memory in its place.  (The phases before each slot's last use were waited for.)
@@ -709,11 +729,17 @@ __global__ void __cluster_dims__(Src<MODE>::kPair ? 2 : 1, 1, 1) __launch_bounds
       const Item t = item_of<WANT_A, kPair>(a, i, rank);
       g += t.k1 - t.k0;
     }
-    for (int j = max(0, g - kSB); j < g; ++j) mbar_wait(&bempty[j % kSB], (uint32_t)((j / kSB) & 1));
+    for (int j = max(0, g - kSB); j < g && mbar_wait(&bempty[j % kSB], (uint32_t)((j / kSB) & 1)); ++j) {}
     g *= S::kHalves;
-    for (int j = max(0, g - kSA); j < g; ++j) mbar_wait(&aempty[j % kSA], (uint32_t)((j / kSA) & 1));
+    for (int j = max(0, g - kSA); j < g && mbar_wait(&aempty[j % kSA], (uint32_t)((j / kSA) & 1)); ++j) {}
   }
   if (kPair) cluster_sync_all();  // the other CTA no longer reads this one's shared memory or arrives here
+  if (tid == 0 && *stop.mine) {
+    // Given up: the roles have stopped at different stages, and copies and signals of stages that only
+    // some of them reached are waited for by none.  They arrive within microseconds.
+    const unsigned long long t0 = globaltimer();
+    while (globaltimer() - t0 < kSettleNs) __nanosleep(1000);
+  }
   if (warp == 1) {
     tc::fence_after_sync();
     if (kPair)
@@ -841,7 +867,8 @@ cudaError_t bg_mode(int mode, const BgArgs& a, const CUtensorMap& tg, const CUte
 }
 
 cudaError_t tensor(int N, int V, int r, int g_bf16, const void* G, const bf16* a, const bf16* W2, int rv,
-                   float* ga, float* gW, int accumulate, uint8_t* ws, int nsm, cudaStream_t stream) {
+                   float* ga, float* gW, int accumulate, int stuck, uint8_t* ws, int nsm,
+                   cudaStream_t stream) {
   const int mode = g_bf16 ? (V % 8 == 0 ? 0 : 3) : (V % 4 == 0 ? 1 : 2);
   const int bm = mode == 0 ? 256 : 128;  // rows of a work item: a pair's or a CTA's
   float* part = (float*)(ws + sizeof(WsHeader));
@@ -852,6 +879,7 @@ cudaError_t tensor(int N, int V, int r, int g_bf16, const void* G, const bf16* a
   p.nrb = (r + kBN - 1) / kBN;
   p.accumulate = accumulate;
   p.out_rv = rv;
+  p.stuck = stuck;
   p.G = G;
   p.status = &((WsHeader*)ws)->status;
   p.nmb = p.per_split = p.b_kmajor = 0;
@@ -927,7 +955,7 @@ size_t bias_grad_workspace_bytes(int N, int V, int r, int w_bf16, int nsm) {
 
 cudaError_t launch_bias_grad(int N, int V, int r, int g_bf16, const void* G, int w_bf16, const void* a,
                              const void* W2, int w2_rv, float* grad_a, float* grad_W2, int accumulate,
-                             void* workspace, int nsm, cudaStream_t stream) {
+                             int stuck, void* workspace, int nsm, cudaStream_t stream) {
   if (N == 0) {  // no rows: grad_a is empty and grad_W2 zero
     if (!grad_W2 || accumulate) return cudaSuccess;
     zero_kernel<<<4 * nsm, 256, 0, stream>>>((long long)V * r / 4, (float4*)grad_W2);
@@ -935,7 +963,7 @@ cudaError_t launch_bias_grad(int N, int V, int r, int g_bf16, const void* G, int
   }
   if (w_bf16)
     return tensor(N, V, r, g_bf16, G, (const bf16*)a, (const bf16*)W2, w2_rv, grad_a, grad_W2, accumulate,
-                  (uint8_t*)workspace, nsm, stream);
+                  stuck, (uint8_t*)workspace, nsm, stream);
   float* part = (float*)((uint8_t*)workspace + sizeof(WsHeader));
   if (g_bf16)
     return plain(N, V, r, (const bf16*)G, (const float*)a, (const float*)W2, w2_rv, grad_a, grad_W2, accumulate, part,

@@ -46,6 +46,6 @@ cudaError_t launch_embedding_grad(int N, int V, int D, float scale, int g_bf16, 
 size_t bias_grad_workspace_bytes(int N, int V, int r, int w_bf16, int nsm);
 cudaError_t launch_bias_grad(int N, int V, int r, int g_bf16, const void* G, int w_bf16, const void* a,
                              const void* W2, int w2_rv, float* grad_a, float* grad_W2, int accumulate,
-                             void* workspace, int nsm, cudaStream_t stream);
+                             int stuck, void* workspace, int nsm, cudaStream_t stream);
 
 }  // namespace dspark
