@@ -207,11 +207,9 @@ __device__ __forceinline__ Item item_of(const BgArgs& a, int i, int rank) {
 }
 
 // Four consecutive elements of a row of G, zero from `n` on.
-template <typename TG>
-__device__ __forceinline__ float4 load_quad(const TG* p, int n) {
+__device__ __forceinline__ float4 load_quad(const float* p, int n) {
   if (n <= 0) return make_float4(0.f, 0.f, 0.f, 0.f);
-  return make_float4(to_f<TG>(p[0]), n > 1 ? to_f<TG>(p[1]) : 0.f, n > 2 ? to_f<TG>(p[2]) : 0.f,
-                     n > 3 ? to_f<TG>(p[3]) : 0.f);
+  return make_float4(p[0], n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f, n > 3 ? p[3] : 0.f);
 }
 // bf16 of four values, and what it leaves of them (exactly): numbers up to bf16's largest, NaN
 __device__ __forceinline__ uint2 take_bf16(float4& f) {
@@ -264,7 +262,6 @@ struct Src {
   static constexpr int kOffB = kStagesA * kStageA, kOffRaw = kOffB + kStagesB * kTileB,
                        kOffBar = kOffRaw + (MODE == 3 ? 2 * kDeep * kWordBytes : kRaw * kRawBytes);
   static constexpr int kSmem = kOffBar + 512 + 1024;
-  using T = typename std::conditional<MODE == 3, bf16, float>::type;
   // The two groups of warps take alternate half stages: with an even number of slots a slot is always
   // the same group's, which has then seen every phase of its barriers before the one it waits for.
   static_assert(kTma || (kSlotsA % 2 == 0 && kRaw % 2 == 0), "a slot belongs to one group");
@@ -558,8 +555,6 @@ __global__ void __cluster_dims__(Src<MODE>::kPair ? 2 : 1, 1, 1) __launch_bounds
     }
   } else if (!S::kTma) {  // ---- G into its parts
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsBring));
-    using TG = typename S::T;
-    const TG* G = (const TG*)a.G;
     // Two groups of four warps take alternate half stages, so that one group's waits and fences pass
     // beside the other's work.  A thread's eight quads of a half: grad_a: 128 rows of 8 quads (the rows
     // of a warp are four apart in pairs: their swizzled stores meet all banks); grad_W2: 32 rows of 32.
@@ -663,57 +658,58 @@ __global__ void __cluster_dims__(Src<MODE>::kPair ? 2 : 1, 1, 1) __launch_bounds
         ++g;
       }
       asm volatile("cp.async.wait_group 0;" ::: "memory");
-    } else
-    for (int i = pair; ok && i < a.items; i += pairs) {
-      const Item t = item_of<WANT_A, kPair>(a, i, rank);
-      for (int s = t.k0; s < t.k1; ++s, ++g) {
-        const int ga = 2 * g + half, slot = ga % kSA;
-        if (lane == 0) {
-          if (S::kTmaRaw) ok = wait_or(&rfull[ga % kRaw], (uint32_t)((ga / kRaw) & 1), stop);
-          if (ok && ga >= kSA) ok = wait_or(&aempty[slot], (uint32_t)((ga / kSA - 1) & 1), stop);
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) {
-          if (lane == 0) atomicMax(a.status, kErrTimeout);
-          break;
-        }
-        float4 r[8];
-        if (S::kTmaRaw) {
-          const float4* in = (const float4*)(raw + (ga % kRaw) * kRawBytes) + prow * kRowQuads + pq;
-#pragma unroll
-          for (int u = 0; u < 8; ++u) r[u] = in[u * kRowStep * kRowQuads];
-        } else {
-          const int row0 = (WANT_A ? t.m0 : s * 64 + 32 * half) + prow;
-          const int col = (WANT_A ? s * 64 + 32 * half : t.m0) + 4 * pq, n = a.V - col;
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int row = row0 + u * kRowStep;
-            r[u] = load_quad<TG>(G + (long long)row * a.V + col, row < a.N ? n : 0);
+    } else {
+      for (int i = pair; ok && i < a.items; i += pairs) {
+        const Item t = item_of<WANT_A, kPair>(a, i, rank);
+        for (int s = t.k0; s < t.k1; ++s, ++g) {
+          const int ga = 2 * g + half, slot = ga % kSA;
+          if (lane == 0) {
+            if (S::kTmaRaw) ok = wait_or(&rfull[ga % kRaw], (uint32_t)((ga / kRaw) & 1), stop);
+            if (ok && ga >= kSA) ok = wait_or(&aempty[slot], (uint32_t)((ga / kSA - 1) & 1), stop);
           }
-        }
-        uint8_t* st = smem + (g % S::kStagesA) * S::kStageA;
-        auto split = [&](auto take) {
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int row = prow + u * kRowStep + (WANT_A ? 0 : 32 * half);
-            const int box = WANT_A ? row >> 6 : pq >> 4, y = row & 63, x = WANT_A ? pq + 8 * half : pq & 15;
-            const uint32_t at = (uint32_t)(box * kBox + y * 128 + (((x >> 1) ^ (y & 7)) << 4) + (x & 1) * 8);
-#pragma unroll
-            for (int h = 0; h < S::kParts; ++h) *(uint2*)(st + h * kTileA + at) = take(r[u]);
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) {
+            if (lane == 0) atomicMax(a.status, kErrTimeout);
+            break;
           }
-        };
-        float most = abs_max(r[0]);
+          float4 r[8];
+          if (S::kTmaRaw) {
+            const float4* in = (const float4*)(raw + (ga % kRaw) * kRawBytes) + prow * kRowQuads + pq;
 #pragma unroll
-        for (int u = 1; u < 8; ++u) most = fmaxf(most, abs_max(r[u]));
-        if (most <= kBf16Most)
-          split([](float4& f) { return take_bf16(f); });
-        else
-          split([](float4& f) { return cut_bf16(f); });
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (S::kTmaRaw) mbar_arrive(&rempty[ga % kRaw]);
-          mbar_arrive(&afull[slot]);
+            for (int u = 0; u < 8; ++u) r[u] = in[u * kRowStep * kRowQuads];
+          } else {
+            const int row0 = (WANT_A ? t.m0 : s * 64 + 32 * half) + prow;
+            const int col = (WANT_A ? s * 64 + 32 * half : t.m0) + 4 * pq, n = a.V - col;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const int row = row0 + u * kRowStep;
+              r[u] = load_quad((const float*)a.G + (long long)row * a.V + col, row < a.N ? n : 0);
+            }
+          }
+          uint8_t* st = smem + (g % S::kStagesA) * S::kStageA;
+          auto split = [&](auto take) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const int row = prow + u * kRowStep + (WANT_A ? 0 : 32 * half);
+              const int box = WANT_A ? row >> 6 : pq >> 4, y = row & 63, x = WANT_A ? pq + 8 * half : pq & 15;
+              const uint32_t at = (uint32_t)(box * kBox + y * 128 + (((x >> 1) ^ (y & 7)) << 4) + (x & 1) * 8);
+#pragma unroll
+              for (int h = 0; h < S::kParts; ++h) *(uint2*)(st + h * kTileA + at) = take(r[u]);
+            }
+          };
+          float most = abs_max(r[0]);
+#pragma unroll
+          for (int u = 1; u < 8; ++u) most = fmaxf(most, abs_max(r[u]));
+          if (most <= kBf16Most)
+            split([](float4& f) { return take_bf16(f); });
+          else
+            split([](float4& f) { return cut_bf16(f); });
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (S::kTmaRaw) mbar_arrive(&rempty[ga % kRaw]);
+            mbar_arrive(&afull[slot]);
+          }
         }
       }
     }

@@ -269,13 +269,8 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* tmap, in
       "l"(tmap), "r"(x), "r"(y), "r"(bar), "l"(policy)
       : "memory");
 }
-// arrival at a barrier of another CTA of the cluster, or of this one (a shared::cluster address).  It
-// releases what this CTA's threads wrote at CTA scope: writes to their own shared memory that a
-// proxy fence has already made visible to the tensor cores of this SM.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// the same without ordering earlier memory accesses before it (TMEM reads are ordered by their own fence)
+// arrival at a barrier of another CTA of the cluster, or of this one (a shared::cluster address), without
+// ordering earlier memory accesses before it (TMEM reads are ordered by their own fence)
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
