@@ -321,8 +321,9 @@ dspark_status dspark_markov_draft_noalloc(int B, int gamma, int V, int r, int d,
  *   workspace  dspark_token_logprobs_workspace_bytes(N, V, top) bytes, 256-byte aligned, zeroed once
  *              before the first call; every call leaves it ready for the next
  * Masked entries are -inf (or the type's lowest number): p = 0.  They are never alternatives when
- * -inf; positions past the last alternative hold -1 and -inf.  A row that is -inf everywhere has
- * norm (-inf, 0), entropy 0 and logp -inf.  NaN or +inf logits make their row's norm[1], logp and
+ * -inf; positions past the last alternative hold -1 and -inf.  Exponentials below 2^-126 count as zero in
+ * the sums and in the gradient.  A row that is -inf everywhere has norm (-inf, 0), entropy 0 and logp
+ * -inf.  NaN or +inf logits make their row's norm[1], logp and
  * entropy NaN; NaN entries are not alternatives and count in no rank.  Sums run in a fixed order: the
  * same row, at the same place within 16 bytes, gives the same bits in calls of any N.  Limits: T > 0 with
  * T and log2(e) / T finite, 0 <= N <= 2^24 (N = 0 does nothing), 2 <= V <= 2^24,
@@ -367,8 +368,9 @@ dspark_status dspark_embedding(int N, int V, int D, float scale, dspark_dtype wd
  * every sum in fp32 and in an order that depends on the tokens alone (the same inputs give the same
  * bits).  grad [N][D] of type gdt, grad_W [V][D] of type odt (rounded
  * once).  accumulate = 0 writes every row (zero for tokens that do not occur); otherwise the sums are
- * added to grad_W and other rows are neither read nor written.  tokens[i] = -1 adds nothing; another
- * token outside [0, V) adds nothing and sets DSPARK_ERR_INVALID in the workspace status.
+ * added to grad_W and other rows are neither read nor written; where grad_W is fp32, numbers below 2^-126
+ * in magnitude count as zero in that addition.  tokens[i] = -1 adds nothing; another token outside [0, V)
+ * adds nothing and sets DSPARK_ERR_INVALID in the workspace status.
  * workspace: dspark_embedding_grad_workspace_bytes(N, V, D) bytes, 256-byte aligned, zeroed once; it
  * serves any V and fewer tokens and columns too.  Limits as above.  Two launches up to 4096 tokens, one
  * with none, else two and one per 9 bits of V (and one to clear counts from 2^18 entries on).

@@ -17,7 +17,8 @@
 // 24 bits (two parts measured 2.5e-6 of the result off, an fp32 product 1e-6); where |G| is above bf16's
 // largest number, as parts cut off and not rounded, so that they are finite.  TMA brings it as it
 // lies, and eight warps split it from one shared-memory buffer into another.  A G whose rows TMA
-// cannot address is brought by the same warps: fp32 element by element, bf16 by copied words.  These
+// cannot address is brought by the same warps: fp32 element by element, bf16 by copied words (3584 x 262143
+// x 256 2.7 ms, three and a half times the aligned size).  These
 // paths take items of 128 rows, one CTA each (a pair gained nothing there: the signals between its CTAs
 // cost what the halved operand saved).
 //
@@ -28,12 +29,13 @@
 //
 // 3584 x 262144 x 256 from bf16: 820 us in a row of calls (370 us per product alone; a library bf16
 // product of the same operands 357 and 313; one CTA per item 385 and 400).  G's stream bounds it: with 16
-// columns in place of 256 a product still takes 335 us (5.6 TB/s).  448 x 151936 x 256 from fp32: 205 us,
-// 94 and 104 per product.  Copies with a step taken out took, of the 95 of grad_a: the split 82, two
+// columns in place of 256 a product still takes 335 us (5.6 TB/s).  448 x 151936 x 256 from fp32: 207 us,
+// 95 and 105 per product.  Copies with a step taken out took, of the 95 of grad_a: the split 82, two
 // thirds of the MMAs 88, W2 88, reading the accumulators 89, all of them 50: the chain of the steps bounds
 // it, through shared memory that moves 288 KB per 64-deep stage (2250 cycles of about 2430).  Fences at
 // cluster scope in a pair's signals had cost 60 us.
-// fp32 weights (small heads): CUDA-core tiles.
+// fp32 weights (small heads): CUDA-core tiles, 22 to 26 TFLOP/s (256 x 8192 x 128 50 us, 448 x 151936 x 256
+// 2.7 ms, twice a library fp32 product).
 #include <cuda.h>
 
 #include "draft.cuh"

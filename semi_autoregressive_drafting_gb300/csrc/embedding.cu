@@ -13,11 +13,12 @@
 // an fp32 partial sum, and the last of them to arrive (a counter per run and columns, no waits) adds
 // those up in their order.
 //
-// Bound by HBM once the table is large: 448 tokens x 256 over 151936 rows of fp32 take 26.7 us (the 156 MB
-// written, 0.86 of a copy's rate; 5 us are the sort), 32768 bf16 rows of 2560 into 1.56 GB 272 us (0.94).
+// Bound by HBM once the table is large: 448 tokens x 256 over 151936 rows of fp32 take 26.4 us (the 156 MB
+// written, 0.87 of a copy's rate; about 5 us are the sort), 32768 bf16 rows of 2560 into 1.56 GB 272 us (0.94).
 // The join in the sum launch replaced a launch of its own that took 27 us in the second case; 16-byte
-// stores two apart, half a sector each, had made the zeroing take 390 us.  The lookup of 32768 rows of
-// 4096 bf16 takes 64 us (5.8 TB/s).
+// stores two apart, half a sector each, had made the zeroing take 390 us.  Over a small table the launches
+// of the sort and the chain behind them bound it: 8192 x 256 fp32 over 10000 rows 26 us, of which the bytes
+// need 3.  The lookup of 32768 rows of 4096 bf16 takes 64 us (5.8 TB/s), of 4095, element by element, 171.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -410,7 +411,8 @@ struct SumArgs {
 };
 
 // A finished row.  Added to the output, it is added by the memory (fp32), so that no warp waits for what
-// is there; each element gets one addition, so its order is not in question.
+// is there (448 tokens x 64: 12.4 us, 18.6 by load and store); each element gets one addition, so its order
+// is not in question.  The memory's additions take subnormal numbers, and leave them, as zero.
 template <int E>
 __device__ __forceinline__ void add_out(float* o, const float* f) {
   if (E == 1) {

@@ -22,12 +22,13 @@
 // it, mostly from L2, and sorts the entries that do; no lists are kept during the pass.  A row of fewer
 // than 2 K quarters, whose maxima say little, is read whole, with the threads' own maxima in their place.
 //
-// Bound by HBM once the rows are many: 3584 x 262144 bf16 rows take 285 us (6.6 TB/s, 0.97 of a copy's
+// Bound by HBM once the rows are many: 3584 x 262144 bf16 rows take 287 us (6.5 TB/s, 0.97 of a copy's
 // rate), the fp32 gradient of 448 x 151936 rows 82 us (6.7 TB/s).  With the merge in the pass itself
 // the first took 340 us: a block that waits for its fence and counter holds registers that loads could
 // use.  512 x 151936 fp32 rows with 20 alternatives take 60 us, 50 of them the pass; ranking the segments
 // by all pairs instead of the counted bound cost 13 us more.  Small calls are a chain of latencies (launch,
-// loads, fence and counter, bound, quarters, sort): 8 x 151936 bf16 rows 6.3 us, 10.3 with 5 alternatives.
+// loads, fence and counter, bound, quarters, sort): 8 x 151936 bf16 rows with 5 alternatives 10.2 us in a
+// row of calls; in a graph 8.2, and 4.3 without alternatives.
 #include "common.cuh"
 #include "kernels.h"
 
