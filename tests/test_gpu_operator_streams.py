@@ -6,7 +6,7 @@ import torch
 import semi_autoregressive_drafting_gb300 as ds
 
 pytestmark = pytest.mark.gpu
-PAUSE = 100_000_000    # cycles: some 50 ms
+PAUSE = 400_000_000    # cycles: some 200 ms
 
 
 def test_memory_of_a_pending_call_is_not_reused():
