@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kThr) verify_part_kernel(const float* __restri
       if (y > m) {
         l = l * ex2v(m - y) + 1.f;
         m = y;
-      } else {
+      } else if (y != -INFINITY) {  // (a masked entry adds nothing, also in front of the first other one)
         l += ex2v(y - m);
       }
     }
