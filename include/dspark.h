@@ -401,6 +401,104 @@ dspark_status dspark_bias_grad(int N, int V, int r, dspark_dtype gdt, const void
                                void* stream);
 
 /*
+ * What a request asks of its logits before they are verified, sampled or trained on: penalties for tokens
+ * that its text holds already, biases, and a grammar's mask.  Row (b, k) of the logits is position k of
+ * request b's block (R = gamma + 1 rows for dspark_verify's target logits, R = 1 for a single token).  Its
+ * text is history[b][0 .. lengths[b]), the first prompt_lengths[b] tokens of it the prompt and the others
+ * generated, and then the generated tokens drafted[b][0 .. k).  With seen = whether the text holds v, c =
+ * how often its generated part does:
+ *   y = z / repetition[b] if z > 0 else z repetition[b], where seen;
+ *   y = y - frequency[b] c - presence[b] [c > 0];   y = y + (the sum of the biases of v, in their order);
+ *   out = y where the mask allows v, -inf elsewhere (whatever the logit is, NaN too).
+ * Arguments (device pointers, row-major, caller-owned):
+ *   logits      B R rows of V elements of type zdt, `ld` elements apart; aligned to their type only
+ *   history     [B][H] int32, rows history_ld >= H apart; H = 0: none.  -1: no token.  lengths [B] int32 or
+ *               NULL (H each), prompt_lengths [B] int32 or NULL (0: all generated)
+ *   drafted     [B][R - 1] int32, -1 for no token, or NULL
+ *   repetition, presence, frequency  [B] fp32, each NULL for none (1, 0, 0).  Where a request's are 1, 0
+ *               and 0 its text is not read
+ *   bias_tokens, bias  [B][nb] int32 and fp32, -1 for no entry; a token may have several; nb = 0: none
+ *   mask        M rows of bits, mask_ld >= ceil(V / 32) words apart: bit v mod 32 of word v / 32 set allows v;
+ *               NULL: none.  mask_rows [B][R] int32 gives each row's, -1 for none; NULL: row i of the mask for
+ *               row i of the logits
+ *   out         B R rows of type odt, out_ld apart, rounded once.  It may be the logits themselves (same
+ *               type and stride): then only what changes is written.  Rows that no mask, penalty or bias
+ *               touches keep their bits when the types are equal
+ * A row whose mask allows nothing is -inf everywhere.  A token outside [-1, V), in what is read, and a length
+ * outside [0, H] or a prompt length outside [0, lengths[b]] make their request's rows NaN, a mask row outside
+ * [-1, M) its row (no status word; no workspace needed).  Limits: B R <= 2^24 (B = 0 does nothing), 1 <= R <=
+ * 32, 2 <= V <= 2^24, B (V / 1024 + 1) < 2^31, H <= 2^24, nb <= 2^16.  One launch.
+ */
+dspark_status dspark_process_logits(int B, int R, int V, dspark_dtype zdt, const void* logits, int64_t ld,
+                                    const int32_t* history, int64_t history_ld, int H, const int32_t* lengths,
+                                    const int32_t* prompt_lengths, const int32_t* drafted, const float* repetition,
+                                    const float* presence, const float* frequency, int nb,
+                                    const int32_t* bias_tokens, const float* bias, const uint32_t* mask,
+                                    int64_t mask_ld, int M, const int32_t* mask_rows, dspark_dtype odt, void* out,
+                                    int64_t out_ld, void* stream);
+
+/*
+ * Gradient of dspark_process_logits' out with respect to the logits:
+ *   out[i][v] = grad[i][v] (1 / repetition[b] if z > 0 else repetition[b], where seen), 0 where masked.
+ * grad: rows of type gdt; logits: the raw ones (read where a text holds their token; NULL without
+ * repetition); out: rows of the logits' type zdt.  out may be grad itself (same type and stride), and does
+ * not overlap the logits.  All else as above.
+ */
+dspark_status dspark_process_logits_grad(int B, int R, int V, dspark_dtype gdt, const void* grad, int64_t grad_ld,
+                                         dspark_dtype zdt, const void* logits, int64_t ld, const int32_t* history,
+                                         int64_t history_ld, int H, const int32_t* lengths,
+                                         const int32_t* prompt_lengths, const int32_t* drafted,
+                                         const float* repetition, const uint32_t* mask, int64_t mask_ld, int M,
+                                         const int32_t* mask_rows, void* out, int64_t out_ld, void* stream);
+
+/*
+ * Distillation from a teacher's K largest log probabilities (dspark_token_logprobs' top_ids and top_logp on
+ * the target's logits): what dspark_draft_loss is to whole target rows.  For row i with student p =
+ * softmax(z / T), the teacher's tokens S = {teacher_ids[i][j]}, q_j = exp(teacher_logp[i][j]), the rest's
+ * q_r = max(0, 1 - sum_j q_j) and p_r = sum of p outside S:
+ *   KL = sum_j q_j (ln q_j - ln p_j) + [rest] q_r (ln q_r - ln p_r)      (0 ln 0 = 0)
+ *   L1 = sum_j |p_j - q_j| + [rest] |p_r - q_r|                          (Eq 10 on these outcomes)
+ *   loss[i] = weight[i] (alpha_kl KL + alpha_l1 L1),   parts[i] = (KL, L1),
+ *   norm[i] = (m, ln sum_v exp((z_v - m) / T), m_r, ln sum_{v not in S} exp((z_v - m_r) / T)),
+ * m and m_r the largest logits of the row and outside S.  rest != 0 counts everything else as one outcome;
+ * rest = 0 leaves it out.  grad_logits is the loss's gradient with respect to z (sign(0) = 0 in L1's).
+ *   logits      rows of V elements of type zdt, `ld` elements apart, aligned to their type only
+ *   teacher_ids [N][K] int32, in any order, -1 for no entry; teacher_logp [N][K] fp32, at the teacher's
+ *               own temperature.  Another id outside [0, V), or an id twice in a row: that row's outputs are
+ *               NaN and DSPARK_ERR_INVALID in the workspace status
+ *   weight      [N] fp32 or NULL (1 each): e.g. Eq 9's position weights over the number of rows.  A row of
+ *               weight 0 (padding) is not read: all its outputs are 0
+ *   outputs     loss [N], parts [N][2], norm [N][4] (16-byte aligned) fp32 and grad_logits, rows of type zdt,
+ *               grad_ld apart; each optional, at least one.  grad_logits may be the logits themselves (same
+ *               stride)
+ *   workspace   dspark_distill_workspace_bytes(N, V, K) bytes, 256-byte aligned, zeroed once before the first
+ *               call; it serves smaller calls too
+ * Masked logits are -inf: p = 0.  A teacher's token that the student masks makes KL +inf; the gradient is
+ * the formula's.  A row that is -inf everywhere has p = 0 throughout and norm (-inf, 0, -inf, 0).  NaN or
+ * +inf logits make their row's outputs NaN (but the maxima).  The outcomes are formed in 64 bits from sums
+ * in 32; sums run in a fixed order.  Limits: T > 0 with T and log2(e) / T finite, finite weights of the
+ * parts, 0 <= N <= 2^24 (N = 0 does nothing), 2 <= V <= 2^24, 1 <= K <= min(128, V),
+ * N (V / 4096 + 2) < 2^31.
+ */
+size_t dspark_distill_workspace_bytes(int N, int V, int K);
+dspark_status dspark_distill_loss(int N, int V, float T, dspark_dtype zdt, const void* logits, int64_t ld, int K,
+                                  const int32_t* teacher_ids, const float* teacher_logp, const float* weight,
+                                  float alpha_kl, float alpha_l1, int rest, float* loss, float* parts, float* norm,
+                                  void* grad_logits, int64_t grad_ld, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/*
+ * The gradient alone, from an earlier call's norm: grad_logits for grad_loss [N] fp32 in weight's place, so
+ * that weights known after the forward pass (a mean over a batch, a scaler) need no second forward pass.
+ * All else as above.
+ */
+dspark_status dspark_distill_grad(int N, int V, float T, dspark_dtype zdt, const void* logits, int64_t ld, int K,
+                                  const int32_t* teacher_ids, const float* teacher_logp, const float* norm,
+                                  const float* grad_loss, float alpha_kl, float alpha_l1, int rest,
+                                  void* grad_logits, int64_t grad_ld, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/*
  * Synchronises `stream`, returns the device status word of `workspace` (the most severe error
  * any draft call recorded since the last read, DSPARK_OK if none) and resets the workspace so
  * the next call starts clean.  DSPARK_ERR_CUDA if the synchronisation itself fails.

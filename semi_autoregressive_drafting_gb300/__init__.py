@@ -14,7 +14,10 @@ h (hidden states [B][gamma][d]), x0 (anchors [B]).
 Beside the draft block: ``token_logprobs`` scores given tokens (log probability, entropy, rank,
 alternatives), ``embedding`` looks rows of a table up, and ``token_logprobs_grad``, ``bias_grad`` and
 ``embedding_grad`` are the gradients that lead from a likelihood back to W1 and W2
-(``examples/train_markov_head.py`` runs them together).  Each has a ``...Plan`` that checks and
+(``examples/train_markov_head.py`` runs them together).  ``process_logits`` applies a request's penalties,
+biases and grammar mask to its logits, before ``verify`` or any of these, and ``process_logits_grad`` leads
+back through it; ``distill_loss`` and ``distill_grad`` train on a teacher's K largest log probabilities, which
+``token_logprobs`` gives, where ``draft_loss`` takes whole target rows.  Each has a ``...Plan`` that checks and
 marshals its arguments once.
 """
 from __future__ import annotations
@@ -33,7 +36,9 @@ __all__ = ["Workspace", "markov_draft", "rnn_draft", "confidence", "tv_label",
            "LogprobWorkspace", "LogprobOutput", "LogprobPlan", "token_logprobs",
            "LogprobGradPlan", "token_logprobs_grad", "EmbeddingPlan", "embedding",
            "EmbeddingGradWorkspace", "EmbeddingGradPlan", "embedding_grad",
-           "BiasGradWorkspace", "BiasGradPlan", "bias_grad"]
+           "BiasGradWorkspace", "BiasGradPlan", "bias_grad",
+           "ProcessPlan", "process_logits", "ProcessGradPlan", "process_logits_grad",
+           "DistillWorkspace", "DistillOutput", "DistillPlan", "distill_loss", "DistillGradPlan", "distill_grad"]
 
 _F32, _BF16 = 0, 1
 _W2_LAYOUT = {"vr": 0, "rv": 1}
@@ -396,7 +401,7 @@ def _tensors(items):
             yield x.buf
         elif isinstance(x, tuple):
             yield from _tensors(x)
-        elif isinstance(x, LogprobOutput):
+        elif isinstance(x, (LogprobOutput, DistillOutput)):
             yield from _tensors(vars(x).values())
 
 
@@ -689,6 +694,248 @@ def bias_grad(grad_logits, a, W2, *, w2_layout="vr", accumulate=False, out=None,
     grad_W2 in W2's layout), fp32; ``accumulate`` adds to ``out[1]``.  See ``dspark_bias_grad``."""
     return BiasGradPlan(grad_logits, a, W2, w2_layout=w2_layout, accumulate=accumulate, out=out,
                         workspace=workspace, stream=stream).run()
+
+
+def _history(history, B):
+    """(address, row stride, H) of histories [B, H]: the tokens of a row are consecutive."""
+    if history is None:
+        return None, 0, 0
+    if history.dtype != torch.int32:
+        raise TypeError("history is int32")
+    if history.dim() != 2 or history.shape[0] != B:
+        raise ValueError(f"history must be [{B}, H], not {list(history.shape)}")
+    H = history.shape[1]
+    if H == 0 or B == 0:
+        return None, H, 0
+    ld = history.stride(0) if B > 1 else H
+    if (H > 1 and history.stride(1) != 1) or ld < H:
+        raise ValueError("the tokens of a row of history are consecutive, and its rows do not overlap")
+    return history.data_ptr(), ld, H
+
+
+def _mask(mask, mask_rows, lead, V):
+    """(address, row stride, rows, address of the rows' choice) of a mask [M, words] int32."""
+    if mask is None:
+        if mask_rows is not None:
+            raise ValueError("mask_rows needs mask")
+        return None, 0, 0, None
+    if mask.dtype != torch.int32:
+        raise TypeError("mask is int32: 32 entries a word")
+    if mask.dim() != 2 or mask.shape[1] < (V + 31) // 32:
+        raise ValueError(f"mask must be [M, >= {(V + 31) // 32}], not {list(mask.shape)}")
+    M = mask.shape[0]
+    ld = mask.stride(0) if M > 1 else mask.shape[1]
+    if (mask.shape[1] > 1 and mask.stride(1) != 1) or ld < mask.shape[1]:
+        raise ValueError("the words of a row of mask are consecutive, and its rows do not overlap")
+    N = 1
+    for n in lead:
+        N *= n
+    if mask_rows is None and M != N:
+        raise ValueError(f"mask needs a row for each of {N} rows, or mask_rows")
+    return mask.data_ptr(), ld, M, _ints(mask_rows, lead, "mask_rows") if mask_rows is not None else None
+
+
+def _block(logits, name):
+    """(leading shape, B, R, V, row stride, address) of logits [B, V] or [B, R, V]."""
+    if logits.dim() not in (2, 3):
+        raise ValueError(f"{name} must be [B, V] or [B, R, V]")
+    lead, _, V, ld, p = _logit_rows(logits, name)
+    return lead, lead[0], lead[1] if len(lead) == 2 else 1, V, ld, p
+
+
+def _requests(B, R, lengths, prompt_lengths, drafted, history):
+    if history is None and (lengths is not None or prompt_lengths is not None):
+        raise ValueError("lengths and prompt_lengths need history")
+    return (_ints(lengths, (B,), "lengths") if lengths is not None else None,
+            _ints(prompt_lengths, (B,), "prompt_lengths") if prompt_lengths is not None else None,
+            _ints(drafted, (B, R - 1), "drafted") if drafted is not None else None)
+
+
+class ProcessPlan(_Plan):
+    """``process_logits`` with its arguments marshalled once (see ``_Plan``)."""
+
+    def __init__(self, logits, *, history=None, lengths=None, prompt_lengths=None, drafted=None, repetition=None,
+                 presence=None, frequency=None, bias_tokens=None, bias=None, mask=None, mask_rows=None, dtype=None,
+                 stream=None, out=None):
+        keep = (logits, history, lengths, prompt_lengths, drafted, repetition, presence, frequency, bias_tokens,
+                bias, mask, mask_rows)
+        dev = _same_device(*keep, out)
+        zdt = _dtype_code(logits)
+        lead, B, R, V, ld, zp = _block(logits, "logits")
+        if out is None:
+            with _on(stream):
+                out = torch.empty(logits.shape, dtype=dtype or logits.dtype, device=dev)
+        elif out.shape != logits.shape or (dtype is not None and out.dtype != dtype):
+            raise ValueError("out has the logits' shape, and the requested dtype")
+        odt = _dtype_code(out)
+        _, _, _, old, op = _logit_rows(out, "out")
+        if (bias_tokens is None) != (bias is None):
+            raise ValueError("bias_tokens and bias go together")
+        nb = bias.shape[-1] if bias is not None else 0
+        hp, hld, H = _history(history, B)
+        mp, mld, M, rows = _mask(mask, mask_rows, lead, V)
+        args = (B, R, V, zdt, zp, ld, hp, hld, H, *_requests(B, R, lengths, prompt_lengths, drafted, history),
+                _f32(repetition, (B,), "repetition"), _f32(presence, (B,), "presence"),
+                _f32(frequency, (B,), "frequency"), nb,
+                _ints(bias_tokens, (B, nb), "bias_tokens") if nb else None, _f32(bias, (B, nb), "bias"),
+                mp, mld, M, rows, odt, op, old)
+        self._set("dspark_process_logits", args, stream, out, keep, dev)
+
+
+def process_logits(logits, *, history=None, lengths=None, prompt_lengths=None, drafted=None, repetition=None,
+                   presence=None, frequency=None, bias_tokens=None, bias=None, mask=None, mask_rows=None, dtype=None,
+                   stream=None, out=None):
+    """A request's penalties, biases and grammar mask applied to its logits, in ``dtype`` (the logits' by
+    default).  See ``dspark_process_logits``.
+
+    logits [B, V], or [B, R, V] for blocks, fp32 or bf16 (rows one stride apart); history [B, H] int32 with
+    ``lengths`` and ``prompt_lengths`` [B] int32; drafted [B, R - 1] int32, which row k counts the first k of;
+    repetition, presence, frequency [B] fp32; bias_tokens, bias [B, nb]; mask [M, >= ceil(V / 32)] int32 words of
+    bits, a set bit allowing its entry, and mask_rows [B] or [B, R] int32 (-1: no mask).  ``out`` may be the
+    logits themselves."""
+    return ProcessPlan(logits, history=history, lengths=lengths, prompt_lengths=prompt_lengths, drafted=drafted,
+                       repetition=repetition, presence=presence, frequency=frequency, bias_tokens=bias_tokens,
+                       bias=bias, mask=mask, mask_rows=mask_rows, dtype=dtype, stream=stream, out=out).run()
+
+
+class ProcessGradPlan(_Plan):
+    """``process_logits_grad`` with its arguments marshalled once (see ``_Plan``)."""
+
+    def __init__(self, grad, logits, *, history=None, lengths=None, prompt_lengths=None, drafted=None,
+                 repetition=None, mask=None, mask_rows=None, stream=None, out=None):
+        keep = (grad, logits, history, lengths, prompt_lengths, drafted, repetition, mask, mask_rows)
+        dev = _same_device(*keep, out)
+        gdt, zdt = _dtype_code(grad), _dtype_code(logits)
+        lead, B, R, V, ld, zp = _block(logits, "logits")
+        if grad.shape != logits.shape:
+            raise ValueError("grad has the logits' shape")
+        if out is None:
+            with _on(stream):
+                out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+        elif out.shape != logits.shape or out.dtype != logits.dtype:
+            raise ValueError("out has the logits' shape and dtype")
+        _, _, _, gld, gp = _logit_rows(grad, "grad")
+        _, _, _, old, op = _logit_rows(out, "out")
+        hp, hld, H = _history(history, B)
+        mp, mld, M, rows = _mask(mask, mask_rows, lead, V)
+        args = (B, R, V, gdt, gp, gld, zdt, zp, ld, hp, hld, H,
+                *_requests(B, R, lengths, prompt_lengths, drafted, history), _f32(repetition, (B,), "repetition"),
+                mp, mld, M, rows, op, old)
+        self._set("dspark_process_logits_grad", args, stream, out, keep, dev)
+
+
+def process_logits_grad(grad, logits, *, history=None, lengths=None, prompt_lengths=None, drafted=None,
+                        repetition=None, mask=None, mask_rows=None, stream=None, out=None):
+    """Gradient with respect to the raw logits, in their dtype, for the gradient ``grad`` with respect to what
+    ``process_logits`` made of them (fp32 or bf16).  ``out`` may be ``grad`` itself.  See
+    ``dspark_process_logits_grad``."""
+    return ProcessGradPlan(grad, logits, history=history, lengths=lengths, prompt_lengths=prompt_lengths,
+                           drafted=drafted, repetition=repetition, mask=mask, mask_rows=mask_rows, stream=stream,
+                           out=out).run()
+
+
+class DistillWorkspace(Workspace):
+    """Zero-initialised device scratch for ``distill_loss`` and ``distill_grad`` (shapes up to N rows, V, K)."""
+
+    def __init__(self, N: int, V: int, K: int, device=None):
+        n = _lib.load().dspark_distill_workspace_bytes(N, V, K)
+        if n == 0:
+            raise ValueError("invalid distillation shape for a workspace")
+        self.nbytes = int(n)
+        self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=device or "cuda")
+
+
+@dataclass
+class DistillOutput:
+    loss: torch.Tensor                # [...]
+    parts: torch.Tensor               # [..., 2] (KL, L1), without their weights
+    norm: torch.Tensor                # [..., 4] (largest logit, ln sum) of the row and outside the teacher's tokens
+    grad_logits: torch.Tensor | None  # the logits' shape and dtype
+
+
+def _teacher(teacher_ids, teacher_logp, lead):
+    K = teacher_ids.shape[-1] if teacher_ids.dim() else 0
+    return K, _ints(teacher_ids, (*lead, K), "teacher_ids"), _f32(teacher_logp, (*lead, K), "teacher_logp")
+
+
+class DistillPlan(_Plan):
+    """``distill_loss`` with its arguments marshalled once (see ``_Plan``)."""
+
+    def __init__(self, logits, teacher_ids, teacher_logp, *, T=1.0, alpha=(1.0, 0.0), rest=True, weight=None,
+                 want_grad=True, workspace=None, stream=None, out=None):
+        dev = _same_device(logits, teacher_ids, teacher_logp, weight, workspace)
+        zdt = _dtype_code(logits)
+        lead, N, V, ld, zp = _logit_rows(logits, "logits")
+        K, ip, lp = _teacher(teacher_ids, teacher_logp, lead)
+        with _on(stream):
+            ws = workspace or DistillWorkspace(N, V, K, device=dev)
+            if out is None:
+                def new(*shape):
+                    return torch.empty((*lead, *shape), dtype=torch.float32, device=dev)
+                grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev) if want_grad else None
+                out = DistillOutput(new(), new(2), new(4), grad)
+        _same_device(logits, out.loss, out.parts, out.norm, out.grad_logits)
+        gp, gld = None, V
+        if want_grad:
+            if out.grad_logits is None:
+                raise ValueError("out has no grad_logits")
+            if out.grad_logits.shape != logits.shape or out.grad_logits.dtype != logits.dtype:
+                raise ValueError("grad_logits has the logits' shape and dtype")
+            _, _, _, gld, gp = _logit_rows(out.grad_logits, "grad_logits")
+        args = (N, V, float(T), zdt, zp, ld, K, ip, lp, _f32(weight, lead, "weight"), float(alpha[0]),
+                float(alpha[1]), int(bool(rest)), _f32(out.loss, lead, "loss"), _f32(out.parts, (*lead, 2), "parts"),
+                _f32(out.norm, (*lead, 4), "norm"), gp, gld, ws.buf.data_ptr(), ws.nbytes)
+        self.workspace = ws
+        self._set("dspark_distill_loss", args, stream, out, (logits, teacher_ids, teacher_logp, weight, ws), dev)
+
+
+def distill_loss(logits, teacher_ids, teacher_logp, *, T=1.0, alpha=(1.0, 0.0), rest=True, weight=None,
+                 want_grad=True, workspace=None, stream=None, out=None) -> DistillOutput:
+    """Loss of softmax(logits / T) against a teacher's K (<= 128) largest log probabilities: ``alpha[0]`` times
+    their relative entropy plus ``alpha[1]`` times their L1 distance, each over the K tokens and, with
+    ``rest``, everything else as one more outcome; with its gradient in the same call (``want_grad``).  See
+    ``dspark_distill_loss``.
+
+    logits [..., V] fp32 or bf16 (rows one stride apart), teacher_ids [..., K] int32 (-1: none) and teacher_logp
+    [..., K] fp32, as ``token_logprobs(..., top=K)`` gives them; weight [...] fp32 (0: a padding row).  ``out``: an
+    earlier call's DistillOutput, whose grad_logits may be the logits themselves."""
+    return DistillPlan(logits, teacher_ids, teacher_logp, T=T, alpha=alpha, rest=rest, weight=weight,
+                       want_grad=want_grad, workspace=workspace, stream=stream, out=out).run()
+
+
+class DistillGradPlan(_Plan):
+    """``distill_grad`` with its arguments marshalled once (see ``_Plan``)."""
+
+    def __init__(self, logits, teacher_ids, teacher_logp, norm, grad_loss, *, T=1.0, alpha=(1.0, 0.0), rest=True,
+                 workspace=None, stream=None, out=None):
+        dev = _same_device(logits, teacher_ids, teacher_logp, norm, grad_loss, workspace, out)
+        zdt = _dtype_code(logits)
+        lead, N, V, ld, zp = _logit_rows(logits, "logits")
+        K, ip, lp = _teacher(teacher_ids, teacher_logp, lead)
+        with _on(stream):
+            ws = workspace or DistillWorkspace(N, V, K, device=dev)
+            if out is None:
+                out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+        if out.shape != logits.shape or out.dtype != logits.dtype:
+            raise ValueError("out has the logits' shape and dtype")
+        if norm is None or grad_loss is None:
+            raise ValueError("norm and grad_loss are required")
+        _, _, _, gld, gp = _logit_rows(out, "out")
+        args = (N, V, float(T), zdt, zp, ld, K, ip, lp, _f32(norm, (*lead, 4), "norm"),
+                _f32(grad_loss, lead, "grad_loss"), float(alpha[0]), float(alpha[1]), int(bool(rest)), gp, gld,
+                ws.buf.data_ptr(), ws.nbytes)
+        self.workspace = ws
+        self._set("dspark_distill_grad", args, stream, out, (logits, teacher_ids, teacher_logp, norm, grad_loss, ws),
+                  dev)
+
+
+def distill_grad(logits, teacher_ids, teacher_logp, norm, grad_loss, *, T=1.0, alpha=(1.0, 0.0), rest=True,
+                 workspace=None, stream=None, out=None):
+    """Gradient of ``distill_loss``'s loss (of weight 1) with respect to the logits, in their dtype, times
+    ``grad_loss`` [...] fp32, from the forward call's ``norm``.  ``out`` may be the logits themselves.  See
+    ``dspark_distill_grad``."""
+    return DistillGradPlan(logits, teacher_ids, teacher_logp, norm, grad_loss, T=T, alpha=alpha, rest=rest,
+                           workspace=workspace, stream=stream, out=out).run()
 
 
 class CapacityRing:

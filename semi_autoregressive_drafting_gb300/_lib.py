@@ -46,6 +46,13 @@ SIGNATURES = {
     "dspark_embedding_grad": (I, [I, I, I, F, I, P, P, I, P, I, P, SZ, P]),
     "dspark_bias_grad_workspace_bytes": (SZ, [I, I, I, I]),
     "dspark_bias_grad": (I, [I, I, I, I, P, I, P, P, I, P, P, I, P, SZ, P]),
+    "dspark_process_logits": (I, [I, I, I, I, P, I64, P, I64, I, P, P, P, P, P, P, I, P, P, P, I64, I, P, I, P, I64,
+                                  P]),
+    "dspark_process_logits_grad": (I, [I, I, I, I, P, I64, I, P, I64, P, I64, I, P, P, P, P, P, I64, I, P, P, I64,
+                                       P]),
+    "dspark_distill_workspace_bytes": (SZ, [I, I, I]),
+    "dspark_distill_loss": (I, [I, I, F, I, P, I64, I, P, P, P, F, F, I, P, P, P, P, I64, P, SZ, P]),
+    "dspark_distill_grad": (I, [I, I, F, I, P, I64, I, P, P, P, P, F, F, I, P, I64, P, SZ, P]),
     "dspark_get_status": (I, [P, SZ, P]),
     "dspark_last_error": (ctypes.c_char_p, []),
     "dspark_draft_path": (I, [I, I, I, I, I]),

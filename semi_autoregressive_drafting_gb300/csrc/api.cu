@@ -106,6 +106,66 @@ bool usable_temperature(float T) {
   return T > 0.f && std::isfinite(T) && std::isfinite(1.4426950408889634f * (1.f / T));
 }
 
+bool known(dspark_dtype t) { return t == DSPARK_F32 || t == DSPARK_BF16; }
+size_t size_of(dspark_dtype t) { return t == DSPARK_BF16 ? 2 : 4; }
+// whether two arrays of N rows of V elements, ld apart, share memory without being the same array
+bool overlap(const void* a, dspark_dtype adt, int64_t ald, const void* b, dspark_dtype bdt, int64_t bld, int64_t N,
+             int V) {
+  if (!a || !b || N < 1) return false;
+  if (a == b && adt == bdt && (ald == bld || N == 1)) return false;
+  const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
+  const uintptr_t a1 = a0 + (uintptr_t)((N - 1) * ald + V) * size_of(adt);
+  const uintptr_t b1 = b0 + (uintptr_t)((N - 1) * bld + V) * size_of(bdt);
+  return a0 < b1 && b0 < a1;
+}
+// What the calls that process logits and their gradients share.
+dspark_status process_args(int B, int R, int V, int64_t ld, int64_t out_ld, dspark_dtype in_dt, const void* in,
+                           dspark_dtype out_dt, const void* out, const int32_t* history, int64_t history_ld, int H,
+                           int nb, const int32_t* bias_tokens, const float* bias, const uint32_t* mask,
+                           int64_t mask_ld, int M, const int32_t* mask_rows) {
+  if (B < 0 || R < 1 || R > 32 || V < 2 || V > (1 << 24) || (long long)B * R > (1 << 24) ||
+      (long long)B * (V / 1024 + 1) >= (1ll << 31))
+    return fail(DSPARK_ERR_INVALID, "bad shape B=%d R=%d V=%d", B, R, V);
+  if (!known(in_dt) || !known(out_dt)) return fail(DSPARK_ERR_INVALID, "unknown dtype");
+  if (ld < V || out_ld < V) return fail(DSPARK_ERR_INVALID, "a row stride is below V=%d", V);
+  if (H < 0 || H > (1 << 24) || nb < 0 || nb > (1 << 16))
+    return fail(DSPARK_ERR_INVALID, "bad history length %d or number of biases %d", H, nb);
+  if (H > 0 && (!history || history_ld < H))
+    return fail(DSPARK_ERR_INVALID, "history is required and its rows are at least H apart");
+  if (nb > 0 && (!bias_tokens || !bias)) return fail(DSPARK_ERR_INVALID, "bias_tokens and bias are required");
+  if (mask && (M < 1 || mask_ld < (V + 31) / 32 || (!mask_rows && (long long)M < (long long)B * R)))
+    return fail(DSPARK_ERR_INVALID, "mask needs rows of V bits, one for each row of logits or chosen by mask_rows");
+  if (mask_rows && !mask) return fail(DSPARK_ERR_INVALID, "mask_rows needs mask");
+  if (B > 0 && (!in || !out)) return fail(DSPARK_ERR_INVALID, "logits, grad and out are required");
+  if (!aligned(in, size_of(in_dt)) || !aligned(out, size_of(out_dt)) || !aligned(mask, 4) || !aligned(history, 4))
+    return fail(DSPARK_ERR_INVALID, "arrays must be aligned to their types");
+  if (overlap(in, in_dt, ld, out, out_dt, out_ld, (int64_t)B * R, V))
+    return fail(DSPARK_ERR_INVALID, "out overlaps what is read without being the same rows of the same type");
+  return DSPARK_OK;
+}
+dspark_status distill_args(int N, int V, float T, dspark_dtype zdt, const void* logits, int64_t ld, int K,
+                           const int32_t* ids, const float* logq, float a_kl, float a_l1, const void* grad,
+                           int64_t gld, const void* norm, const void* workspace, size_t workspace_bytes) {
+  if (N < 0 || N > (1 << 24) || V < 2 || V > (1 << 24) || (long long)N * (V / 4096 + 2) >= (1ll << 31))
+    return fail(DSPARK_ERR_INVALID, "bad shape N=%d V=%d", N, V);
+  if (K < 1 || K > 128 || K > V) return fail(DSPARK_ERR_INVALID, "K must be 1..min(128, V), not %d", K);
+  if (!usable_temperature(T)) return fail(DSPARK_ERR_INVALID, "T must be finite and log2(e) / T too");
+  if (!known(zdt)) return fail(DSPARK_ERR_INVALID, "unknown dtype");
+  if (ld < V || (grad && gld < V)) return fail(DSPARK_ERR_INVALID, "a row stride is below V=%d", V);
+  if (!std::isfinite(a_kl) || !std::isfinite(a_l1))
+    return fail(DSPARK_ERR_INVALID, "the loss weights must be finite");
+  if (N > 0 && (!logits || !ids || !logq))
+    return fail(DSPARK_ERR_INVALID, "logits, teacher_ids and teacher_logp are required");
+  if (!aligned(logits, size_of(zdt)) || !aligned(grad, size_of(zdt)) || !aligned(norm, 16))
+    return fail(DSPARK_ERR_INVALID, "logits and grad_logits must be aligned to their type and norm to 16 bytes");
+  if (overlap(logits, zdt, ld, grad, zdt, gld, N, V))
+    return fail(DSPARK_ERR_INVALID, "grad_logits overlaps the logits without being the same rows");
+  const size_t need = distill_workspace_bytes(N, V, K);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need)
+    return fail(DSPARK_ERR_WORKSPACE, "workspace must be 256-byte aligned and >= %zu bytes", need);
+  return DSPARK_OK;
+}
+
 struct WsLayout {
   size_t keys, hdot, ml, mlt, l1p, rnn_s, rnn_a, rnn_gh, rnn_flag, ybuf, w2t, total;
 };
@@ -645,6 +705,89 @@ dspark_status dspark_bias_grad(int N, int V, int r, dspark_dtype gdt, const void
                                    w2_layout == DSPARK_W2_RV, grad_a, grad_W2, accumulate != 0, stuck, workspace,
                                    di.sms, (cudaStream_t)stream);
   return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, "bias gradient launch");
+}
+
+dspark_status dspark_process_logits(int B, int R, int V, dspark_dtype zdt, const void* logits, int64_t ld,
+                                    const int32_t* history, int64_t history_ld, int H, const int32_t* lengths,
+                                    const int32_t* prompt_lengths, const int32_t* drafted, const float* repetition,
+                                    const float* presence, const float* frequency, int nb,
+                                    const int32_t* bias_tokens, const float* bias, const uint32_t* mask,
+                                    int64_t mask_ld, int M, const int32_t* mask_rows, dspark_dtype odt, void* out,
+                                    int64_t out_ld, void* stream) {
+  g_err.clear();
+  const dspark_status s = process_args(B, R, V, ld, out_ld, zdt, logits, odt, out, history, history_ld, H, nb,
+                                       bias_tokens, bias, mask, mask_ld, M, mask_rows);
+  if (s != DSPARK_OK || B == 0) return s;
+  cudaError_t e = launch_process(0, B, R, V, zdt == DSPARK_BF16, logits, ld, odt == DSPARK_BF16, out, out_ld, nullptr,
+                                 0, history, history_ld, H, lengths, prompt_lengths, drafted, repetition, presence,
+                                 frequency, nb, bias_tokens, bias, mask, mask_ld, M, mask_rows, (cudaStream_t)stream);
+  return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, "process logits launch");
+}
+
+dspark_status dspark_process_logits_grad(int B, int R, int V, dspark_dtype gdt, const void* grad, int64_t grad_ld,
+                                         dspark_dtype zdt, const void* logits, int64_t ld, const int32_t* history,
+                                         int64_t history_ld, int H, const int32_t* lengths,
+                                         const int32_t* prompt_lengths, const int32_t* drafted,
+                                         const float* repetition, const uint32_t* mask, int64_t mask_ld, int M,
+                                         const int32_t* mask_rows, void* out, int64_t out_ld, void* stream) {
+  g_err.clear();
+  const dspark_status s = process_args(B, R, V, grad_ld, out_ld, gdt, grad, zdt, out, history, history_ld, H, 0,
+                                       nullptr, nullptr, mask, mask_ld, M, mask_rows);
+  if (s != DSPARK_OK) return s;
+  if (ld < V) return fail(DSPARK_ERR_INVALID, "a row stride is below V=%d", V);
+  if (B > 0 && repetition && !logits) return fail(DSPARK_ERR_INVALID, "repetition needs the logits");
+  if (!aligned(logits, size_of(zdt))) return fail(DSPARK_ERR_INVALID, "arrays must be aligned to their types");
+  if (repetition && (overlap(logits, zdt, ld, out, zdt, out_ld, (int64_t)B * R, V) || (B > 0 && logits == out)))
+    return fail(DSPARK_ERR_INVALID, "out overlaps the logits");
+  if (B == 0) return DSPARK_OK;
+  cudaError_t e = launch_process(1, B, R, V, gdt == DSPARK_BF16, grad, grad_ld, zdt == DSPARK_BF16, out, out_ld,
+                                 logits, ld, history, history_ld, H, lengths, prompt_lengths, drafted, repetition,
+                                 nullptr, nullptr, 0, nullptr, nullptr, mask, mask_ld, M, mask_rows,
+                                 (cudaStream_t)stream);
+  return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, "process logits gradient launch");
+}
+
+size_t dspark_distill_workspace_bytes(int N, int V, int K) {
+  if (N < 0 || N > (1 << 24) || V < 2 || V > (1 << 24) || (long long)N * (V / 4096 + 2) >= (1ll << 31) || K < 1 ||
+      K > 128 || K > V)
+    return 0;
+  return distill_workspace_bytes(N, V, K);
+}
+
+dspark_status dspark_distill_loss(int N, int V, float T, dspark_dtype zdt, const void* logits, int64_t ld, int K,
+                                  const int32_t* teacher_ids, const float* teacher_logp, const float* weight,
+                                  float alpha_kl, float alpha_l1, int rest, float* loss, float* parts, float* norm,
+                                  void* grad_logits, int64_t grad_ld, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  g_err.clear();
+  if (N != 0 && !loss && !parts && !norm && !grad_logits) return fail(DSPARK_ERR_INVALID, "no output requested");
+  const dspark_status s = distill_args(N, V, T, zdt, logits, ld, K, teacher_ids, teacher_logp, alpha_kl, alpha_l1,
+                                       grad_logits, grad_ld, norm, workspace, workspace_bytes);
+  if (s != DSPARK_OK) return s;
+  if (!aligned(parts, 8)) return fail(DSPARK_ERR_INVALID, "parts must be aligned to 8 bytes");
+  if (N == 0) return DSPARK_OK;
+  cudaError_t e = launch_distill(N, V, T, zdt == DSPARK_BF16, logits, ld, K, teacher_ids, teacher_logp, weight,
+                                 alpha_kl, alpha_l1, rest != 0, nullptr, loss, parts, norm, grad_logits, grad_ld,
+                                 workspace, (cudaStream_t)stream);
+  return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, "distillation loss launch");
+}
+
+dspark_status dspark_distill_grad(int N, int V, float T, dspark_dtype zdt, const void* logits, int64_t ld, int K,
+                                  const int32_t* teacher_ids, const float* teacher_logp, const float* norm,
+                                  const float* grad_loss, float alpha_kl, float alpha_l1, int rest,
+                                  void* grad_logits, int64_t grad_ld, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  g_err.clear();
+  const dspark_status s = distill_args(N, V, T, zdt, logits, ld, K, teacher_ids, teacher_logp, alpha_kl, alpha_l1,
+                                       grad_logits, grad_ld, norm, workspace, workspace_bytes);
+  if (s != DSPARK_OK) return s;
+  if (N == 0) return DSPARK_OK;
+  if (!norm || !grad_loss || !grad_logits)
+    return fail(DSPARK_ERR_INVALID, "norm, grad_loss and grad_logits are required");
+  cudaError_t e = launch_distill(N, V, T, zdt == DSPARK_BF16, logits, ld, K, teacher_ids, teacher_logp, grad_loss,
+                                 alpha_kl, alpha_l1, rest != 0, norm, nullptr, nullptr, nullptr, grad_logits, grad_ld,
+                                 workspace, (cudaStream_t)stream);
+  return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, "distillation gradient launch");
 }
 
 dspark_status dspark_get_status(void* workspace, size_t workspace_bytes, void* stream) {

@@ -47,5 +47,20 @@ size_t bias_grad_workspace_bytes(int N, int V, int r, int w_bf16, int nsm);
 cudaError_t launch_bias_grad(int N, int V, int r, int g_bf16, const void* G, int w_bf16, const void* a,
                              const void* W2, int w2_rv, float* grad_a, float* grad_W2, int accumulate,
                              int stuck, void* workspace, int nsm, cudaStream_t stream);
+// grad: `in` is the gradient with respect to the processed logits and `raw` the logits (of out's type);
+// otherwise `in` is the logits and `raw` is not used.
+cudaError_t launch_process(int grad, int B, int R, int V, int i_bf16, const void* in, long long in_ld, int o_bf16,
+                           void* out, long long out_ld, const void* raw, long long raw_ld, const int32_t* history,
+                           long long history_ld, int H, const int32_t* lengths, const int32_t* prompts,
+                           const int32_t* drafted, const float* repetition, const float* presence,
+                           const float* frequency, int nb, const int32_t* bias_tokens, const float* bias,
+                           const uint32_t* mask, long long mask_ld, int M, const int32_t* mask_rows,
+                           cudaStream_t stream);
+size_t distill_workspace_bytes(int N, int V, int K);
+// norm_in: the gradient alone, from an earlier call's normalisers (then loss, parts and norm are NULL).
+cudaError_t launch_distill(int N, int V, float T, int bf16, const void* logits, long long ld, int K,
+                           const int32_t* ids, const float* logq, const float* weight, float a_kl, float a_l1,
+                           int rest, const float* norm_in, float* loss, float* parts, float* norm, void* grad,
+                           long long gld, void* workspace, cudaStream_t stream);
 
 }  // namespace dspark
