@@ -427,7 +427,7 @@ dspark_status dspark_bias_grad(int N, int V, int r, dspark_dtype gdt, const void
  * A row whose mask allows nothing is -inf everywhere.  A token outside [-1, V), in what is read, and a length
  * outside [0, H] or a prompt length outside [0, lengths[b]] make their request's rows NaN, a mask row outside
  * [-1, M) its row (no status word; no workspace needed).  Limits: B R <= 2^24 (B = 0 does nothing), 1 <= R <=
- * 32, 2 <= V <= 2^24, B (V / 1024 + 1) < 2^31, H <= 2^24, nb <= 2^16.  One launch.
+ * 32, 2 <= V <= 2^24, B (V / 1024 + 1) < 2^31, H <= 2^24, nb <= 1024.  One launch.
  */
 dspark_status dspark_process_logits(int B, int R, int V, dspark_dtype zdt, const void* logits, int64_t ld,
                                     const int32_t* history, int64_t history_ld, int H, const int32_t* lengths,

@@ -128,7 +128,7 @@ dspark_status process_args(int B, int R, int V, int64_t ld, int64_t out_ld, dspa
     return fail(DSPARK_ERR_INVALID, "bad shape B=%d R=%d V=%d", B, R, V);
   if (!known(in_dt) || !known(out_dt)) return fail(DSPARK_ERR_INVALID, "unknown dtype");
   if (ld < V || out_ld < V) return fail(DSPARK_ERR_INVALID, "a row stride is below V=%d", V);
-  if (H < 0 || H > (1 << 24) || nb < 0 || nb > (1 << 16))
+  if (H < 0 || H > (1 << 24) || nb < 0 || nb > 1024)
     return fail(DSPARK_ERR_INVALID, "bad history length %d or number of biases %d", H, nb);
   if (H > 0 && (!history || history_ld < H))
     return fail(DSPARK_ERR_INVALID, "history is required and its rows are at least H apart");

@@ -11,10 +11,14 @@
 //
 // Forward: a warp takes a 4 KB segment of a row, puts -inf in place of the row's own tokens, and leaves the
 // segment's maximum and sum; a second launch, one block per row, joins them, fetches the K logits and forms
-// the outcomes in 64 bits (K + 1 exponentials and logarithms a row).  The gradient is a third pass.
+// the outcomes.  The gradient is a third pass.
 #include "common.cuh"
 #include "kernels.h"
 #include "rows.cuh"
+
+#include <map>
+#include <mutex>
+#include <utility>
 
 namespace dspark {
 namespace {
@@ -25,6 +29,8 @@ constexpr int kMaxK = 128;
 constexpr int kIdLane = kMaxK / 32;   // a row's tokens per lane
 constexpr int kSegment = 8;           // 16-byte loads per lane of a segment (4 KB)
 constexpr float kL2e = 1.4426950408889634f;
+template <typename T>
+constexpr int kSegEntries = 32 * kSegment * Lg<T>::E;
 
 // What a row's gradient needs beside the logits.
 struct RowCoef {
@@ -34,7 +40,7 @@ struct RowCoef {
 
 struct DsArgs {
   int V, K, nchunk, rest;
-  float T, a_kl, a_l1;
+  float T, invT, invT_lo, a_kl, a_l1;
   long long ld, gld;
   const int32_t* ids;
   const float* logq;
@@ -56,19 +62,44 @@ __device__ __forceinline__ void load_ids(int (&id)[kIdLane], const int32_t* ids,
   }
 }
 
+// -inf in place of the entries whose bits are set
 template <typename T>
-__device__ __forceinline__ void put(uint4& q, int e, uint32_t fill) {
+__device__ __forceinline__ uint4 without(const uint4& q, uint32_t bits) {
   uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (sizeof(T) == 4) {
-      w[i] = e == i ? fill : w[i];
+      w[i] = (bits >> i) & 1u ? Lg<T>::kFill : w[i];
     } else {
-      w[i] = e == 2 * i ? (w[i] & 0xFFFF0000u) | (fill & 0xFFFFu) : w[i];
-      w[i] = e == 2 * i + 1 ? (w[i] & 0xFFFFu) | (fill & 0xFFFF0000u) : w[i];
+      const uint32_t m = ((bits >> (2 * i)) & 1u ? 0xFFFFu : 0u) | ((bits >> (2 * i)) & 2u ? 0xFFFF0000u : 0u);
+      w[i] = (w[i] & ~m) | (Lg<T>::kFill & m);
     }
   }
-  q = make_uint4(w[0], w[1], w[2], w[3]);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The maximum and the sum of 2^((z - m) log2(e) / T) of a warp's segment, whose 16-byte groups q gives by number:
+// registers, or shared memory read twice.
+template <typename T, typename Q>
+__device__ __forceinline__ float2 segment_sum(const Q& q, float s2) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int u = 0; u < kSegment; ++u) m = Lg<T>::max16(m, q(u));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const F2 nm = f2(m == -INFINITY ? 0.f : -m, m == -INFINITY ? 0.f : -m), s22 = f2(s2, s2);
+  F2 S = f2(0.f, 0.f);
+#pragma unroll
+  for (int u = 0; u < kSegment; ++u) {
+    const uint4 g = q(u);
+#pragma unroll
+    for (int e = 0; e < Lg<T>::E / 2; ++e) {
+      const float2 y = un2(mul2(add2(Lg<T>::pair(g, e), nm), s22));
+      S = add2(S, f2(ex2p(y.x), ex2p(y.y)));
+    }
+  }
+  const float2 two = un2(S);
+  return make_float2(m, warp_sum(two.x + two.y));
 }
 
 // One warp's segment: its maximum and sum of 2^((z - m) log2(e) / T) outside S.
@@ -88,169 +119,484 @@ __global__ void __launch_bounds__(kThr) distill_part_kernel(const T* __restrict_
   for (int u = 0; u < kSegment; ++u) q[u] = load16<T>(z, (g0 + u * 32 + lane) * E - head, a.V);
   int id[kIdLane];
   load_ids(id, a.ids + row * a.K, a.K);
+  unsigned long long mine = 0ull;   // E bits for each of the lane's groups: the row's own tokens
 #pragma unroll
   for (int i = 0; i < kIdLane; ++i) {
     uint32_t here = __ballot_sync(0xffffffffu, id[i] >= 0 && id[i] >= first && id[i] < last);
     while (here) {
       const int src = __ffs(here) - 1;
       here &= here - 1;
-      const int at = __shfl_sync(0xffffffffu, id[i], src) - first;
-      const int g = at / E, e = at % E;
-      if ((g & 31) == lane) {
-#pragma unroll
-        for (int u = 0; u < kSegment; ++u)
-          if (u == g >> 5) put<T>(q[u], e, Lg<T>::kFill);
-      }
+      const int at = __shfl_sync(0xffffffffu, id[i], src) - first, g = at / E;
+      if ((g & 31) == lane) mine |= 1ull << ((g >> 5) * E + at % E);
     }
   }
-  float m = -INFINITY;
+  if (__any_sync(0xffffffffu, mine != 0ull)) {
 #pragma unroll
-  for (int u = 0; u < kSegment; ++u) m = Lg<T>::max16(m, q[u]);
+    for (int u = 0; u < kSegment; ++u) q[u] = without<T>(q[u], (uint32_t)(mine >> (u * E)) & ((1u << E) - 1u));
+  }
+  const float2 p = segment_sum<T>([&](int u) { return q[u]; }, kL2e / a.T);
+  if (lane == 0) a.part[(row * a.nchunk + ch) * kWarps + warp] = p;
+}
+
+// ------------------------------------------------------------------ the outcomes of a row
+// In fp32, with numbers as sums of two where one would round away what they hold (ln S is up to 17, half a step
+// of that 1e-6; 1 - Q is what Q's last digits make it).  64-bit arithmetic for these few numbers took 11 us of a
+// row's 18.
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two add_two(float a, float b) {
+  const float s = a + b, t = s - a;
+  return Two{s, isinf(s) ? 0.f : (a - (s - t)) + (b - t)};
+}
+// (x - m) / T, with 1 / T in two parts
+__device__ __forceinline__ Two scaled(float x, float m, const Two& invT) {
+  const Two d = add_two(x, -m);
+  const float y = d.hi * invT.hi;
+  return Two{y, isinf(y) ? 0.f : fmaf(d.hi, invT.hi, -y) + fmaf(d.lo, invT.hi, d.hi * invT.lo)};
+}
+__device__ __forceinline__ Two minus(const Two& a, const Two& b) {
+  const Two s = add_two(a.hi, -b.hi);
+  return Two{s.hi, s.lo + (a.lo - b.lo)};
+}
+__device__ __forceinline__ Two plus(const Two& a, const Two& b) {
+  const Two s = add_two(a.hi, b.hi);
+  return Two{s.hi, s.lo + (a.lo + b.lo)};
+}
+// ln 2 in two parts: nine bits, so that its multiples are exact, and the rest (to 2e-12)
+constexpr float kLn2a = 0.693359375f, kLn2b = -2.12194440e-4f;
+// exp x to some 2^-26 of itself: 2^k e^r with |r| <= 0.35, and e^r = 1 + r + r^2 (1/2 + r/6 + ...) by its series, of
+// which only what is small is rounded
+__device__ __forceinline__ Two exp_two(const Two& x) {
+  if (!(x.hi > -87.f && x.hi < 88.f)) return Two{x.hi >= 88.f ? INFINITY : isnan(x.hi) ? x.hi : 0.f, 0.f};
+  const float k = rintf(x.hi * kL2e);
+  const Two r0 = add_two(fmaf(-k, kLn2a, x.hi), -k * kLn2b);
+  const Two r = add_two(r0.hi, r0.lo + (x.lo - fmaf(k, kLn2b, -(k * kLn2b))));
+  float s = 1.f / 40320.f;
+  s = fmaf(s, r.hi, 1.f / 5040.f);
+  s = fmaf(s, r.hi, 1.f / 720.f);
+  s = fmaf(s, r.hi, 1.f / 120.f);
+  s = fmaf(s, r.hi, 1.f / 24.f);
+  s = fmaf(s, r.hi, 1.f / 6.f);
+  s = fmaf(s, r.hi, 0.5f);
+  const Two e = add_two(1.f, r.hi);
+  const Two y = add_two(e.hi, fmaf(r.hi * r.hi, s, fmaf(r.hi, r.lo, r.lo)) + e.lo);
+  const float p = __int_as_float((127 + (int)k) << 23);   // (k from -126 to 127)
+  return Two{y.hi * p, y.lo * p};
+}
+// exp x to 2^-22 of itself (the instruction's), however long x is; of -inf and NaN too
+__device__ __forceinline__ float exp_of(const Two& x) {
+  const float y = x.hi * kL2e;
+  const float lo = fmaf(x.hi, kL2e, -y) + fmaf(x.hi, 1.925963033e-8f, x.lo * kL2e);   // (log2 e's own rest)
+  const float e = ex2p(y);
+  return isinf(y) ? e : fmaf(e, lo * 0.69314718f, e);
+}
+// ln S of a sum: the power of two split off, its multiple of ln 2 in parts
+__device__ __forceinline__ Two ln_two(float S) {
+  if (!(S > 0.f) || isinf(S)) return Two{S == 0.f ? -INFINITY : S > 0.f ? S : NAN, 0.f};
+  const int b = __float_as_int(S);
+  int k = (b >> 23) - 127;   // (a sum that counts is at least 2^-126)
+  float f = __int_as_float((b & 0x7FFFFF) | 0x3F800000);
+  if (f > 1.41421356f) {
+    f *= 0.5f;
+    ++k;
+  }
+  const Two s = add_two((float)k * kLn2a, log1pf(f - 1.f));
+  return Two{s.hi, fmaf((float)k, kLn2b, s.lo)};
+}
+
+__device__ __forceinline__ Two warp_sum(Two v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float s2 = kL2e / a.T, nm = m == -INFINITY ? 0.f : -m;
-  float S = 0.f;
+  for (int o = 16; o > 0; o >>= 1)
+    v = plus(v, Two{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
+  return v;
+}
+
+// A row's K tokens in shared memory.
+struct RowSm {
+  int id[kMaxK], bad;   // a token outside [-1, V), or one that is there twice
+  float lq[kMaxK];
+  Two q[kMaxK];
+  float z[kMaxK];       // the row's logits there
+  float mass, rest;     // the teacher's: of the tokens, and what is left
+};
+constexpr int kSeen = 2048;
+struct SeenSm {
+  uint8_t by[kSeen];    // who was the last with an id of these low bits
+};
+__device__ __forceinline__ bool in_vocabulary(int id, int V) { return id >= 0 && id < V; }
+// kMaxK threads, a token each (barrier 1 among them).
+__device__ __forceinline__ void load_teacher(RowSm& sm, SeenSm& seen, const DsArgs& a, long long row, int tid) {
+  const int id = tid < a.K ? __ldg(a.ids + row * a.K + tid) : -1;
+  const float lq = tid < a.K ? __ldg(a.logq + row * a.K + tid) : -INFINITY;
+  if (tid == 0) sm.bad = 0;
+  sm.id[tid] = id;
+  const bool have = in_vocabulary(id, a.V);
+  if (have) seen.by[id % kSeen] = (uint8_t)tid;
+  sm.lq[tid] = have ? lq : -INFINITY;
+  sm.q[tid] = exp_two(Two{have ? lq : -INFINITY, 0.f});
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+  bool bad = id < -1 || id >= a.V;
+  if (have && seen.by[id % kSeen] != tid) {   // (another one: of two equal ids one finds the other here)
+    int n = 0;
+    for (int j = 0; j < a.K; ++j) n += sm.id[j] == id ? 1 : 0;
+    bad = n > 1;
+  }
+  if (bad) sm.bad = 1;
+  if (tid < 32) {
+    Two Q{0.f, 0.f};   // with its roundings
 #pragma unroll
-  for (int u = 0; u < kSegment; ++u) {
-#pragma unroll
-    for (int e = 0; e < E / 2; ++e) {
-      const float2 f = un2(Lg<T>::pair(q[u], e));
-      S += ex2p((f.x + nm) * s2) + ex2p((f.y + nm) * s2);
+    for (int i = 0; i < kIdLane; ++i)
+      if (i * 32 < a.K) Q = plus(Q, sm.q[i * 32 + tid]);
+    Q = warp_sum(Q);
+    const Two left = add_two(1.f - Q.hi, -Q.lo);   // (1 - Q.hi is exact where it matters)
+    if (tid == 0) {
+      sm.mass = Q.hi;
+      sm.rest = left.hi > 0.f ? left.hi : left.hi <= 0.f ? 0.f : left.hi;   // (NaN stays)
     }
   }
-  S = warp_sum(S);
-  if (lane == 0) a.part[(row * a.nchunk + ch) * kWarps + warp] = make_float2(m, S);
 }
 
-// Sum over the block's 128 threads in a fixed order; every thread has it.
-__device__ __forceinline__ double block_sum(double v, double* sm) {
+// One warp's work on a row, up to four tokens per lane (its reductions need no barriers), in two parts: what the
+// gradient needs, which the other blocks wait for and which takes no logarithm, then the loss.
+struct Outcomes {
+  float mr, mall;     // the largest logit of the rest, of the row
+  float S, all;       // the sums relative to them (of this call's segments)
+  float p[kIdLane], pr;
+  bool nan;
+};
+__device__ __forceinline__ float sign(float x) { return x > 0.f ? 1.f : x < 0.f ? -1.f : x; }
+
+// The maxima, the sums and the student's probabilities, FWD: from the segments, part; otherwise from the normalisers
+// of an earlier call.
+template <bool FWD>
+__device__ __forceinline__ void row_sums(Outcomes& y, const RowSm& sm, const DsArgs& a, long long row,
+                                         const float2* part, int nseg) {
+  const int lane = (int)(threadIdx.x & 31);
+  const Two inv{a.invT, a.invT_lo};
+  Two ls{0.f, 0.f}, lsr{0.f, 0.f};
+  if (!FWD) {
+    const float4 n = __ldg((const float4*)a.norm_in + row);
+    y.mall = n.x;
+    ls.hi = n.y;
+    y.mr = n.z;
+    lsr.hi = n.w;
+  }
+  float z[kIdLane], e = 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
-  __syncthreads();
-  return (sm[0] + sm[1]) + (sm[2] + sm[3]);
+  for (int i = 0; i < kIdLane; ++i)
+    z[i] = i * 32 < a.K && in_vocabulary(sm.id[i * 32 + lane], a.V) ? sm.z[i * 32 + lane] : -INFINITY;
+  if (FWD) {
+    float m = -INFINITY, mz = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
+    for (int i = lane; i < nseg; i += 32) m = fmaxf(m, part[i].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      mz = fmaxf(mz, __shfl_xor_sync(0xffffffffu, mz, o));
+    }
+    y.mr = m;
+    y.mall = fmaxf(m, mz);
+  }
+#pragma unroll
+  for (int i = 0; i < kIdLane; ++i) {
+    y.p[i] = 0.f;
+    if (i * 32 >= a.K || z[i] == -INFINITY) continue;
+    const Two d = scaled(z[i], y.mall, inv);
+    y.p[i] = exp_of(FWD ? d : minus(d, ls));
+    e += y.p[i];
+  }
+  const Two d = y.mr == -INFINITY ? Two{-INFINITY, 0.f} : scaled(y.mr, y.mall, inv);
+  if (FWD) {
+    const float s2 = kL2e * a.invT;
+    float S = 0.f;
+    for (int i = lane; i < nseg; i += 32) {
+      const float2 p = part[i];
+      // (an empty segment is left out; NaN stays)
+      if (p.x != -INFINITY || isnan(p.y)) S = fmaf(p.y, ex2p((p.x - y.mr) * s2), S);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      S += __shfl_xor_sync(0xffffffffu, S, o);
+      e += __shfl_xor_sync(0xffffffffu, e, o);
+    }
+    const float r = y.mr == -INFINITY && !isnan(S) ? 0.f : S * exp_of(d);
+    y.S = S;
+    y.all = r + e;
+    const float one = y.all > 0.f ? __fdividef(1.f, y.all) : y.all == 0.f ? 0.f : NAN;   // (a row without entries: p = 0)
+    y.pr = r * one;
+#pragma unroll
+    for (int i = 0; i < kIdLane; ++i) y.p[i] *= one;
+    y.nan = isnan(y.all);
+  } else {
+    y.pr = exp_of(plus(d, minus(lsr, ls)));
+    y.S = lsr.hi;   // (its logarithm)
+    y.nan = isnan(ls.hi) || isnan(lsr.hi);
+  }
+  y.nan |= sm.bad != 0 || isnan(sm.rest);
 }
 
-// One block per row joins the segments (FWD) or takes the normalisers of an earlier call, forms the
-// outcomes, and leaves the loss and what the gradient needs.
+// What the gradient needs: for the rest, and at, for the lane's tokens.
+template <bool FWD>
+__device__ __forceinline__ RowCoef row_gradient(const Outcomes& y, const RowSm& sm, const DsArgs& a, float w,
+                                                float (&at)[kIdLane]) {
+  const int lane = (int)(threadIdx.x & 31);
+  // t_j = p_j times the loss's derivative by p_j
+  const float qr = sm.rest, tr = a.rest ? fmaf(-a.a_kl, qr, a.a_l1 * (y.pr * sign(y.pr - qr))) : 0.f;
+  float t[kIdLane], M = 0.f;
+#pragma unroll
+  for (int i = 0; i < kIdLane; ++i) {
+    t[i] = 0.f;
+    if (i * 32 >= a.K) continue;
+    const Two q = sm.q[i * 32 + lane];
+    t[i] = fmaf(-a.a_kl, q.hi, a.a_l1 * (y.p[i] * sign((y.p[i] - q.hi) - q.lo)));
+    M += t[i];
+  }
+  M = a.a_l1 == 0.f ? -a.a_kl * (a.rest ? fmaxf(sm.mass, 1.f) : sm.mass) : dspark::warp_sum(M) + tr;
+  const float scale = w * a.invT;
+#pragma unroll
+  for (int i = 0; i < kIdLane; ++i) at[i] = y.nan ? NAN : scale * fmaf(-y.p[i], M, t[i]);
+  if (y.nan) return RowCoef{0.f, 0.f, NAN, 0.f};
+  if (y.mr == -INFINITY) return RowCoef{0.f, 0.f, 0.f, 0.f};
+  const float c = scale * fmaf(-y.pr, M, tr);
+  return RowCoef{-y.mr, FWD ? 0.f : y.S, FWD ? __fdividef(c, y.S) : c, 0.f};
+}
+
+__device__ __forceinline__ void row_loss(const Outcomes& y, const RowSm& sm, const DsArgs& a, long long row, float w) {
+  const int lane = (int)(threadIdx.x & 31);
+  const Two inv{a.invT, a.invT_lo}, never{-INFINITY, 0.f};
+  const Two lsr = y.mr == -INFINITY && !isnan(y.S) ? Two{0.f, 0.f} : ln_two(y.S);
+  const Two ls = y.mall == -INFINITY && !isnan(y.all) ? Two{0.f, 0.f} : ln_two(y.all);
+  float kl = 0.f, l1 = 0.f;
+#pragma unroll
+  for (int i = 0; i < kIdLane; ++i) {
+    const int j = i * 32 + lane;
+    if (j >= a.K || !in_vocabulary(sm.id[j], a.V)) continue;
+    const Two q = sm.q[j], lp = sm.z[j] == -INFINITY ? never : minus(scaled(sm.z[j], y.mall, inv), ls);
+    kl += q.hi != 0.f ? q.hi * ((sm.lq[j] - lp.hi) - lp.lo) : 0.f;
+    l1 += fabsf((y.p[i] - q.hi) - q.lo);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    kl += __shfl_xor_sync(0xffffffffu, kl, o);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+  }
+  if (lane != 0) return;
+  if (a.rest) {
+    const float qr = sm.rest;
+    const Two lpr = y.mr == -INFINITY ? never : plus(scaled(y.mr, y.mall, inv), minus(lsr, ls));
+    kl = qr != 0.f ? fmaf(qr, (logf(qr) - lpr.hi) - lpr.lo, kl) : kl;
+    l1 += fabsf(y.pr - qr);
+  }
+  const float k = a.a_kl != 0.f ? a.a_kl * kl : 0.f, l = a.a_l1 != 0.f ? a.a_l1 * l1 : 0.f;
+  if (a.loss) a.loss[row] = y.nan ? NAN : w * (k + l);
+  if (a.parts) ((float2*)a.parts)[row] = y.nan ? make_float2(NAN, NAN) : make_float2(kl, l1);
+  if (a.norm)
+    ((float4*)a.norm)[row] = sm.bad ? make_float4(NAN, NAN, NAN, NAN)
+                                    : make_float4(y.mall, ls.hi + ls.lo, y.mr, lsr.hi + lsr.lo);
+}
+// A padding row's outputs.
+__device__ __forceinline__ void row_zero(const DsArgs& a, long long row) {
+  if (a.loss) a.loss[row] = 0.f;
+  if (a.parts) ((float2*)a.parts)[row] = make_float2(0.f, 0.f);
+  if (a.norm) ((float4*)a.norm)[row] = make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+// One block per row.
 template <typename T, bool FWD>
 __global__ void __launch_bounds__(kMaxK) distill_rows_kernel(const T* __restrict__ logits, const DsArgs a) {
-  __shared__ double s_sum[4];
-  __shared__ float s_m[4];
-  __shared__ int s_id[kMaxK];
+  __shared__ RowSm sm;
+  __shared__ SeenSm seen;
   const long long row = blockIdx.x;
   const int tid = (int)threadIdx.x;
   const float w = a.weight ? a.weight[row] : 1.f;
   if (w == 0.f) {  // a padding row: not read
     if (tid == 0) {
-      if (a.loss) a.loss[row] = 0.f;
-      if (a.parts) ((float2*)a.parts)[row] = make_float2(0.f, 0.f);
-      if (a.norm) ((float4*)a.norm)[row] = make_float4(0.f, 0.f, 0.f, 0.f);
+      row_zero(a, row);
       if (a.coef) a.coef[row] = RowCoef{0.f, 0.f, 0.f, 0.f};
     }
     if (a.at && tid < a.K) a.at[row * a.K + tid] = 0.f;
     return;
   }
   const T* z = logits + row * a.ld;
-  const int id = tid < a.K ? a.ids[row * a.K + tid] : -1;
-  const float lq = id >= 0 && id < a.V ? a.logq[row * a.K + tid] : -INFINITY;
-  const float zj = id >= 0 && id < a.V ? to_f<T>(z[id]) : -INFINITY;
-  s_id[tid] = id;
+  load_teacher(sm, seen, a, row, tid);
+  if (in_vocabulary(sm.id[tid], a.V)) sm.z[tid] = to_f<T>(z[sm.id[tid]]);
   __syncthreads();
-  bool bad = id < -1 || id >= a.V;
-  if (id >= 0)
-    for (int j = 0; j < tid; ++j) bad |= s_id[j] == id;
-  bad = __syncthreads_or(bad);
-
-  const double invT = 1.0 / (double)a.T;
-  float mr, mall;
-  double lsr, ls;   // ln of the sums relative to mr, mall
-  double dj;        // (z_j - mall) / T
-  bool none;        // the row is -inf everywhere
-  if (FWD) {
-    pdl_wait();
-    // the rest: the segments' maximum, then their sums relative to it
-    const int head = row_head(z), nseg = (a.V + head + 32 * kSegment * Lg<T>::E - 1) / (32 * kSegment * Lg<T>::E);
-    const float2* part = a.part + row * a.nchunk * kWarps;
-    float m = -INFINITY;
-    for (int i = tid; i < nseg; i += kMaxK) m = fmaxf(m, __ldcg(&part[i].x));
-    float mz = zj;
+  if (tid >= 32) return;
+  if (FWD) pdl_wait();
+  const int nseg = (a.V + row_head(z) + kSegEntries<T> - 1) / kSegEntries<T>;
+  const float2* part = a.part + row * a.nchunk * kWarps;
+  Outcomes y;
+  float at[kIdLane];
+  row_sums<FWD>(y, sm, a, row, part, nseg);
+  const RowCoef c = row_gradient<FWD>(y, sm, a, w, at);
+  if (FWD) row_loss(y, sm, a, row, w);
+  if (tid == 0 && sm.bad) atomicMax(&a.hdr->status, kErrInvalid);
+  if (a.at) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      mz = fmaxf(mz, __shfl_xor_sync(0xffffffffu, mz, o));
-    }
-    __shared__ float s_z[4];
-    if ((tid & 31) == 0) {
-      s_m[tid >> 5] = m;
-      s_z[tid >> 5] = mz;
-    }
-    __syncthreads();
-    mr = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-    mall = fmaxf(mr, fmaxf(fmaxf(s_z[0], s_z[1]), fmaxf(s_z[2], s_z[3])));
-    const float s2 = kL2e / a.T;
-    double S = 0.0;
-    for (int i = tid; i < nseg; i += kMaxK) {
-      const float2 p = __ldcg(part + i);
-      // (an empty segment is left out; NaN stays)
-      if (p.x != -INFINITY || isnan(p.y)) S += (double)p.y * (double)ex2p((p.x - mr) * s2);
-    }
-    S = block_sum(S, s_sum);
-    none = mall == -INFINITY;
-    lsr = mr == -INFINITY && !isnan(S) ? 0.0 : log(S);
-    dj = id >= 0 && zj != -INFINITY ? ((double)zj - (double)mall) * invT : -INFINITY;
-    const double e = id >= 0 && zj != -INFINITY ? exp(dj) : 0.0;
-    const double Sr = mr == -INFINITY && !isnan(S) ? 0.0 : S * exp(((double)mr - (double)mall) * invT);
-    const double all = Sr + block_sum(e, s_sum);
-    ls = none && !isnan(all) ? 0.0 : log(all);
-  } else {
-    const float4 n = ((const float4*)a.norm_in)[row];
-    mall = n.x;
-    ls = n.y;
-    mr = n.z;
-    lsr = n.w;
-    none = mall == -INFINITY;
-    dj = id >= 0 && zj != -INFINITY ? ((double)zj - (double)mall) * invT : -INFINITY;
+    for (int i = 0; i < kIdLane; ++i)
+      if (i * 32 + tid < a.K) a.at[row * a.K + i * 32 + tid] = at[i];
   }
-  // the outcomes; thread j holds the j-th, all hold the rest
-  const double lp = dj - ls, p = exp(lp);
-  const double lpr = mr == -INFINITY ? -INFINITY : ((double)mr - (double)mall) * invT + lsr - ls, pr = exp(lpr);
-  const double q = id >= 0 ? exp((double)lq) : 0.0;
-  const double Q = block_sum(q, s_sum);
-  const double qr = Q < 1.0 ? 1.0 - Q : Q >= 1.0 ? 0.0 : Q;   // (NaN stays)
-  const double sgn = p > q ? 1.0 : p < q ? -1.0 : p - q, sgnr = pr > qr ? 1.0 : pr < qr ? -1.0 : pr - qr;
-  const double a_kl = a.a_kl, a_l1 = a.a_l1;
-  const double t = id >= 0 ? -a_kl * q + a_l1 * (p * sgn) : 0.0;
-  const double tr = a.rest ? -a_kl * qr + a_l1 * (pr * sgnr) : 0.0;
-  const double M = block_sum(t, s_sum) + tr;
-  if (FWD && (a.loss || a.parts)) {
-    double kl = id >= 0 && q != 0.0 ? q * ((double)lq - lp) : 0.0, l1 = id >= 0 ? fabs(p - q) : 0.0;
-    kl = block_sum(kl, s_sum);
-    l1 = block_sum(l1, s_sum);
-    if (a.rest) {
-      if (qr != 0.0) kl += qr * (log(qr) - lpr);
-      l1 += fabs(pr - qr);
-    }
-    if (tid == 0) {
-      const double k = a_kl != 0.0 ? a_kl * kl : 0.0, l = a_l1 != 0.0 ? a_l1 * l1 : 0.0;
-      // NaN anywhere in the row is in its sum, and so in lp_r or ls
-      if (a.loss) a.loss[row] = bad || isnan(ls) ? NAN : (float)((double)w * (k + l));
-      if (a.parts) ((float2*)a.parts)[row] = bad || isnan(ls) ? make_float2(NAN, NAN) : make_float2((float)kl, (float)l1);
-    }
+  if (a.coef && tid == 0) a.coef[row] = c;
+}
+
+// ------------------------------------------------------------------ loss and gradient of a row on the chip
+// A cluster of blocks takes a row, each block a whole number of segments: the row is read once and stays in their
+// shared memory.  Every block gets the segments' partial results and the row's logits at the teacher's tokens, and a
+// warp of it forms what its gradient needs (sending that from one block takes another barrier); in the first block
+// another warp forms the loss, which nobody waits for.
+template <typename T>
+__device__ __forceinline__ uint4 grad16(const uint4& q, const RowCoef& c, float s2) {
+  constexpr int E = Lg<T>::E;
+  float f[E];
+  const F2 nm = f2(c.nm, c.nm), s22 = f2(s2, s2), ls = f2(-c.ls * kL2e, -c.ls * kL2e), cc = f2(c.c, c.c);
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) {
+    const float2 y = un2(fma2(add2(Lg<T>::pair(q, e), nm), s22, ls));
+    const float2 g = un2(mul2(f2(ex2p(y.x), ex2p(y.y)), cc));
+    f[2 * e] = g.x;
+    f[2 * e + 1] = g.y;
   }
-  const bool nan = bad || isnan(ls) || isnan(lsr);
-  const double scale = (double)w * invT;
-  if (a.at && tid < a.K) a.at[row * a.K + tid] = nan ? NAN : (float)(scale * (t - (id >= 0 ? p * M : 0.0)));
+  return pack16<T>(f);
+}
+
+__device__ __forceinline__ void st_cluster_f(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// (a load each time it is asked for, so that a segment takes no 32 registers: six blocks per SM)
+__device__ __forceinline__ uint4 lds16(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(smem_u32(p)));
+  return v;
+}
+
+constexpr int kChipBlocks = 4;   // per SM
+struct ChipSm {
+  RowSm row;
+  SeenSm seen;
+  uint64_t full;
+  RowCoef coef;
+  float at[kMaxK];    // the gradient at the row's tokens
+};
+
+// A block's share of a row: 16-byte groups [ga, gb) of the row's, of which [wa, wb) lie whole inside it; its entries
+// are [va, vb) (va < 0 in front of a row that starts inside a group).
+struct Share {
+  int head, ngroups, ga, gb, wa, wb, va, vb;
+};
+template <typename T>
+__device__ __forceinline__ Share share_of(const T* z, int V, int groups, uint32_t rank) {
+  constexpr int E = Lg<T>::E;
+  Share s;
+  s.head = row_head(z);
+  s.ngroups = (V + s.head + E - 1) / E;
+  s.ga = min((int)rank * groups, s.ngroups);
+  s.gb = min(s.ga + groups, s.ngroups);
+  s.va = s.ga * E - s.head;
+  s.vb = min(s.gb * E - s.head, V);
+  s.wa = s.ga + (s.va < 0 ? 1 : 0);
+  s.wb = s.gb * E - s.head > V ? s.gb - 1 : s.gb;
+  return s;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThr, kChipBlocks)
+    distill_chip_kernel(const T* logits, T* grad, const DsArgs a, int C, int segs) {
+  constexpr int E = Lg<T>::E, kGroups = 32 * kSegment;   // 16-byte groups of a segment
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ ChipSm sm;
+  uint4* buf = (uint4*)smem;                              // [segs][kGroups]
+  float2* part = (float2*)(buf + segs * kGroups);         // [C segs]
+  const uint32_t rank = cluster_rank();
+  const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5, groups = segs * kGroups;
+  const long long row = blockIdx.x / (unsigned)C;
+  const T* z = logits + row * a.ld;
+  T* o = grad + row * a.gld;
+  const Share s = share_of(z, a.V, groups, rank);
+  // whole groups by bulk copies, those at the ends of the row by entries
   if (tid == 0) {
-    if (FWD && a.norm)
-      ((float4*)a.norm)[row] = bad ? make_float4(NAN, NAN, NAN, NAN) : make_float4(mall, (float)ls, mr, (float)lsr);
-    if (a.coef) {
-      const double c = mr == -INFINITY ? 0.0 : scale * (tr - pr * M);
-      a.coef[row] = RowCoef{mr == -INFINITY ? 0.f : -mr, (float)lsr, nan ? NAN : (float)c, 0.f};
-    }
-    if (bad && a.hdr) atomicMax(&a.hdr->status, kErrInvalid);
+    mbar_init(&sm.full, 1u);
+    fence_mbar_init();
+    const uint32_t bytes = s.wb > s.wa ? (uint32_t)(s.wb - s.wa) * 16u : 0u;
+    mbar_expect_tx(&sm.full, bytes);
+    const uint64_t pol = policy_evict_first();
+    for (uint32_t at = 0; at < bytes; at += 16384u)
+      bulk_g2s((uint8_t*)(buf + (s.wa - s.ga)) + at, (const uint8_t*)(z + (long long)s.wa * E - s.head) + at,
+               min(16384u, bytes - at), &sm.full, pol);
   }
+  // (no block writes to another's shared memory before that one has started)
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+  const float w = a.weight ? __ldg(a.weight + row) : 1.f;
+  if (tid < kMaxK) load_teacher(sm.row, sm.seen, a, row, tid);
+  if (tid == kThr - 32 && s.ga < s.wa) buf[0] = load16<T>(z, s.va, a.V);
+  if (tid == kThr - 64 && s.wb < s.gb && s.wb >= s.wa) buf[s.wb - s.ga] = load16<T>(z, s.wb * E - s.head, a.V);
+  for (int i = (s.gb - s.ga) + tid; i < groups; i += kThr) {   // behind the row
+    const uint32_t f = Lg<T>::kFill;
+    buf[i] = make_uint4(f, f, f, f);
+  }
+  __syncthreads();
+  // (a wait that runs out: once more, so that nothing is in flight at the end)
+  bool ok = mbar_wait(&sm.full, 0u);
+  if (!ok) ok = mbar_wait(&sm.full, 0u) && false;
+  asm volatile("barrier.cluster.wait;" ::: "memory");
+  // the row's own tokens out of the rest
+  const int id = tid < kMaxK ? sm.row.id[tid] : -1;
+  const bool here = id >= max(s.va, 0) && id < s.vb;
+  if (here) {
+    T* p = (T*)buf + (id + s.head - s.ga * E);
+    const float x = ok ? to_f<T>(*p) : NAN;
+    for (int c = 0; c < C; ++c) st_cluster_f(cluster_addr(&sm.row.z[tid], (uint32_t)c), x);
+    *p = from_f<T>(-INFINITY);
+  }
+  __syncthreads();
+  const float s2 = kL2e / a.T;
+  for (int sg = warp; sg < segs; sg += kWarps) {
+    const uint4* at = buf + sg * kGroups + lane;
+    float2 p = segment_sum<T>([&](int u) { return lds16(at + u * 32); }, s2);
+    if (!ok) p.y = NAN;
+    if (lane < C) st_cluster_f2(cluster_addr(&part[(int)rank * segs + sg], (uint32_t)lane), p);
+  }
+  cluster_sync_all();
+  const int nseg = (s.ngroups + kGroups - 1) / kGroups;
+  if (warp == 0 || (warp == 1 && rank == 0)) {
+    Outcomes y;
+    if (w != 0.f) row_sums<true>(y, sm.row, a, row, part, nseg);
+    if (warp == 0) {
+      float at[kIdLane] = {};
+      RowCoef c{0.f, 0.f, 0.f, 0.f};   // a padding row: zeros, whatever was read
+      if (w != 0.f) c = row_gradient<true>(y, sm.row, a, w, at);
+#pragma unroll
+      for (int i = 0; i < kIdLane; ++i)
+        if (i * 32 < a.K) sm.at[i * 32 + lane] = at[i];
+      if (lane == 0) sm.coef = c;
+    } else if (w != 0.f) {
+      row_loss(y, sm.row, a, row, w);
+      if (lane == 0 && sm.row.bad) atomicMax(&a.hdr->status, kErrInvalid);
+    } else if (lane == 0) {
+      row_zero(a, row);
+    }
+  }
+  if (!ok && tid == 0) atomicMax(&a.hdr->status, kErrTimeout);
+  __syncthreads();
+  const RowCoef c = sm.coef;
+  const bool same = row_head((const T*)o) == s.head, none = c.c == 0.f;   // (zeros, whatever the entries are)
+  for (int g = s.ga + tid; g < s.gb; g += kThr) {
+    const int v0 = g * E - s.head;
+    const uint4 q = none ? make_uint4(0u, 0u, 0u, 0u) : grad16<T>(buf[g - s.ga], c, s2);
+    if (same && v0 >= 0 && v0 + E <= a.V) {
+      __stcs((uint4*)(o + v0), q);
+    } else {
+      T f[E];
+      memcpy(f, &q, 16);
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (v0 + e >= 0 && v0 + e < a.V) o[v0 + e] = f[e];
+    }
+  }
+  __syncthreads();
+  if (here) o[id] = from_f<T>(sm.at[tid]);
 }
 
 constexpr int kGPer = 4;  // 16-byte groups per thread
@@ -276,25 +622,23 @@ __global__ void __launch_bounds__(kThr) distill_grad_kernel(const T* logits, T* 
   load_ids(id, a.ids + row * a.K, a.K);
   pdl_wait();
   const float4 cf = __ldcg((const float4*)(a.coef + row));
-  const float invT = 1.f / a.T, nm = cf.x, ls = cf.y, c = cf.z;
+  const RowCoef c{cf.x, cf.y, cf.z, 0.f};
+  const bool none = c.c == 0.f;   // (zeros, whatever the entries are)
+  const float s2 = kL2e / a.T;
   const bool same = row_head((const T*)o) == head;
 #pragma unroll
   for (int u = 0; u < kGPer; ++u) {
     const int v0 = (g0 + u * 32 + lane) * E - head;
     if (v0 >= a.V) break;
-    float f[E];
-#pragma unroll
-    for (int e = 0; e < E / 2; ++e) {
-      const float2 zz = un2(Lg<T>::pair(q[u], e));
-      f[2 * e] = c == 0.f ? 0.f : c * ex2p(fmaf(zz.x + nm, invT, -ls) * kL2e);
-      f[2 * e + 1] = c == 0.f ? 0.f : c * ex2p(fmaf(zz.y + nm, invT, -ls) * kL2e);
-    }
+    const uint4 y = none ? make_uint4(0u, 0u, 0u, 0u) : grad16<T>(q[u], c, s2);
     if (same && v0 >= 0 && v0 + E <= a.V) {
-      __stcs((uint4*)(o + v0), pack16<T>(f));
+      __stcs((uint4*)(o + v0), y);
     } else {
+      T f[E];
+      memcpy(f, &y, 16);
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if (v0 + e >= 0 && v0 + e < a.V) o[v0 + e] = from_f<T>(f[e]);
+        if (v0 + e >= 0 && v0 + e < a.V) o[v0 + e] = f[e];
     }
   }
   __syncwarp();
@@ -303,6 +647,11 @@ __global__ void __launch_bounds__(kThr) distill_grad_kernel(const T* logits, T* 
     if (id[i] >= first && id[i] < last && id[i] >= 0 && id[i] < a.V)
       o[id[i]] = from_f<T>(__ldcg(a.at + row * a.K + i * 32 + lane));
 }
+
+// Segments of a block's share of a row: 64 KB, three blocks per SM, and as many as its shared memory holds; blocks
+// of a cluster at most; blocks for every SM.
+constexpr int kSegs = 16, kMostSegs = 50, kMostC = 16, kFill = 152;
+constexpr int kMostSmem = kMostSegs * 4096 + kMostC * kMostSegs * (int)sizeof(float2);
 
 constexpr size_t al(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -348,6 +697,65 @@ cudaError_t gradient(int N, const T* logits, T* grad, DsArgs a, bool al_rows, cu
   return launch_pdl(distill_grad_kernel<T>, (unsigned)N * (unsigned)a.nchunk, kThr, 0, stream, logits, grad, a);
 }
 
+// How rows of nseg segments go to the chip: in clusters of C blocks of `segs` segments, of which the device holds
+// `clusters` at once.
+struct ChipShape {
+  int C, segs, clusters;
+};
+size_t chip_smem(int C, int segs) { return (size_t)segs * 4096 + (size_t)C * segs * sizeof(float2); }
+cudaLaunchConfig_t chip_config(const ChipShape& h, int clusters, cudaLaunchAttribute* at, cudaStream_t stream) {
+  at->id = cudaLaunchAttributeClusterDimension;
+  at->val.clusterDim.x = (unsigned)h.C;
+  at->val.clusterDim.y = at->val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(clusters * h.C));
+  cfg.blockDim = dim3(kThr);
+  cfg.dynamicSmemBytes = chip_smem(h.C, h.segs);
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+// The cluster size of which the most fit, of blocks of at most kSegs segments where 16 blocks hold the row so (a
+// cluster lies inside a GPC, so the smallest size is not always it).  Asked for once for each length of row, and kept.
+template <typename T>
+cudaError_t chip_shape(int nseg, ChipShape* shape) {
+  static std::mutex mu;
+  static std::map<std::pair<int, int>, ChipShape> known;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(mu);
+  ChipShape& best = known[{dev, nseg}];
+  if (best.C == 0) {
+    auto kernel = distill_chip_kernel<T>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    const int least = (nseg + kSegs - 1) / kSegs;
+    for (int C = least < kMostC ? least : kMostC; C <= kMostC && C <= nseg; ++C) {
+      ChipShape h{C, (nseg + C - 1) / C, 0};
+      cudaLaunchAttribute at{};
+      const cudaLaunchConfig_t cfg = chip_config(h, 1, &at, nullptr);
+      e = cudaOccupancyMaxActiveClusters(&h.clusters, kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      if (h.clusters > best.clusters) best = h;
+    }
+  }
+  *shape = best;
+  return cudaSuccess;
+}
+
+template <typename T>
+cudaError_t on_chip(int N, int nseg, const T* logits, T* grad, const DsArgs& a, ChipShape h, cudaStream_t stream) {
+  // few rows: blocks for every SM (a row's results do not depend on how many share it)
+  const int most = nseg < kMostC ? nseg : kMostC, C = kFill / N < most ? kFill / N : most;
+  if (C > h.C) h = ChipShape{C, (nseg + C - 1) / C, 1};
+  cudaLaunchAttribute at{};
+  const cudaLaunchConfig_t cfg = chip_config(h, N, &at, stream);
+  return cudaLaunchKernelEx(&cfg, distill_chip_kernel<T>, logits, grad, a, h.C, h.segs);
+}
+
 template <typename T>
 cudaError_t run(int N, const T* logits, T* grad, const DsArgs& a, cudaStream_t stream) {
   const bool al_rows = ((uintptr_t)logits % 16) == 0 && (a.ld * (long long)sizeof(T)) % 16 == 0;
@@ -356,6 +764,13 @@ cudaError_t run(int N, const T* logits, T* grad, const DsArgs& a, cudaStream_t s
     distill_rows_kernel<T, false><<<(unsigned)N, kMaxK, 0, stream>>>(logits, a);
     e = cudaGetLastError();
   } else {
+    const int nseg = (a.V + (al_rows ? 0 : Lg<T>::E - 1) + kSegEntries<T> - 1) / kSegEntries<T>;
+    if (grad && nseg <= kMostC * kMostSegs) {
+      ChipShape shape;
+      e = chip_shape<T>(nseg, &shape);
+      if (e != cudaSuccess) return e;
+      if (shape.clusters > 0) return on_chip(N, nseg, logits, grad, a, shape, stream);
+    }
     e = forward(N, logits, a, al_rows, stream);
   }
   if (e != cudaSuccess || !grad) return e;
@@ -379,6 +794,8 @@ cudaError_t launch_distill(int N, int V, float T, int bf16, const void* logits, 
   a.nchunk = 0;
   a.rest = rest;
   a.T = T;
+  a.invT = 1.f / T;
+  a.invT_lo = (float)(1.0 / (double)T - (double)a.invT);
   a.a_kl = a_kl;
   a.a_l1 = a_l1;
   a.ld = ld;

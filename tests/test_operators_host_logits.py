@@ -40,7 +40,7 @@ def process(lib, B=4, R=2, V=100, idt=0, z=P, ld=100, h=P, hld=8, H=8, nb=0, bt=
 
 def test_process_refusals(lib):
     assert process(lib, B=0) == 0
-    for kw in BAD + [dict(nb=-1), dict(nb=(1 << 16) + 1), dict(nb=3), dict(nb=3, bt=P)]:
+    for kw in BAD + [dict(nb=-1), dict(nb=1025), dict(nb=3), dict(nb=3, bt=P)]:
         assert process(lib, **kw) == 1, kw
         assert lib.dspark_last_error()
 
