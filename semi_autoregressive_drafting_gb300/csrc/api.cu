@@ -766,8 +766,12 @@ dspark_status dspark_distill_loss(int N, int V, float T, dspark_dtype zdt, const
   if (s != DSPARK_OK) return s;
   if (!aligned(parts, 8)) return fail(DSPARK_ERR_INVALID, "parts must be aligned to 8 bytes");
   if (N == 0) return DSPARK_OK;
+  // Failure-path test hook, as for the bias gradients: DSPARK_TEST_STUCK_WAIT = mbar makes the wait for a row's
+  // copies count as one that has run out.
+  const char* f = std::getenv("DSPARK_TEST_STUCK_WAIT");
+  const int stuck = f && !std::strcmp(f, "mbar");
   cudaError_t e = launch_distill(N, V, T, zdt == DSPARK_BF16, logits, ld, K, teacher_ids, teacher_logp, weight,
-                                 alpha_kl, alpha_l1, rest != 0, nullptr, loss, parts, norm, grad_logits, grad_ld,
+                                 alpha_kl, alpha_l1, rest != 0, nullptr, loss, parts, norm, grad_logits, grad_ld, stuck,
                                  workspace, (cudaStream_t)stream);
   return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, "distillation loss launch");
 }
@@ -785,7 +789,7 @@ dspark_status dspark_distill_grad(int N, int V, float T, dspark_dtype zdt, const
   if (!norm || !grad_loss || !grad_logits)
     return fail(DSPARK_ERR_INVALID, "norm, grad_loss and grad_logits are required");
   cudaError_t e = launch_distill(N, V, T, zdt == DSPARK_BF16, logits, ld, K, teacher_ids, teacher_logp, grad_loss,
-                                 alpha_kl, alpha_l1, rest != 0, norm, nullptr, nullptr, nullptr, grad_logits, grad_ld,
+                                 alpha_kl, alpha_l1, rest != 0, norm, nullptr, nullptr, nullptr, grad_logits, grad_ld, 0,
                                  workspace, (cudaStream_t)stream);
   return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, "distillation gradient launch");
 }

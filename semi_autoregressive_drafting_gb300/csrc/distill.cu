@@ -9,9 +9,18 @@
 // The rest has a maximum and a sum of its own, P_v = exp((z_v - m_r) / T - ln S_r): no difference of two sums
 // near one is formed, and a rest that is far below the row's maximum keeps its digits.
 //
-// Forward: a warp takes a 4 KB segment of a row, puts -inf in place of the row's own tokens, and leaves the
-// segment's maximum and sum; a second launch, one block per row, joins them, fetches the K logits and forms
-// the outcomes.  The gradient is a third pass.
+// Loss with gradient: a cluster of blocks reads a row once into their shared memory (bulk copies), puts -inf in place
+// of the row's own tokens, forms the maximum and sum of each 4 KB segment, exchanges them (distributed shared
+// memory), forms the outcomes and writes the gradient: each logit crosses HBM once each way.  Rows that no cluster
+// holds (above 3.2 MB), and the loss alone: a warp takes a segment in registers, a second launch with one block per
+// row joins the segments and forms the outcomes, and a third, for the gradient, reads the row again.  Both form the
+// same sums in the same order.  The gradient of given normalisers is the last two of these.
+//
+// 3584 x 262144 bf16, 64 tokens: 740 us (5.1 TB/s; three passes would be 850), bound by what is resident: 24 of 28 MB
+// of shared memory hold rows, for 11 us each, of which the loads take 3, the sums 2, the exchange and the outcomes
+// 4 and the gradient 2.5 (resident clusters that load the next row behind the gradient: 838; blocks of half the
+// size, twice as many: 1010).  448 x 151936 fp32: 116 us (4.7 TB/s).  The gradient alone: 540 and 84 us (6.95 and 6.5
+// TB/s); the loss alone, 499 x 50021 fp32: 28 us, two launches.  The teacher's part is hidden behind the loads.
 #include "common.cuh"
 #include "kernels.h"
 #include "rows.cuh"
@@ -39,7 +48,7 @@ struct RowCoef {
 };
 
 struct DsArgs {
-  int V, K, nchunk, rest;
+  int V, K, nchunk, rest, stuck;
   float T, invT, invT_lo, a_kl, a_l1;
   long long ld, gld;
   const int32_t* ids;
@@ -538,7 +547,7 @@ __global__ void __launch_bounds__(kThr, kChipBlocks)
   }
   __syncthreads();
   // (a wait that runs out: once more, so that nothing is in flight at the end)
-  bool ok = mbar_wait(&sm.full, 0u);
+  bool ok = !a.stuck && mbar_wait(&sm.full, 0u);
   if (!ok) ok = mbar_wait(&sm.full, 0u) && false;
   asm volatile("barrier.cluster.wait;" ::: "memory");
   // the row's own tokens out of the rest
@@ -786,13 +795,14 @@ size_t distill_workspace_bytes(int N, int V, int K) {
 cudaError_t launch_distill(int N, int V, float T, int bf16, const void* logits, long long ld, int K,
                            const int32_t* ids, const float* logq, const float* weight, float a_kl, float a_l1,
                            int rest, const float* norm_in, float* loss, float* parts, float* norm, void* grad,
-                           long long gld, void* workspace, cudaStream_t stream) {
+                           long long gld, int stuck, void* workspace, cudaStream_t stream) {
   const Ws s = layout(workspace, N, V, K);
   DsArgs a;
   a.V = V;
   a.K = K;
   a.nchunk = 0;
   a.rest = rest;
+  a.stuck = stuck;
   a.T = T;
   a.invT = 1.f / T;
   a.invT_lo = (float)(1.0 / (double)T - (double)a.invT);

@@ -61,6 +61,6 @@ size_t distill_workspace_bytes(int N, int V, int K);
 cudaError_t launch_distill(int N, int V, float T, int bf16, const void* logits, long long ld, int K,
                            const int32_t* ids, const float* logq, const float* weight, float a_kl, float a_l1,
                            int rest, const float* norm_in, float* loss, float* parts, float* norm, void* grad,
-                           long long gld, void* workspace, cudaStream_t stream);
+                           long long gld, int stuck, void* workspace, cudaStream_t stream);
 
 }  // namespace dspark

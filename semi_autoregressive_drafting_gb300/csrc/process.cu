@@ -7,12 +7,18 @@
 //   -inf where the mask's bit of v is clear.
 //   dL/dz = dL/dy (1 / rho if z > 0 else rho, where seen), 0 where masked.
 //
-// A block takes a slice of the vocabulary for all rows of a request.  It counts the text's tokens of its slice in
-// shared memory (each block reads the whole text, from L2; nothing waits for an atomic's answer), copies its
-// entries of every row, masked, in 16- and 32-byte pieces, and then writes the touched entries again: a bit for
-// each entry says which, warps list those bits, and a lane takes an (entry, row) pair, so that the entries that no
-// text and no bias touches cost a copy.  Patching them in the copying lanes instead, where a warp waits for each
-// other's branches, took 2 to 3 times as long (64 x 8 x 151936: 268 us against 97).
+// A block takes a slice of the vocabulary for all rows of a request.  Its warps count the text's tokens of the slice in
+// shared memory (each block reads the whole text, from L2; nothing waits for an atomic's answer) and set a bit for
+// each entry that the text or a bias touches.  Then they copy units of 64 bytes per lane, masked, in 16- and 32-byte
+// pieces; entries that a mask rules out are not read.  A warp lists its unit's touched entries, and a lane takes one
+// of them, whose line is still in the L1: the entries that no text touches cost a copy.  (Patching them in the lane
+// that copies them, where a warp waits for each other's branches, took 3 times as long.)  The gradient writes its
+// touched entries after the whole slice, in (entry, row) pairs, since they also wait for the raw logits.
+//
+// HBM bounds the copy: 64 x 8 x 151936 bf16 rows to fp32 take 77 us (6.1 TB/s) without a text, and 93 with texts of
+// 4096 tokens on average (5.0 TB/s): the counting, the lists and the entries written twice are instructions (61 % of
+// the issue slots) and latency.  512 x 151936 fp32 rows, three quarters of them masked, 117 us (4.3 TB/s); without
+// text and mask 96 (6.5 TB/s).  Roles for warps in resident blocks (some copy, some count ahead) reached 97 and 139.
 #include "common.cuh"
 #include "kernels.h"
 #include "rows.cuh"
@@ -22,19 +28,20 @@
 namespace dspark {
 namespace {
 
-constexpr int kThr = 256, kBlocks = 5;     // threads of a block, blocks per SM
-constexpr int kSlice = 4096;               // entries of a block's slice, with several rows
-constexpr int kSliceOne = 8192;            // with one
-constexpr int kLong = 24576, kThrLong = 1024, kSliceLong = 16384;   // texts of this many tokens per row
-constexpr int kChunk = 512;                // entries that a warp looks through for touched ones; slices are multiples
-constexpr int kMostBias = 1024;
-constexpr int kMostSmem = kSliceLong * 4 + kSliceLong / 8 + kMostBias * 6;
+constexpr int kThr = 256;                  // threads of a block
+// Blocks per SM and entries of a slice: a block's life is a chain of latencies (the request's numbers, its text, the
+// logits, the touched ones), which the other blocks' copies and a larger slice hide; slices much larger leave few
+// blocks, and five blocks leave a thread too few registers to copy and list.  512 x 1 rows: 128 us with slices of
+// 8192, 117 with 16384; 64 x 8 rows: 98 with 4096, 93 with 8192, 114 with 12288, 151 with five blocks.  The gradient,
+// 512 x 7 rows: 690 us with four blocks, 640 with five, 727 with six.
+constexpr int kBlocks = 4, kBlocksGrad = 5;
+constexpr int kSlice = 8192, kSliceOne = 16384;   // with several rows, with one
+// Texts of this many tokens per row go to blocks of more threads and larger slices, which read them fewer times
+// (8 requests with texts of up to 131072: 22 us, with small blocks 51).
+constexpr int kLong = 24576, kThrLong = 1024, kSliceLong = 16384;
+constexpr int kChunk = 256;                // entries that a warp looks through for touched ones, in the gradient
+constexpr int kListed = 128;               // touched entries of a unit that a warp lists at a time
 constexpr int kMaxRows = 32;               // rows of a block at most
-constexpr uint32_t kSeen = 1u << 31;       // the prompt holds the token
-constexpr uint32_t kDrafted = 1u << 30;    // one of the drafted tokens
-constexpr uint32_t kBiased = 1u << 29;
-constexpr uint32_t kCount = kBiased - 1u;  // how often the generated part of the history holds it
-
 struct PrArgs {
   int R, V, S, nslice, H, nb, M;
   long long in_ld, out_ld, raw_ld, history_ld, mask_ld;
@@ -170,33 +177,62 @@ __device__ __forceinline__ float one_entry(float x, float raw, bool seen, int c,
   return biased ? y + bias : y;
 }
 
-// A block's slice [s0, s0 + n) of the vocabulary, in shared memory: how often the text holds each token, and
-// the bits of those that a text or a bias touches.
+// How often a text generates each token is counted in 16 bits where no text is longer than that, else in 32; the
+// gradient needs no counts.  (What shared memory the blocks of an SM take is missing in its L1, where the loads on
+// their way have their places: with 205 KB of it taken a copy of 77 us took 97.)
+enum Count { kNoCount, kCount16, kCount32 };
+
+// A block's slice [s0, s0 + n) of the vocabulary, in shared memory.
+template <int COUNT>
 struct Slice {
-  uint32_t* count;    // [S]
-  uint32_t* touched;  // [S / 32]
-  float* bias;        // [nb] the sums of the slice's biased tokens
+  uint32_t* touched;  // [S / 32] bits: what a text touches
+  uint32_t* text;     // [S / 32] tokens of the prompt (without counts: of the history)
+  uint32_t* drafted;  // [S / 32] tokens that are drafted
+  uint32_t* biased;   // [S / 32]
+  uint32_t* count;    // [S / 2] or [S]
+  float* bias;        // [nb] the sums of the biased tokens
   uint16_t* bias_u;   // [nb] those tokens, each once
   int s0, n;
-  // (nothing waits for the old values; a flag stays once set, and a count cannot reach it)
-  __device__ __forceinline__ void add(int u, uint32_t flag) const {
-    if (flag)
-      atomicOr(&count[u], flag);
+  static constexpr int kPer32 = 4 * 4 + (COUNT == kCount16 ? 64 : COUNT == kCount32 ? 128 : 0);   // bytes for 32 entries
+  __device__ __forceinline__ Slice(uint8_t* smem, int S, int nb, int V, int slice) {
+    const int words = S / 32;
+    touched = (uint32_t*)smem;
+    text = touched + words;
+    drafted = text + words;
+    biased = drafted + words;
+    count = biased + words;
+    bias = (float*)(smem + (size_t)words * kPer32);
+    bias_u = (uint16_t*)(bias + nb);
+    s0 = slice * S;
+    n = min(S, V - s0);
+  }
+  static __device__ __forceinline__ bool is(const uint32_t* bits, int u) { return (bits[u >> 5] >> (u & 31)) & 1u; }
+  // (nothing waits for the old values)
+  static __device__ __forceinline__ void set(uint32_t* bits, int u) { atomicOr(&bits[u >> 5], 1u << (u & 31)); }
+  __device__ __forceinline__ void add(int u, bool prompt) const {
+    if (COUNT == kNoCount || prompt)
+      set(text, u);
+    else if (COUNT == kCount16)
+      atomicAdd(&count[u >> 1], 1u << (16 * (u & 1)));
     else
       atomicAdd(&count[u], 1u);
-    atomicOr(&touched[u >> 5], 1u << (u & 31));
+    set(touched, u);
+  }
+  __device__ __forceinline__ int times(int u) const {
+    return COUNT == kNoCount ? 0 : COUNT == kCount16 ? (int)((const uint16_t*)count)[u] : (int)count[u];
   }
 };
 
 // Counts a text of L tokens, the first P of them the prompt, by the block's threads.  Returns the largest token + 1 as
 // an unsigned number, of this thread's share: above V when a token is outside [-1, V).
-__device__ __forceinline__ uint32_t count_text(const Slice& sl, const int32_t* h, int L, int P) {
+template <int COUNT>
+__device__ __forceinline__ uint32_t count_text(const Slice<COUNT>& sl, const int32_t* h, int L, int P) {
   uint32_t most = 0u;
   const int tid = (int)threadIdx.x, nthr = (int)blockDim.x;
   auto one = [&](int i, int t) {
     most = max(most, (uint32_t)(t + 1));
     const int u = t - sl.s0;
-    if ((unsigned)u < (unsigned)sl.n) sl.add(u, i < P ? kSeen : 0u);
+    if ((unsigned)u < (unsigned)sl.n) sl.add(u, i < P);
   };
   const int head = min(L, (int)((16 - ((uintptr_t)h & 15)) & 15) >> 2);   // up to a 16-byte boundary
   const int n4 = (L - head) >> 2;
@@ -222,7 +258,8 @@ __device__ __forceinline__ uint32_t count_text(const Slice& sl, const int32_t* h
 
 // One warp: the slice's biases, those of one token in the list's order: a step of 32 entries at a time, the
 // entries of a token in one step added by the first of them.  n: how many tokens have some.
-__device__ __forceinline__ uint32_t add_biases(const Slice& sl, const int32_t* tokens, const float* bias, int nb,
+template <int COUNT>
+__device__ __forceinline__ uint32_t add_biases(const Slice<COUNT>& sl, const int32_t* tokens, const float* bias, int nb,
                                                int* n) {
   uint32_t most = 0u;
   const int lane = (int)(threadIdx.x & 31);
@@ -238,7 +275,7 @@ __device__ __forceinline__ uint32_t add_biases(const Slice& sl, const int32_t* t
     const uint32_t peers = __match_any_sync(0xffffffffu, mine ? u : -1 - lane);
     const bool first = mine && lane == __ffs(peers) - 1;
     int slot = -1;   // of an earlier step
-    if (first && (sl.count[u] & kBiased))
+    if (first && sl.is(sl.biased, u))
       for (slot = 0; sl.bias_u[slot] != u;) ++slot;
     float sum = slot >= 0 ? sl.bias[slot] : 0.f;
     for (; todo; todo &= todo - 1) {
@@ -250,7 +287,8 @@ __device__ __forceinline__ uint32_t add_biases(const Slice& sl, const int32_t* t
     if (first && slot < 0) {
       slot = have + __popc(fresh & ((1u << lane) - 1u));
       sl.bias_u[slot] = (uint16_t)u;
-      atomicOr(&sl.count[u], kBiased);
+      sl.set(sl.biased, u);
+      sl.set(sl.touched, u);
     }
     if (first) sl.bias[slot] = sum;
     have += __popc(fresh);
@@ -263,23 +301,18 @@ __device__ __forceinline__ uint32_t add_biases(const Slice& sl, const int32_t* t
 // TI: the input's type; TO: the output's; GRAD: the input is dL/dy and the raw logits have the output's type.
 // units: what a warp copies at a time (64 bytes per lane of one row), per row of the slice.  A warp counts its
 // share of the text, then takes units until none is left.
-template <typename TI, typename TO, bool GRAD, int THR>
-__global__ void __launch_bounds__(THR, THR == kThr ? kBlocks : 1)
+template <typename TI, typename TO, bool GRAD, int COUNT, int THR>
+__global__ void __launch_bounds__(THR, THR != kThr ? 1 : GRAD ? kBlocksGrad : kBlocks)
     process_kernel(const TI* in, TO* out, const TO* raw, const PrArgs a, const int units, const bool same) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int s_next, s_biased;
+  __shared__ int s_next, s_biased, s_bad;
+  __shared__ uint64_t s_counted;
   __shared__ int s_drafted[kMaxRows];
-  __shared__ uint16_t s_list[THR / 32][kChunk];
+  __shared__ uint16_t s_list[THR / 32][GRAD ? kChunk / 2 : kListed];
   __shared__ int s_mask[kMaxRows];   // the rows' masks (-1: none, -2: not a row of the mask)
   const int b = (int)(blockIdx.x / (unsigned)a.nslice);
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  Slice sl;
-  sl.count = (uint32_t*)smem;
-  sl.touched = sl.count + a.S;
-  sl.bias = (float*)(sl.touched + a.S / 32);
-  sl.bias_u = (uint16_t*)(sl.bias + a.nb);
-  sl.s0 = (int)(blockIdx.x % (unsigned)a.nslice) * a.S;
-  sl.n = min(a.S, a.V - sl.s0);
+  const Slice<COUNT> sl(smem, a.S, a.nb, a.V, (int)(blockIdx.x % (unsigned)a.nslice));
   const int s0 = sl.s0, s1 = sl.s0 + sl.n;
   const float rho = a.repetition ? __ldg(a.repetition + b) : 1.f;
   const float pres = !GRAD && a.presence ? __ldg(a.presence + b) : 0.f;
@@ -292,8 +325,12 @@ __global__ void __launch_bounds__(THR, THR == kThr ? kBlocks : 1)
     s_drafted[tid] = a.drafted && tid < a.R - 1 ? __ldg(a.drafted + (long long)b * (a.R - 1) + tid) : -1;
   }
   const bool biased = !GRAD && a.nb > 0;
-  for (int i = tid; i < (a.S + a.S / 32) / 4; i += THR) ((uint4*)smem)[i] = make_uint4(0u, 0u, 0u, 0u);
-  if (tid == 0) s_next = s_biased = 0;
+  for (int i = tid; i < a.S / 32 * (sl.kPer32 / 16); i += THR) ((uint4*)smem)[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (tid == 0) {
+    s_next = s_biased = s_bad = 0;
+    mbar_init(&s_counted, THR / 32);
+    fence_mbar_init();
+  }
   const bool penalised = rho != 1.f || pres != 0.f || freq != 0.f, any = penalised || biased;
   __syncthreads();
 
@@ -309,12 +346,22 @@ __global__ void __launch_bounds__(THR, THR == kThr ? kBlocks : 1)
       if (tid < a.R - 1) {   // (R <= 32: the first warp)
         const int t = s_drafted[tid], u = t - s0;
         most = max(most, (uint32_t)(t + 1));
-        if ((unsigned)u < (unsigned)sl.n) sl.add(u, kDrafted);
+        if ((unsigned)u < (unsigned)sl.n) {
+          sl.set(sl.drafted, u);
+          sl.set(sl.touched, u);
+        }
       }
     }
   }
 
-  // the copy, masked; touched entries are written again below
+  if (!GRAD && any) {
+    if (most > (uint32_t)a.V) s_bad = 1;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s_counted);
+  }
+
+  // the copy, masked
+  bool counted = false, wrong = false;
   using W = typename std::conditional<sizeof(TO) == 2, uint16_t, uint32_t>::type;
   const uint32_t fill = GRAD ? 0u : sizeof(TO) == 2 ? 0xFF80FF80u : 0xFF800000u;
   const uint32_t nan = sizeof(TO) == 2 ? 0x7FFF7FFFu : 0x7FFFFFFFu;
@@ -326,7 +373,7 @@ __global__ void __launch_bounds__(THR, THR == kThr ? kBlocks : 1)
     const int r = unit / units;
     if (r >= a.R) break;
     const int m = s_mask[r];
-    if (same && m == -1) continue;
+    if (same && m == -1 && (GRAD || !any)) continue;
     const long long row = (long long)b * a.R + r;
     const TI* z = in + row * a.in_ld;
     TO* o = out + row * a.out_ld;
@@ -354,7 +401,7 @@ __global__ void __launch_bounds__(THR, THR == kThr ? kBlocks : 1)
         if (same && bits[i] == 0xFFu) continue;
         Raw<TO> y;
         convert8(y, x[i]);
-        mask8(y, bits[i], m == -2 ? nan : fill);
+        if (mask || m == -2) mask8(y, bits[i], m == -2 ? nan : fill);
         store8(o + v0, y);
       } else {
 #pragma unroll 1
@@ -366,7 +413,66 @@ __global__ void __launch_bounds__(THR, THR == kThr ? kBlocks : 1)
         }
       }
     }
+    if constexpr (!GRAD) {
+      if (!any || m == -2) continue;
+      __syncwarp();   // (the warp's stores before those below)
+      if (!counted) {
+        // (the wait ends: no warp waits before it has arrived; one that ran out would be told by NaN)
+        wrong = !mbar_wait_warp(&s_counted, 0u) || s_bad;
+        counted = true;
+      }
+      const int u00 = v00 - lane * 8, va = max(u00, s0), vb = min(u00 + 256 * kDepth, s1);   // the unit's entries
+      if (wrong) {
+        for (int v = va + lane; v < vb; v += 32) o[v] = from_f<TO>(NAN);
+        continue;
+      }
+      // the unit's touched entries, kListed at a time: 32 entries' bits per lane make a list, a lane takes one of it
+      uint16_t* list = s_list[warp];
+      for (int w0 = (va - s0) >> 5; w0 * 32 < vb - s0; w0 += 32) {
+        const int e0 = (w0 + lane) * 32 + s0;   // the lane's first entry
+        uint32_t t = e0 < vb ? sl.touched[w0 + lane] : 0u;
+        if (e0 < va) t &= 0xFFFFFFFFu << (va - e0);
+        if (t && vb - e0 < 32) t &= (1u << (vb - e0)) - 1u;
+        if (mask && t) t &= __ldg(mask + (e0 >> 5));   // (slices begin at whole words)
+        if (!__any_sync(0xffffffffu, t != 0u)) continue;
+        const int mine = __popc(t);
+        int at = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, at, d);
+          if (lane >= d) at += y;
+        }
+        const int all = __shfl_sync(0xffffffffu, at, 31);
+        at -= mine;
+        for (int base = 0; base < all; base += kListed) {
+          int k = at - base;
+          for (uint32_t bits = t; bits; bits &= bits - 1u, ++k)
+            if ((unsigned)k < (unsigned)kListed) list[k] = (uint16_t)(e0 - s0 + __ffs(bits) - 1);
+          __syncwarp();
+          for (int i = lane; i < min(all - base, kListed); i += 32) {
+            const int u = list[i], v = s0 + u;
+            const float f = to_f<TI>(z[v]);
+            int n = sl.times(u);
+            bool seen = n > 0 || sl.is(sl.text, u);
+            if (r > 0 && sl.is(sl.drafted, u))
+              for (int d = 0; d < r; ++d)
+                if (s_drafted[d] == v) {
+                  ++n;
+                  seen = true;
+                }
+            float bias = 0.f;
+            const bool has = biased && sl.is(sl.biased, u);
+            if (has)
+              for (int j = 0; j < s_biased; ++j)
+                if (sl.bias_u[j] == u) bias = sl.bias[j];
+            if (seen || has) o[v] = from_f<TO>(one_entry<GRAD>(f, f, seen, n, rho, pres, freq, has, bias));
+          }
+          __syncwarp();
+        }
+      }
+    }
   }
+  if constexpr (!GRAD) return;
   const bool bad = __syncthreads_or(most > (uint32_t)a.V);
   if (bad) {
     for (int r = 0; r < a.R; ++r)
@@ -394,24 +500,24 @@ __global__ void __launch_bounds__(THR, THR == kThr ? kBlocks : 1)
 #pragma unroll
     for (int j = 0; j < kDeep; ++j) {
       if (!on[j]) continue;
-      const uint32_t w = sl.count[v[j] - s0];
-      int n = (int)(w & kCount);
-      bool seen = (w & (kSeen | kCount)) != 0u;
-      if (w & kDrafted)
+      const int u = v[j] - s0;
+      int n = sl.times(u);
+      bool seen = n > 0 || sl.is(sl.text, u);
+      if (sl.is(sl.drafted, u))
         for (int d = 0; d < r[j]; ++d)
           if (s_drafted[d] == v[j]) {
             ++n;
             seen = true;
           }
-      if ((seen || mine) && mine == ((w & kBiased) != 0u))
+      if ((seen || mine) && mine == (biased && sl.is(sl.biased, u)))
         out[((long long)b * a.R + r[j]) * a.out_ld + v[j]] =
             from_f<TO>(one_entry<GRAD>(f[j], g[j], seen, n, rho, pres, freq, mine, bias[j]));
     }
   };
   // a warp lists the entries of kChunk that the text touches, then takes them in (entry, row) pairs
-  uint16_t* list = s_list[warp];
+  uint8_t* list = (uint8_t*)s_list[warp];
   for (int c = warp; c * kChunk < sl.n; c += THR / 32) {
-    uint32_t w = ((const uint16_t*)sl.touched)[c * 32 + lane];
+    uint32_t w = ((const uint8_t*)sl.touched)[c * 32 + lane];
     int all = __popc(w), at = all;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -420,7 +526,7 @@ __global__ void __launch_bounds__(THR, THR == kThr ? kBlocks : 1)
     }
     at -= all;
     all = __shfl_sync(0xffffffffu, at + all, 31);
-    for (; w; w &= w - 1) list[at++] = (uint16_t)(lane * 16 + __ffs(w) - 1);
+    for (; w; w &= w - 1) list[at++] = (uint8_t)(lane * 8 + __ffs(w) - 1);
     __syncwarp();
     const int pairs = all * a.R;
     for (int i0 = lane; i0 - lane < pairs; i0 += 32 * kDeep) {
@@ -453,20 +559,19 @@ __global__ void __launch_bounds__(THR, THR == kThr ? kBlocks : 1)
 }
 
 // Slices of at most S entries, smaller ones where that gives every SM its blocks.
-template <typename TI, typename TO, bool GRAD, int THR>
+template <typename TI, typename TO, bool GRAD, int COUNT, int THR>
 cudaError_t launch(int B, const TI* in, TO* out, const TO* raw, PrArgs a, int S, int blocks, cudaStream_t stream) {
   const long long even = ((long long)B * a.V + blocks - 1) / blocks;
-  if (even < S) S = (int)((even + kChunk - 1) / kChunk) * kChunk;
+  if (even < S) S = (int)((even + kChunk * 2 - 1) / (kChunk * 2)) * (kChunk * 2);
   a.S = S;
   a.nslice = (a.V + S - 1) / S;
   constexpr int unit = 32 * (64 / (int)sizeof(Raw<TI>));   // groups
   const bool al = ((uintptr_t)out % (8 * sizeof(TO))) == 0 && (a.out_ld * sizeof(TO)) % (8 * sizeof(TO)) == 0;
   const int units = (S / 8 + (al ? 0 : 1) + unit - 1) / unit;
-  const size_t smem = (size_t)S * 4 + S / 8 + (size_t)a.nb * 6;
-  auto kernel = process_kernel<TI, TO, GRAD, THR>;
-  // (beside the lists: 48 KB are exceeded by long slices, and by the larger blocks)
-  if (S > kSlice || THR > kThr) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
+  const size_t smem = (size_t)S / 32 * Slice<COUNT>::kPer32 + (size_t)a.nb * 6;
+  auto kernel = process_kernel<TI, TO, GRAD, COUNT, THR>;
+  if (smem > 32 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
     if (e != cudaSuccess) return e;
   }
   kernel<<<(unsigned)B * (unsigned)a.nslice, THR, smem, stream>>>(in, out, raw, a, units,
@@ -477,9 +582,19 @@ cudaError_t launch(int B, const TI* in, TO* out, const TO* raw, PrArgs a, int S,
 // Long texts of few rows: large slices read them fewer times, by blocks of more threads.
 template <typename TI, typename TO, bool GRAD>
 cudaError_t run(int B, const TI* in, TO* out, const TO* raw, PrArgs a, cudaStream_t stream) {
-  if (GRAD) a.nb = 0;
-  if (a.H / a.R >= kLong) return launch<TI, TO, GRAD, kThrLong>(B, in, out, raw, a, kSliceLong, 152, stream);
-  return launch<TI, TO, GRAD, kThr>(B, in, out, raw, a, a.R > 1 ? kSlice : kSliceOne, 304, stream);
+  const bool wide = a.H + a.R > 65535;
+  if (GRAD) {
+    a.nb = 0;
+    if (a.H / a.R >= kLong) return launch<TI, TO, GRAD, kNoCount, kThrLong>(B, in, out, raw, a, kSliceLong, 152, stream);
+    return launch<TI, TO, GRAD, kNoCount, kThr>(B, in, out, raw, a, kSlice, 304, stream);
+  }
+  constexpr int C16 = GRAD ? kNoCount : kCount16, C32 = GRAD ? kNoCount : kCount32;
+  if (a.H / a.R >= kLong)
+    return wide ? launch<TI, TO, GRAD, C32, kThrLong>(B, in, out, raw, a, kSliceLong, 152, stream)
+                : launch<TI, TO, GRAD, C16, kThrLong>(B, in, out, raw, a, kSliceLong, 152, stream);
+  const int S = a.R > 1 ? kSlice : kSliceOne;
+  return wide ? launch<TI, TO, GRAD, C32, kThr>(B, in, out, raw, a, S, 304, stream)
+              : launch<TI, TO, GRAD, C16, kThr>(B, in, out, raw, a, S, 304, stream);
 }
 
 template <bool GRAD>

@@ -348,6 +348,33 @@ def test_gradient_is_the_slope():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,R,V,H,nb", [(1, 1, 5000, 30000, 0), (2, 1, 40001, 70000, 40), (1, 2, 3000, 60000, 5),
+                                        (3, 4, 9000, 66000, 3)])
+def test_long_texts(B, R, V, H, nb):
+    # texts that are counted in 16 and in 32 bits, by blocks of both sizes
+    z, x = make(B, R, V, H, seed=H, nb=nb, masked=2)
+    x["lengths"][0] = H
+    x["history"][0, :] = 17                                          # one token tens of thousands of times
+    x["history"][0, ::3] = V - 1
+    check(z, x)
+    w = {k: v for k, v in x.items() if k not in ("presence", "frequency", "bias", "bias_tokens")}
+    g = torch.randn(B, R, V, generator=torch.Generator().manual_seed(9))
+    want, tol, _, _ = reference(z, w, grad=g)
+    same(ds.process_logits_grad(g.cuda(), z.cuda(), **dev(w)), want, tol * 1.01)
+
+
+@pytest.mark.gpu
+def test_many_biases_of_one_slice_and_repeats_across_steps():
+    V, nb = 3000, 1024
+    g = torch.Generator().manual_seed(2)
+    z = torch.randn(2, 2, V, generator=g)
+    x = dict(bias_tokens=torch.randint(-1, 300, (2, nb), generator=g, dtype=torch.int32), bias=torch.randn(2, nb, generator=g),
+             history=torch.randint(0, 600, (2, 50), generator=g, dtype=torch.int32), frequency=torch.tensor([0.5, 0.0]))
+    a = check(z, x)
+    assert torch.equal(a, ds.process_logits(z.cuda(), **dev(x)))
+
+
+@pytest.mark.gpu
 def test_offsets_past_32_bits():
     V, R = 1 << 24, 1
     B = 131                                                            # B V > 2^31 entries
