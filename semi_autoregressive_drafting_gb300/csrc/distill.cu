@@ -569,6 +569,8 @@ __global__ void __launch_bounds__(kThr, kChipBlocks)
   }
   cluster_sync_all();
   const int nseg = (s.ngroups + kGroups - 1) / kGroups;
+  if (!ok && tid == 0) atomicMax(&a.hdr->status, kErrTimeout);
+  if (!grad && !(warp == 1 && rank == 0)) return;   // (the loss alone)
   if (warp == 0 || (warp == 1 && rank == 0)) {
     Outcomes y;
     if (w != 0.f) row_sums<true>(y, sm.row, a, row, part, nseg);
@@ -587,21 +589,33 @@ __global__ void __launch_bounds__(kThr, kChipBlocks)
       row_zero(a, row);
     }
   }
-  if (!ok && tid == 0) atomicMax(&a.hdr->status, kErrTimeout);
+  if (!grad) return;
   __syncthreads();
   const RowCoef c = sm.coef;
-  const bool same = row_head((const T*)o) == s.head, none = c.c == 0.f;   // (zeros, whatever the entries are)
-  for (int g = s.ga + tid; g < s.gb; g += kThr) {
-    const int v0 = g * E - s.head;
-    const uint4 q = none ? make_uint4(0u, 0u, 0u, 0u) : grad16<T>(buf[g - s.ga], c, s2);
-    if (same && v0 >= 0 && v0 + E <= a.V) {
+  // 16-byte groups on the output's boundaries: the buffer's own, or entries from any place of it
+  const T* entries = (const T*)buf + (s.head - s.ga * E);   // entry v at [v]
+  const int ohead = row_head((const T*)o), e0 = max(s.va, 0), e1 = s.vb;
+  const bool same = ohead == s.head, none = c.c == 0.f;   // (zeros, whatever the entries are)
+  for (int v0 = (e0 + ohead) / E * E - ohead + tid * E; v0 < e1; v0 += kThr * E) {
+    const bool whole = v0 >= e0 && v0 + E <= e1;
+    uint4 q;
+    if (same) {
+      q = *(const uint4*)(entries + v0);
+    } else {
+      T f[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] = whole || (v0 + e >= e0 && v0 + e < e1) ? entries[v0 + e] : from_f<T>(0.f);
+      memcpy(&q, f, 16);
+    }
+    q = none ? make_uint4(0u, 0u, 0u, 0u) : grad16<T>(q, c, s2);
+    if (whole) {
       __stcs((uint4*)(o + v0), q);
     } else {
       T f[E];
       memcpy(f, &q, 16);
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if (v0 + e >= 0 && v0 + e < a.V) o[v0 + e] = f[e];
+        if (v0 + e >= e0 && v0 + e < e1) o[v0 + e] = f[e];
     }
   }
   __syncthreads();
@@ -657,6 +671,9 @@ __global__ void __launch_bounds__(kThr) distill_grad_kernel(const T* logits, T* 
       o[id[i]] = from_f<T>(__ldcg(a.at + row * a.K + i * 32 + lane));
 }
 
+// The loss alone: one launch on the chip for up to 64 MB of logits, else two (64 x 47358 fp32 rows 7.0 us and 11.9,
+// 2000 x 8000 bf16 20 and 25, 448 x 151936 fp32 63 and 50).
+constexpr int kFewSegs = 16384;
 // Segments of a block's share of a row: 64 KB, three blocks per SM, and as many as its shared memory holds; blocks
 // of a cluster at most; blocks for every SM.
 constexpr int kSegs = 16, kMostSegs = 50, kMostC = 16, kFill = 152;
@@ -774,7 +791,7 @@ cudaError_t run(int N, const T* logits, T* grad, const DsArgs& a, cudaStream_t s
     e = cudaGetLastError();
   } else {
     const int nseg = (a.V + (al_rows ? 0 : Lg<T>::E - 1) + kSegEntries<T> - 1) / kSegEntries<T>;
-    if (grad && nseg <= kMostC * kMostSegs) {
+    if ((grad || (long long)N * nseg <= kFewSegs) && nseg <= kMostC * kMostSegs) {
       ChipShape shape;
       e = chip_shape<T>(nseg, &shape);
       if (e != cudaSuccess) return e;

@@ -15,9 +15,9 @@
 // that copies them, where a warp waits for each other's branches, took 3 times as long.)  The gradient writes its
 // touched entries after the whole slice, in (entry, row) pairs, since they also wait for the raw logits.
 //
-// HBM bounds the copy: 64 x 8 x 151936 bf16 rows to fp32 take 77 us (6.1 TB/s) without a text, and 93 with texts of
-// 4096 tokens on average (5.0 TB/s): the counting, the lists and the entries written twice are instructions (61 % of
-// the issue slots) and latency.  512 x 151936 fp32 rows, three quarters of them masked, 117 us (4.3 TB/s); without
+// HBM bounds the copy: 64 x 8 x 151936 bf16 rows to fp32 take 77 us (6.1 TB/s) without a text, and 84 with texts of
+// 4096 tokens on average (5.5 TB/s): the counting, the lists and the entries written twice are instructions (61 % of
+// the issue slots) and latency.  512 x 151936 fp32 rows, three quarters of them masked, 112 us (4.5 TB/s); without
 // text and mask 96 (6.5 TB/s).  Roles for warps in resident blocks (some copy, some count ahead) reached 97 and 139.
 #include "common.cuh"
 #include "kernels.h"
@@ -33,12 +33,13 @@ constexpr int kThr = 256;                  // threads of a block
 // logits, the touched ones), which the other blocks' copies and a larger slice hide; slices much larger leave few
 // blocks, and five blocks leave a thread too few registers to copy and list.  512 x 1 rows: 128 us with slices of
 // 8192, 117 with 16384; 64 x 8 rows: 98 with 4096, 93 with 8192, 114 with 12288, 151 with five blocks.  The gradient,
-// 512 x 7 rows: 690 us with four blocks, 640 with five, 727 with six.
+// 512 x 7 rows: 690 us with four blocks, 631 with five, 727 with six.
 constexpr int kBlocks = 4, kBlocksGrad = 5;
 constexpr int kSlice = 8192, kSliceOne = 16384;   // with several rows, with one
-// Texts of this many tokens per row go to blocks of more threads and larger slices, which read them fewer times
-// (8 requests with texts of up to 131072: 22 us, with small blocks 51).
-constexpr int kLong = 24576, kThrLong = 1024, kSliceLong = 16384;
+// Where a text may have this many tokens for each entry that a block copies, its blocks have more threads and larger
+// slices, which read it fewer times (8 requests with texts of up to 131072: 22 us, with small blocks 51).
+constexpr int kLong = 3, kThrLong = 1024, kSliceLong = 16384;
+constexpr int kFill = 152, kLeast = 512;   // blocks for every SM; entries of the slices that this makes, in multiples
 constexpr int kChunk = 256;                // entries that a warp looks through for touched ones, in the gradient
 constexpr int kListed = 128;               // touched entries of a unit that a warp lists at a time
 constexpr int kMaxRows = 32;               // rows of a block at most
@@ -70,6 +71,21 @@ __device__ __forceinline__ void ld16(uint32_t* w, const void* p) {
   asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
                : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                : "l"(p)
+               : "memory");
+}
+// Eight entries, if `on`, from a boundary of their size.  (A predicate: the loads of a unit are on their way together.)
+__device__ __forceinline__ void load8_if(Raw<float>& x, const float* p, bool on) {
+  asm volatile("{\n.reg .pred q;\nsetp.ne.u32 q, %9, 0;\n"
+               "@q ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n}"
+               : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3]), "=r"(x.w[4]), "=r"(x.w[5]), "=r"(x.w[6]),
+                 "=r"(x.w[7])
+               : "l"(p), "r"((uint32_t)on)
+               : "memory");
+}
+__device__ __forceinline__ void load8_if(Raw<__nv_bfloat16>& x, const __nv_bfloat16* p, bool on) {
+  asm volatile("{\n.reg .pred q;\nsetp.ne.u32 q, %5, 0;\n@q ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n}"
+               : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3])
+               : "l"(p), "r"((uint32_t)on)
                : "memory");
 }
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const Raw<__nv_bfloat16>& x) {
@@ -190,8 +206,8 @@ struct Slice {
   uint32_t* drafted;  // [S / 32] tokens that are drafted
   uint32_t* biased;   // [S / 32]
   uint32_t* count;    // [S / 2] or [S]
-  float* bias;        // [nb] the sums of the biased tokens
-  uint16_t* bias_u;   // [nb] those tokens, each once
+  uint16_t* before;   // [S / 32] 1 + the place in `bias` of the first of a word's biased tokens
+  float* bias;        // [nb] their sums
   int s0, n;
   static constexpr int kPer32 = 4 * 4 + (COUNT == kCount16 ? 64 : COUNT == kCount32 ? 128 : 0);   // bytes for 32 entries
   __device__ __forceinline__ Slice(uint8_t* smem, int S, int nb, int V, int slice) {
@@ -201,8 +217,8 @@ struct Slice {
     drafted = text + words;
     biased = drafted + words;
     count = biased + words;
-    bias = (float*)(smem + (size_t)words * kPer32);
-    bias_u = (uint16_t*)(bias + nb);
+    before = (uint16_t*)(smem + (size_t)words * kPer32);
+    bias = (float*)(before + words);
     s0 = slice * S;
     n = min(S, V - s0);
   }
@@ -217,6 +233,9 @@ struct Slice {
     else
       atomicAdd(&count[u], 1u);
     set(touched, u);
+  }
+  __device__ __forceinline__ int place(int u) const {
+    return before[u >> 5] - 1 + __popc(biased[u >> 5] & ((1u << (u & 31)) - 1u));
   }
   __device__ __forceinline__ int times(int u) const {
     return COUNT == kNoCount ? 0 : COUNT == kCount16 ? (int)((const uint16_t*)count)[u] : (int)count[u];
@@ -256,46 +275,65 @@ __device__ __forceinline__ uint32_t count_text(const Slice<COUNT>& sl, const int
   return most;
 }
 
-// One warp: the slice's biases, those of one token in the list's order: a step of 32 entries at a time, the
-// entries of a token in one step added by the first of them.  n: how many tokens have some.
+// The bits of the slice's biased tokens, by the block's threads; t: entry tid.  in: bits of the entries of the slice.
+// Returns the largest token + 1.
 template <int COUNT>
-__device__ __forceinline__ uint32_t add_biases(const Slice<COUNT>& sl, const int32_t* tokens, const float* bias, int nb,
-                                               int* n) {
+__device__ __forceinline__ uint32_t list_biases(const Slice<COUNT>& sl, const int32_t* tokens, int nb, int t,
+                                                uint32_t* in) {
   uint32_t most = 0u;
-  const int lane = (int)(threadIdx.x & 31);
-  int t = lane < nb ? __ldg(tokens + lane) : -1, have = 0;
-  for (int i0 = 0; i0 < nb; i0 += 32) {
-    const int i = i0 + lane, next = i + 32 < nb ? __ldg(tokens + i + 32) : -1, u = t - sl.s0;
-    most = max(most, (uint32_t)(t + 1));
+  for (int i = (int)threadIdx.x;;) {
+    const int u = t - sl.s0;
     const bool mine = (unsigned)u < (unsigned)sl.n;
-    t = next;
-    uint32_t todo = __ballot_sync(0xffffffffu, mine);
-    if (!todo) continue;
+    most = max(most, (uint32_t)(t + 1));
+    if (mine) {
+      sl.set(sl.biased, u);
+      sl.set(sl.touched, u);
+    }
+    if (i < nb) sl.bias[i] = 0.f;
+    const uint32_t some = __ballot_sync(0xffffffffu, mine);
+    if ((threadIdx.x & 31) == 0) in[i >> 5] = some;
+    i += (int)blockDim.x;
+    if (i - (int)(threadIdx.x & 31) >= nb) return most;
+    t = i < nb ? __ldg(tokens + i) : -1;
+  }
+}
+
+// One warp: their sums.  Step by step of 32 entries, each word of bits that is met gets places for its tokens, and the
+// biases are added, those of one token in the list's order: the entries of a token in one step by the first of them.
+template <int COUNT>
+__device__ __forceinline__ void add_biases(const Slice<COUNT>& sl, const int32_t* tokens, const float* bias, int nb,
+                                           const uint32_t* in) {
+  const int lane = (int)(threadIdx.x & 31);
+  const uint32_t bits = lane * 32 < nb ? in[lane] : 0u;
+  int places = 0;
+  for (uint32_t steps = __ballot_sync(0xffffffffu, bits != 0u); steps; steps &= steps - 1) {
+    const int step = __ffs(steps) - 1, i = step * 32 + lane;
+    const bool mine = (__shfl_sync(0xffffffffu, bits, step) >> lane) & 1u;
+    const int u = mine ? __ldg(tokens + i) - sl.s0 : -1 - lane;
     const float x = mine ? __ldg(bias + i) : 0.f;
-    const uint32_t peers = __match_any_sync(0xffffffffu, mine ? u : -1 - lane);
+    const uint32_t word = __match_any_sync(0xffffffffu, mine ? u >> 5 : u);
+    const bool opens = mine && lane == __ffs(word) - 1 && sl.before[u >> 5] == 0;
+    const int n = opens ? __popc(sl.biased[u >> 5]) : 0;
+    int at = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, at, d);
+      if (lane >= d) at += y;
+    }
+    if (opens) sl.before[u >> 5] = (uint16_t)(places + at - n + 1);
+    places += __shfl_sync(0xffffffffu, at, 31);
+    __syncwarp();
+    const uint32_t peers = __match_any_sync(0xffffffffu, u);
     const bool first = mine && lane == __ffs(peers) - 1;
-    int slot = -1;   // of an earlier step
-    if (first && sl.is(sl.biased, u))
-      for (slot = 0; sl.bias_u[slot] != u;) ++slot;
-    float sum = slot >= 0 ? sl.bias[slot] : 0.f;
-    for (; todo; todo &= todo - 1) {
+    float sum = first ? sl.bias[sl.place(u)] + x : 0.f;
+    for (uint32_t todo = __ballot_sync(0xffffffffu, mine && !first); todo; todo &= todo - 1) {
       const int j = __ffs(todo) - 1;
       const float y = __shfl_sync(0xffffffffu, x, j);
       if ((peers >> j) & 1u) sum += y;
     }
-    const uint32_t fresh = __ballot_sync(0xffffffffu, first && slot < 0);
-    if (first && slot < 0) {
-      slot = have + __popc(fresh & ((1u << lane) - 1u));
-      sl.bias_u[slot] = (uint16_t)u;
-      sl.set(sl.biased, u);
-      sl.set(sl.touched, u);
-    }
-    if (first) sl.bias[slot] = sum;
-    have += __popc(fresh);
+    if (first) sl.bias[sl.place(u)] = sum;
     __syncwarp();
   }
-  if (lane == 0) *n = have;
-  return most;
 }
 
 // TI: the input's type; TO: the output's; GRAD: the input is dL/dy and the raw logits have the output's type.
@@ -305,7 +343,8 @@ template <typename TI, typename TO, bool GRAD, int COUNT, int THR>
 __global__ void __launch_bounds__(THR, THR != kThr ? 1 : GRAD ? kBlocksGrad : kBlocks)
     process_kernel(const TI* in, TO* out, const TO* raw, const PrArgs a, const int units, const bool same) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int s_next, s_biased, s_bad;
+  __shared__ int s_next, s_bad;
+  __shared__ uint32_t s_in[32];      // which biases are of the slice's tokens (nb <= 1024)
   __shared__ uint64_t s_counted;
   __shared__ int s_drafted[kMaxRows];
   __shared__ uint16_t s_list[THR / 32][GRAD ? kChunk / 2 : kListed];
@@ -325,9 +364,12 @@ __global__ void __launch_bounds__(THR, THR != kThr ? 1 : GRAD ? kBlocksGrad : kB
     s_drafted[tid] = a.drafted && tid < a.R - 1 ? __ldg(a.drafted + (long long)b * (a.R - 1) + tid) : -1;
   }
   const bool biased = !GRAD && a.nb > 0;
-  for (int i = tid; i < a.S / 32 * (sl.kPer32 / 16); i += THR) ((uint4*)smem)[i] = make_uint4(0u, 0u, 0u, 0u);
+  const int32_t* bias_tokens = biased ? a.bias_tokens + (long long)b * a.nb : nullptr;
+  const int t0 = biased && tid < a.nb ? __ldg(bias_tokens + tid) : -1;
+  for (int i = tid; i < a.S / 32 * (sl.kPer32 / 16) + (biased ? a.S / 256 : 0); i += THR)
+    ((uint4*)smem)[i] = make_uint4(0u, 0u, 0u, 0u);
   if (tid == 0) {
-    s_next = s_biased = s_bad = 0;
+    s_next = s_bad = 0;
     mbar_init(&s_counted, THR / 32);
     fence_mbar_init();
   }
@@ -335,9 +377,12 @@ __global__ void __launch_bounds__(THR, THR != kThr ? 1 : GRAD ? kBlocksGrad : kB
   __syncthreads();
 
   uint32_t most = 0u;   // the largest token + 1
+  if (biased) {
+    most = list_biases(sl, bias_tokens, a.nb, t0, s_in);
+    __syncthreads();
+  }
   if (any) {
-    if (biased && warp == 0) most = add_biases(sl, a.bias_tokens + (long long)b * a.nb, a.bias + (long long)b * a.nb, a.nb,
-                                                &s_biased);
+    if (biased && warp == 0) add_biases(sl, bias_tokens, a.bias + (long long)b * a.nb, a.nb, s_in);
     if (penalised) {
       if (L < 0 || L > a.H || P < 0 || P > L)
         most = 0xFFFFFFFFu;
@@ -391,9 +436,15 @@ __global__ void __launch_bounds__(THR, THR != kThr ? 1 : GRAD ? kBlocksGrad : kB
       bits[i] = m != -2 && v0 >= lo && v0 + 8 <= hi ? 0xFFu : 0u;
       if (mask && bits[i]) bits[i] = mask_bits(mask, v0);
     }
+    // (entries that the mask rules out are not needed)
+    if (((uintptr_t)(z + v00) & (sizeof(Raw<TI>) - 1)) == 0) {
 #pragma unroll
-    for (int i = 0; i < kDepth; ++i)   // (entries that the mask rules out are not needed)
-      if (bits[i] && !(same && bits[i] == 0xFFu)) x[i] = load8(z + v00 + i * 256, off);
+      for (int i = 0; i < kDepth; ++i) load8_if(x[i], z + v00 + i * 256, bits[i] && !(same && bits[i] == 0xFFu));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kDepth; ++i)
+        if (bits[i] && !(same && bits[i] == 0xFFu)) x[i] = load8(z + v00 + i * 256, off);
+    }
 #pragma unroll
     for (int i = 0; i < kDepth; ++i) {
       const int v0 = v00 + i * 256;
@@ -449,6 +500,7 @@ __global__ void __launch_bounds__(THR, THR != kThr ? 1 : GRAD ? kBlocksGrad : kB
           for (uint32_t bits = t; bits; bits &= bits - 1u, ++k)
             if ((unsigned)k < (unsigned)kListed) list[k] = (uint16_t)(e0 - s0 + __ffs(bits) - 1);
           __syncwarp();
+#pragma unroll 1
           for (int i = lane; i < min(all - base, kListed); i += 32) {
             const int u = list[i], v = s0 + u;
             const float f = to_f<TI>(z[v]);
@@ -460,115 +512,79 @@ __global__ void __launch_bounds__(THR, THR != kThr ? 1 : GRAD ? kBlocksGrad : kB
                   ++n;
                   seen = true;
                 }
-            float bias = 0.f;
             const bool has = biased && sl.is(sl.biased, u);
-            if (has)
-              for (int j = 0; j < s_biased; ++j)
-                if (sl.bias_u[j] == u) bias = sl.bias[j];
-            if (seen || has) o[v] = from_f<TO>(one_entry<GRAD>(f, f, seen, n, rho, pres, freq, has, bias));
+            if (seen || has)
+              o[v] = from_f<TO>(one_entry<GRAD>(f, f, seen, n, rho, pres, freq, has, has ? sl.bias[sl.place(u)] : 0.f));
           }
           __syncwarp();
         }
       }
     }
   }
-  if constexpr (!GRAD) return;
-  const bool bad = __syncthreads_or(most > (uint32_t)a.V);
-  if (bad) {
-    for (int r = 0; r < a.R; ++r)
-      for (int v = s0 + tid; v < s1; v += THR) out[((long long)b * a.R + r) * a.out_ld + v] = from_f<TO>(NAN);
-    return;
-  }
-  if (!any) return;
-
-  // kDeep touched entries per lane, in rows r (v < 0: none): their logits are fetched, then written anew
-  constexpr int kDeep = 4;
-  auto again = [&](const int (&v)[kDeep], const int (&r)[kDeep], const float (&bias)[kDeep], bool mine) {
-    float f[kDeep], g[kDeep];
-    bool on[kDeep];
-#pragma unroll
-    for (int j = 0; j < kDeep; ++j) {
-      on[j] = false;
-      if (v[j] < 0) continue;
-      const int m = s_mask[r[j]];
-      if (m == -2 || !allowed(m >= 0 ? a.mask + (long long)m * a.mask_ld : nullptr, v[j])) continue;
-      const long long row = (long long)b * a.R + r[j];
-      f[j] = to_f<TI>(in[row * a.in_ld + v[j]]);
-      g[j] = GRAD ? to_f<TO>(raw[row * a.raw_ld + v[j]]) : f[j];
-      on[j] = true;
+  if constexpr (GRAD) {
+    const bool bad = __syncthreads_or(most > (uint32_t)a.V);
+    if (bad) {
+      for (int r = 0; r < a.R; ++r)
+        for (int v = s0 + tid; v < s1; v += THR) out[((long long)b * a.R + r) * a.out_ld + v] = from_f<TO>(NAN);
+      return;
     }
+    if (!any) return;
+    // a warp lists the touched entries of kChunk, then takes them in (entry, row) pairs, kDeep per lane
+    constexpr int kDeep = 4;
+    uint8_t* list = (uint8_t*)s_list[warp];
+    for (int c = warp; c * kChunk < sl.n; c += THR / 32) {
+      uint32_t w = ((const uint8_t*)sl.touched)[c * 32 + lane];
+      int all = __popc(w), at = all;
 #pragma unroll
-    for (int j = 0; j < kDeep; ++j) {
-      if (!on[j]) continue;
-      const int u = v[j] - s0;
-      int n = sl.times(u);
-      bool seen = n > 0 || sl.is(sl.text, u);
-      if (sl.is(sl.drafted, u))
-        for (int d = 0; d < r[j]; ++d)
-          if (s_drafted[d] == v[j]) {
-            ++n;
-            seen = true;
-          }
-      if ((seen || mine) && mine == (biased && sl.is(sl.biased, u)))
-        out[((long long)b * a.R + r[j]) * a.out_ld + v[j]] =
-            from_f<TO>(one_entry<GRAD>(f[j], g[j], seen, n, rho, pres, freq, mine, bias[j]));
-    }
-  };
-  // a warp lists the entries of kChunk that the text touches, then takes them in (entry, row) pairs
-  uint8_t* list = (uint8_t*)s_list[warp];
-  for (int c = warp; c * kChunk < sl.n; c += THR / 32) {
-    uint32_t w = ((const uint8_t*)sl.touched)[c * 32 + lane];
-    int all = __popc(w), at = all;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, at, o);
-      if (lane >= o) at += y;
-    }
-    at -= all;
-    all = __shfl_sync(0xffffffffu, at + all, 31);
-    for (; w; w &= w - 1) list[at++] = (uint8_t)(lane * 8 + __ffs(w) - 1);
-    __syncwarp();
-    const int pairs = all * a.R;
-    for (int i0 = lane; i0 - lane < pairs; i0 += 32 * kDeep) {
-      const float none[kDeep] = {};
-      int v[kDeep], r[kDeep];
-#pragma unroll
-      for (int j = 0; j < kDeep; ++j) {
-        const int i = i0 + j * 32, slot = i / a.R;
-        r[j] = i - slot * a.R;
-        v[j] = i < pairs ? s0 + c * kChunk + list[slot] : -1;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, at, d);
+        if (lane >= d) at += y;
       }
-      again(v, r, none, false);
-    }
-    __syncwarp();
-  }
-  // the biased ones
-  const int pairs = biased ? s_biased * a.R : 0;
-  for (int i0 = tid; i0 < pairs; i0 += THR * kDeep) {
-    float bias[kDeep];
-    int v[kDeep], r[kDeep];
+      at -= all;
+      all = __shfl_sync(0xffffffffu, at + all, 31);
+      for (; w; w &= w - 1) list[at++] = (uint8_t)(lane * 8 + __ffs(w) - 1);
+      __syncwarp();
+      const int pairs = all * a.R;
+      for (int i0 = lane; i0 - lane < pairs; i0 += 32 * kDeep) {
+        float f[kDeep], g[kDeep];
+        long long to[kDeep];
 #pragma unroll
-    for (int j = 0; j < kDeep; ++j) {
-      const int i = i0 + j * THR, slot = i / a.R;
-      r[j] = i - slot * a.R;
-      v[j] = i < pairs ? s0 + sl.bias_u[slot] : -1;
-      bias[j] = i < pairs ? sl.bias[slot] : 0.f;
+        for (int j = 0; j < kDeep; ++j) {
+          const int i = i0 + j * 32, slot = i / a.R, r = i - slot * a.R;
+          to[j] = -1;
+          if (i >= pairs) continue;
+          const int u = c * kChunk + list[slot], v = s0 + u, m = s_mask[r];
+          bool seen = sl.is(sl.text, u);
+          for (int d = 0; d < r && !seen; ++d) seen = s_drafted[d] == v;
+          if (!seen || m == -2 || !allowed(m >= 0 ? a.mask + (long long)m * a.mask_ld : nullptr, v)) continue;
+          const long long row = (long long)b * a.R + r;
+          f[j] = to_f<TI>(in[row * a.in_ld + v]);
+          g[j] = to_f<TO>(raw[row * a.raw_ld + v]);
+          to[j] = row * a.out_ld + v;
+        }
+#pragma unroll
+        for (int j = 0; j < kDeep; ++j)
+          if (to[j] >= 0) out[to[j]] = from_f<TO>(one_entry<GRAD>(f[j], g[j], true, 0, rho, 0.f, 0.f, false, 0.f));
+      }
+      __syncwarp();
     }
-    again(v, r, bias, true);
   }
 }
 
 // Slices of at most S entries, smaller ones where that gives every SM its blocks.
+int slice_of(int B, int V, int S, int blocks) {
+  const long long even = ((long long)B * V + blocks - 1) / blocks;
+  return even < S ? (int)((even + kLeast - 1) / kLeast) * kLeast : S;
+}
+
 template <typename TI, typename TO, bool GRAD, int COUNT, int THR>
-cudaError_t launch(int B, const TI* in, TO* out, const TO* raw, PrArgs a, int S, int blocks, cudaStream_t stream) {
-  const long long even = ((long long)B * a.V + blocks - 1) / blocks;
-  if (even < S) S = (int)((even + kChunk * 2 - 1) / (kChunk * 2)) * (kChunk * 2);
+cudaError_t launch(int B, const TI* in, TO* out, const TO* raw, PrArgs a, int S, cudaStream_t stream) {
   a.S = S;
   a.nslice = (a.V + S - 1) / S;
   constexpr int unit = 32 * (64 / (int)sizeof(Raw<TI>));   // groups
   const bool al = ((uintptr_t)out % (8 * sizeof(TO))) == 0 && (a.out_ld * sizeof(TO)) % (8 * sizeof(TO)) == 0;
   const int units = (S / 8 + (al ? 0 : 1) + unit - 1) / unit;
-  const size_t smem = (size_t)S / 32 * Slice<COUNT>::kPer32 + (size_t)a.nb * 6;
+  const size_t smem = (size_t)S / 32 * Slice<COUNT>::kPer32 + (a.nb > 0 ? (size_t)a.nb * 4 + S / 16 : 0);
   auto kernel = process_kernel<TI, TO, GRAD, COUNT, THR>;
   if (smem > 32 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
@@ -579,22 +595,23 @@ cudaError_t launch(int B, const TI* in, TO* out, const TO* raw, PrArgs a, int S,
   return cudaGetLastError();
 }
 
-// Long texts of few rows: large slices read them fewer times, by blocks of more threads.
+template <typename TI, typename TO, bool GRAD, int COUNT>
+cudaError_t run_count(int B, const TI* in, TO* out, const TO* raw, const PrArgs& a, cudaStream_t stream) {
+  const int S = slice_of(B, a.V, !GRAD && a.R == 1 ? kSliceOne : kSlice, 2 * kFill);
+  if (a.H / a.R >= kLong * (long long)(S < a.V ? S : a.V))
+    return launch<TI, TO, GRAD, COUNT, kThrLong>(B, in, out, raw, a, slice_of(B, a.V, kSliceLong, kFill), stream);
+  return launch<TI, TO, GRAD, COUNT, kThr>(B, in, out, raw, a, S, stream);
+}
+
 template <typename TI, typename TO, bool GRAD>
 cudaError_t run(int B, const TI* in, TO* out, const TO* raw, PrArgs a, cudaStream_t stream) {
-  const bool wide = a.H + a.R > 65535;
-  if (GRAD) {
+  if constexpr (GRAD) {
     a.nb = 0;
-    if (a.H / a.R >= kLong) return launch<TI, TO, GRAD, kNoCount, kThrLong>(B, in, out, raw, a, kSliceLong, 152, stream);
-    return launch<TI, TO, GRAD, kNoCount, kThr>(B, in, out, raw, a, kSlice, 304, stream);
+    return run_count<TI, TO, GRAD, kNoCount>(B, in, out, raw, a, stream);
+  } else {
+    return a.H + a.R <= 65535 ? run_count<TI, TO, GRAD, kCount16>(B, in, out, raw, a, stream)
+                              : run_count<TI, TO, GRAD, kCount32>(B, in, out, raw, a, stream);
   }
-  constexpr int C16 = GRAD ? kNoCount : kCount16, C32 = GRAD ? kNoCount : kCount32;
-  if (a.H / a.R >= kLong)
-    return wide ? launch<TI, TO, GRAD, C32, kThrLong>(B, in, out, raw, a, kSliceLong, 152, stream)
-                : launch<TI, TO, GRAD, C16, kThrLong>(B, in, out, raw, a, kSliceLong, 152, stream);
-  const int S = a.R > 1 ? kSlice : kSliceOne;
-  return wide ? launch<TI, TO, GRAD, C32, kThr>(B, in, out, raw, a, S, 304, stream)
-              : launch<TI, TO, GRAD, C16, kThr>(B, in, out, raw, a, S, 304, stream);
 }
 
 template <bool GRAD>
