@@ -401,9 +401,9 @@ dspark_status dspark_bias_grad(int N, int V, int r, dspark_dtype gdt, const void
                                void* stream);
 
 /*
- * What a request asks of its logits before they are verified (dspark_verify's target logits), scored or trained on: penalties for tokens
- * that its text holds already, biases, and a grammar's mask.  Row (b, k) of the logits is position k of
- * request b's block (R = gamma + 1 rows for dspark_verify's target logits, R = 1 for a single token).  Its
+ * What a request asks of its logits before they are verified (dspark_verify's target logits), scored or
+ * trained on: penalties for tokens that its text holds already, biases, and a grammar's mask.  Row (b, k) of
+ * the logits is position k of request b's block (R = gamma + 1 rows for dspark_verify's target logits, R = 1 for a single token).  Its
  * text is history[b][0 .. lengths[b]), the first prompt_lengths[b] tokens of it the prompt and the others
  * generated, and then the generated tokens drafted[b][0 .. k).  With seen = whether the text holds v, c =
  * how often its generated part does:
@@ -477,8 +477,8 @@ dspark_status dspark_process_logits_grad(int B, int R, int V, dspark_dtype gdt, 
  * the formula's.  A row that is -inf everywhere has p = 0 throughout and norm (-inf, 0, -inf, 0).  NaN or
  * +inf logits make their row's outputs NaN (but the maxima).  Sums in fp32 in a fixed order (a row has the same
  * bits in calls of any N), and the outcomes in pairs of fp32 numbers where one would round away what the sums
- * hold.  One launch with grad_logits for rows of up to 3.2 MB (whose logits are read once), else two, and one for
- * the gradient; a wait inside the first that exceeds about one second makes its row NaN and sets
+ * hold.  For rows of up to 3.2 MB one launch with grad_logits (their logits are read once), and for the loss
+ * alone of up to 64 MB of logits; else two, and one for the gradient.  A wait inside the one launch that exceeds about one second makes its row NaN and sets
  * DSPARK_ERR_TIMEOUT in the workspace status.  Limits: T > 0 with T and log2(e) / T finite, finite weights of the
  * parts, 0 <= N <= 2^24 (N = 0 does nothing), 2 <= V <= 2^24, 1 <= K <= min(128, V),
  * N (V / 4096 + 2) < 2^31.

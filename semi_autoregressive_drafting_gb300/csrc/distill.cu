@@ -11,10 +11,11 @@
 //
 // Loss with gradient: a cluster of blocks reads a row once into their shared memory (bulk copies), puts -inf in place
 // of the row's own tokens, forms the maximum and sum of each 4 KB segment, exchanges them (distributed shared
-// memory), forms the outcomes and writes the gradient: each logit crosses HBM once each way.  Rows that no cluster
-// holds (above 3.2 MB), and the loss alone: a warp takes a segment in registers, a second launch with one block per
-// row joins the segments and forms the outcomes, and a third, for the gradient, reads the row again.  Both form the
-// same sums in the same order.  The gradient of given normalisers is the last two of these.
+// memory), forms the outcomes and writes the gradient: each logit crosses HBM once each way.  The loss alone of few
+// rows goes this way too.  Rows that no cluster holds (above 3.2 MB), and the loss alone of many: a warp takes a
+// segment in registers, a second launch with one block per row joins the segments and forms the outcomes, and a
+// third, for the gradient, reads the row again.  Both form the same sums in the same order.  The gradient of given
+// normalisers is the last two of these.
 //
 // 3584 x 262144 bf16, 64 tokens: 740 us (5.1 TB/s; three passes would be 850), bound by what is resident: 24 of 28 MB
 // of shared memory hold rows, for 11 us each, of which the loads take 3, the sums 2, the exchange and the outcomes
