@@ -130,10 +130,10 @@ dspark_status process_args(int B, int R, int V, int64_t ld, int64_t out_ld, dspa
   if (ld < V || out_ld < V) return fail(DSPARK_ERR_INVALID, "a row stride is below V=%d", V);
   if (H < 0 || H > (1 << 24) || nb < 0 || nb > 1024)
     return fail(DSPARK_ERR_INVALID, "bad history length %d or number of biases %d", H, nb);
-  if (H > 0 && (!history || history_ld < H))
+  if (B > 0 && H > 0 && (!history || history_ld < H))
     return fail(DSPARK_ERR_INVALID, "history is required and its rows are at least H apart");
-  if (nb > 0 && (!bias_tokens || !bias)) return fail(DSPARK_ERR_INVALID, "bias_tokens and bias are required");
-  if (mask && (M < 1 || mask_ld < (V + 31) / 32 || (!mask_rows && (long long)M < (long long)B * R)))
+  if (B > 0 && nb > 0 && (!bias_tokens || !bias)) return fail(DSPARK_ERR_INVALID, "bias_tokens and bias are required");
+  if (B > 0 && mask && (M < 1 || mask_ld < (V + 31) / 32 || (!mask_rows && (long long)M < (long long)B * R)))
     return fail(DSPARK_ERR_INVALID, "mask needs rows of V bits, one for each row of logits or chosen by mask_rows");
   if (mask_rows && !mask) return fail(DSPARK_ERR_INVALID, "mask_rows needs mask");
   if (B > 0 && (!in || !out)) return fail(DSPARK_ERR_INVALID, "logits, grad and out are required");

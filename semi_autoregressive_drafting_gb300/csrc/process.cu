@@ -15,9 +15,9 @@
 // that copies them, where a warp waits for each other's branches, took 3 times as long.)  The gradient writes its
 // touched entries after the whole slice, in (entry, row) pairs, since they also wait for the raw logits.
 //
-// HBM bounds the copy: 64 x 8 x 151936 bf16 rows to fp32 take 77 us (6.1 TB/s) without a text, and 84 with texts of
-// 4096 tokens on average (5.5 TB/s): the counting, the lists and the entries written twice are instructions (61 % of
-// the issue slots) and latency.  512 x 151936 fp32 rows, three quarters of them masked, 112 us (4.5 TB/s); without
+// HBM bounds the copy: 64 x 8 x 151936 bf16 rows to fp32 take 77 us (6.1 TB/s) without a text, and 85 with texts of
+// 4096 tokens on average (5.5 TB/s): the counting, the lists and the entries written twice are instructions (50 % of
+// the issue slots) and latency.  512 x 151936 fp32 rows, three quarters of them masked, 113 us (4.5 TB/s); without
 // text and mask 96 (6.5 TB/s).  Roles for warps in resident blocks (some copy, some count ahead) reached 97 and 139.
 #include "common.cuh"
 #include "kernels.h"
@@ -579,19 +579,20 @@ int slice_of(int B, int V, int S, int blocks) {
 }
 
 // Up to twice as many slices where the blocks then fill what the device holds of them at a time more evenly: a round of
-// blocks counted as its copies and as much again as kRound entries' (77 x 7 x 50021: 51 us, then 46; 72 x 8 x 68171: 75
-// and 66).
+// blocks counted as its copies and as much again as kRound entries' (the gradient of 77 x 7 x 50021: 51 us, then 45; 72 x 8 x
+// 68171: 75 and 66).
 int even_slice(int B, int V, int S, int resident) {
   const int least = (V + S - 1) / S;
   long long best = 0;
   int chosen = S;
-  for (int n = least; n <= 2 * least; ++n) {
+  for (int n = least, step = (least + 15) / 16; n <= 2 * least; n += step) {   // (17 tries at most)
     const int each = ((V + n - 1) / n + kLeast - 1) / kLeast * kLeast;
     const long long cost = ((long long)B * n + resident - 1) / resident * (each + kRound);
     if (best == 0 || cost < best) {
       best = cost;
       chosen = each;
     }
+    if (each == kLeast) break;
   }
   return chosen;
 }

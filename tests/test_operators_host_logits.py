@@ -168,3 +168,10 @@ def test_distill_plan_refuses_shapes_and_types(lib, on_gpu):
     for n, g in [(f(4, 2), f(4)), (f(4, 4), f(3)), (None, f(4)), (f(4, 4), None)]:
         with pytest.raises(ValueError):
             ds.DistillGradPlan(z, i, q, n, g, workspace=ws, out=f(4, 40))
+
+
+def test_no_request_needs_no_arrays(lib):
+    """Empty arrays have no address; a call without requests does nothing."""
+    assert process(lib, B=0, z=None, out=None, h=None, hld=0, nb=3, mask=None, rows=None) == 0
+    assert process(lib, B=0, M=0, rows=None) == 0
+    assert process(lib, B=0, R=33) == 1
