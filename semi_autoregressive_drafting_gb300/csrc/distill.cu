@@ -625,6 +625,34 @@ __global__ void __launch_bounds__(kThr, kChipBlocks)
 
 constexpr int kGPer = 4;  // 16-byte groups per thread
 
+__device__ __forceinline__ uint4 shuffle16(const uint4& q, int lane) {
+  return make_uint4(__shfl_sync(0xffffffffu, q.x, lane), __shfl_sync(0xffffffffu, q.y, lane),
+                    __shfl_sync(0xffffffffu, q.z, lane), __shfl_sync(0xffffffffu, q.w, lane));
+}
+// the 16 bytes that begin k entries into those of a, which b follows
+template <typename T>
+__device__ __forceinline__ uint4 shift16(const uint4& a, const uint4& b, int k) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  const int words = k * (int)sizeof(T) / 4;
+#pragma unroll
+  for (int i = 0; i < 7; ++i) w[i] = words & 1 ? w[i + 1] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = words & 2 ? w[i + 2] : w[i];
+  if (sizeof(T) == 2)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16 * (k & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// entries va .. vb - 1 of those that y holds from entry v0 on
+template <typename T>
+__device__ __forceinline__ void store_some(T* o, int v0, const uint4& y, int va, int vb) {
+  T f[Lg<T>::E];
+  memcpy(f, &y, 16);
+#pragma unroll
+  for (int e = 0; e < Lg<T>::E; ++e)
+    if (v0 + e >= va && v0 + e < vb) o[v0 + e] = f[e];
+}
+
 // dL/dz = c P_v outside S, `at` at the row's tokens.
 template <typename T>
 __global__ void __launch_bounds__(kThr) distill_grad_kernel(const T* logits, T* grad, const DsArgs a) {
@@ -649,21 +677,32 @@ __global__ void __launch_bounds__(kThr) distill_grad_kernel(const T* logits, T* 
   const RowCoef c{cf.x, cf.y, cf.z, 0.f};
   const bool none = c.c == 0.f;   // (zeros, whatever the entries are)
   const float s2 = kL2e / a.T;
-  const bool same = row_head((const T*)o) == head;
+#pragma unroll
+  for (int u = 0; u < kGPer; ++u) q[u] = none ? make_uint4(0u, 0u, 0u, 0u) : grad16<T>(q[u], c, s2);
+  // entries past a group's first at which the output's 16-byte groups begin: a lane stores from there on, with what it
+  // lacks from the next lane; the ends of the warp's entries are its own (1758 x 128892 bf16 into rows of another
+  // alignment: 163 us, entry by entry 500)
+  const int k = (head - row_head((const T*)o)) & (E - 1);
 #pragma unroll
   for (int u = 0; u < kGPer; ++u) {
-    const int v0 = (g0 + u * 32 + lane) * E - head;
-    if (v0 >= a.V) break;
-    const uint4 y = none ? make_uint4(0u, 0u, 0u, 0u) : grad16<T>(q[u], c, s2);
-    if (same && v0 >= 0 && v0 + E <= a.V) {
-      __stcs((uint4*)(o + v0), y);
-    } else {
-      T f[E];
-      memcpy(f, &y, 16);
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (v0 + e >= 0 && v0 + e < a.V) o[v0 + e] = f[e];
+    const int v0 = (g0 + u * 32 + lane) * E - head, v = v0 + k;
+    uint4 y = q[u];
+    bool more = true;   // whether the next lane's are there
+    if (k) {
+      uint4 next = shuffle16(q[u], (lane + 1) & 31);
+      if (u + 1 < kGPer) {
+        const uint4 x = shuffle16(q[u + 1], 0);
+        if (lane == 31) next = x;
+      } else {
+        more = lane < 31;
+      }
+      y = shift16<T>(q[u], next, k);
+      if (u == 0 && lane == 0) store_some(o, v0, q[0], max(v0, 0), min(v, a.V));
     }
+    if (more && v >= 0 && v + E <= a.V)
+      __stcs((uint4*)(o + v), y);
+    else
+      store_some(o, v, y, max(v, 0), min(more ? v + E : v0 + E, a.V));
   }
   __syncwarp();
 #pragma unroll

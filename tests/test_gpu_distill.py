@@ -388,3 +388,21 @@ def test_a_first_call_can_be_captured():
     torch.cuda.synchronize()
     want = ds.distill_loss(z, ids, lq)
     assert torch.equal(plan.out.grad_logits, want.grad_logits) and torch.equal(plan.out.loss, want.loss)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [5, 1031, 9001])
+def test_the_gradient_alone_into_rows_of_any_alignment(V, dtype):
+    z, ids, lq = make(3, V, 4, seed=61)
+    z, ids, lq = z.to(dtype).cuda(), ids.cuda(), lq.cuda()
+    o = ds.distill_loss(z, ids, lq)
+    one = torch.ones(3, device="cuda")
+    want = ds.distill_grad(z, ids, lq, o.norm, one)   # (rows aligned as the logits' are)
+    for pad in range(8):
+        for off in range(0, 8, 3):
+            buf = torch.full((3 * (V + pad) + 16,), 7.0, dtype=dtype, device="cuda")
+            out = buf[off:off + 3 * (V + pad)].view(3, V + pad)[:, :V]
+            ds.distill_grad(z, ids, lq, o.norm, one, out=out)
+            assert torch.equal(out, want), (pad, off)
+            assert (buf[:off] == 7.0).all() and (buf[off + 3 * (V + pad) - pad:] == 7.0).all()
