@@ -26,9 +26,7 @@
 #include "kernels.h"
 #include "rows.cuh"
 
-#include <map>
 #include <mutex>
-#include <utility>
 
 namespace dspark {
 namespace {
@@ -786,13 +784,15 @@ cudaLaunchConfig_t chip_config(const ChipShape& h, int clusters, cudaLaunchAttri
 // cluster lies inside a GPC, so the smallest size is not always it).  Asked for once for each length of row, and kept.
 template <typename T>
 cudaError_t chip_shape(int nseg, ChipShape* shape) {
+  constexpr int kDevices = 16;   // beyond these: asked at each call
   static std::mutex mu;
-  static std::map<std::pair<int, int>, ChipShape> known;
+  static ChipShape known[kDevices][kMostC * kMostSegs + 1];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lk(mu);
-  ChipShape& best = known[{dev, nseg}];
+  ChipShape best{0, 0, 0};
+  if (dev < kDevices) best = known[dev][nseg];
   if (best.C == 0) {
     auto kernel = distill_chip_kernel<T>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
@@ -807,6 +807,7 @@ cudaError_t chip_shape(int nseg, ChipShape* shape) {
       if (e != cudaSuccess) return e;
       if (h.clusters > best.clusters) best = h;
     }
+    if (dev < kDevices) known[dev][nseg] = best;
   }
   *shape = best;
   return cudaSuccess;
