@@ -467,7 +467,7 @@ dspark_status dspark_process_logits_grad(int B, int R, int V, dspark_dtype gdt, 
  *               own temperature.  Another id outside [0, V), or an id twice in a row: that row's outputs are
  *               NaN and DSPARK_ERR_INVALID in the workspace status
  *   weight      [N] fp32 or NULL (1 each): e.g. Eq 9's position weights over the number of rows.  A row of
- *               weight 0 (padding) is not read: all its outputs are 0
+ *               weight 0 (padding) may hold anything: all its outputs are 0
  *   outputs     loss [N], parts [N][2], norm [N][4] (16-byte aligned) fp32 and grad_logits, rows of type zdt,
  *               grad_ld apart; each optional, at least one.  grad_logits may be the logits themselves (same
  *               stride)

@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kMaxK) distill_rows_kernel(const T* __restrict
   const long long row = blockIdx.x;
   const int tid = (int)threadIdx.x;
   const float w = a.weight ? a.weight[row] : 1.f;
-  if (w == 0.f) {  // a padding row: not read
+  if (w == 0.f) {  // a padding row: whatever it holds
     if (tid == 0) {
       row_zero(a, row);
       if (a.coef) a.coef[row] = RowCoef{0.f, 0.f, 0.f, 0.f};

@@ -118,3 +118,23 @@ def test_the_loss_alone_in_calls_of_any_size(N, V, pad, dtype):
         few = ds.distill_loss(z[i:j], ids[i:j], logq[i:j], alpha=(0.3, 0.7), want_grad=False)
         for name in ("loss", "parts", "norm"):
             assert torch.equal(getattr(few, name), getattr(big, name)[i:j]), name
+
+
+@pytest.mark.parametrize("N,V", [(6, 3000), (17000, 130), (3, 1_700_000)])
+@pytest.mark.parametrize("grad", [True, False])
+def test_padding_rows_may_hold_anything(N, V, grad):
+    """One launch and several: rows of weight 0, with NaN logits and impossible ids, give 0 and set no status."""
+    z, ids, logq = teacher(N, V, 4, 8)
+    w = torch.ones(N, device="cuda")
+    want = ds.distill_loss(z, ids, logq, weight=w, want_grad=grad)
+    w[1] = 0.0
+    z[1], ids[1], logq[1] = float("nan"), V + 5, float("nan")
+    ws = ds.DistillWorkspace(N, V, 4)
+    o = ds.distill_loss(z, ids, logq, weight=w, want_grad=grad, workspace=ws)
+    assert ws.status() == 0
+    for name in ("loss", "parts", "norm") + (("grad_logits",) if grad else ()):
+        x, y = getattr(o, name), getattr(want, name)
+        assert not x[1].any() and torch.equal(x[0], y[0]) and torch.equal(x[2:], y[2:]), name
+    if grad:
+        g = ds.distill_grad(z, ids, logq, o.norm, w, workspace=ws)
+        assert ws.status() == 0 and not g[1].any() and torch.isfinite(g).all()
