@@ -166,6 +166,8 @@ dspark_status dspark_confidence(int B, int gamma, int V, int r, int d, dspark_dt
  *   l1 = || softmax(draft/T) - softmax(target/T) ||_1,  cstar = clamp(1 - l1/2, 0, 1),
  * the acceptance probability of the standard speculative accept/reject rule.
  * draft_logits, target_logits: [N][V] fp32.  cstar, l1: [N] fp32 (l1 may be NULL).
+ * Masked entries are -inf: their probability is 0.  A row that is -inf everywhere has nothing in common with
+ * any other: l1 is 2 and cstar 0.  NaN or +inf logits make both NaN.
  */
 dspark_status dspark_tv_label(int N, int V, float T, const float* draft_logits,
                               const float* target_logits, float* cstar, float* l1, void* stream);

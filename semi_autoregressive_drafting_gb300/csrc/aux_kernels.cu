@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(512) tv_label_kernel(int V, float invT, const 
     lse_merge(mt, lt, sm[2][w], sm[3][w]);
   }
   const float Ld = md + logf(ld), Lt = mt + logf(lt);
+  const bool empty = Ld == -INFINITY || Lt == -INFINITY;  // a row that is -inf everywhere
   __syncthreads();
   float acc = 0.f;
   for (int v = tid; v < V; v += blockDim.x)
@@ -94,8 +95,9 @@ __global__ void __launch_bounds__(512) tv_label_kernel(int V, float invT, const 
   if (tid == 0) {
     float s = 0.f;
     for (int w = 0; w < nw; ++w) s += sm[0][w];
+    if (empty) s = 2.f;
     if (l1) l1[blockIdx.x] = s;
-    cstar[blockIdx.x] = fminf(1.f, fmaxf(0.f, 1.f - 0.5f * s));
+    cstar[blockIdx.x] = acceptance(s);
   }
 }
 

@@ -145,7 +145,7 @@ __device__ __forceinline__ void lse_push(float& m, float& l, float y) {
   if (y > m) {
     l = l * __expf(m - y) + 1.f;
     m = y;
-  } else {
+  } else if (y != -INFINITY) {  // (a masked entry adds nothing, also in front of the first other one)
     l += __expf(y - m);
   }
 }
@@ -159,6 +159,11 @@ __device__ __forceinline__ void lse_merge(float& m, float& l, float m2, float l2
   const float mm = fmaxf(m, m2);
   l = l * __expf(m - mm) + l2 * __expf(m2 - mm);
   m = mm;
+}
+// Eq 8 from the rows' distance (NaN stays).  A row that is -inf everywhere has nothing in common with any
+// other: the kernels give it the distance 2, the largest there is.
+__device__ __forceinline__ float acceptance(float l1) {
+  return l1 != l1 ? l1 : fminf(1.f, fmaxf(0.f, 1.f - 0.5f * l1));
 }
 __device__ __forceinline__ void best_merge(float& best, uint32_t& tok, float b2, uint32_t t2) {
   if (b2 > best || (b2 == best && t2 < tok)) {
