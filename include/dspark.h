@@ -235,6 +235,10 @@ dspark_status dspark_verify(int B, int gamma, int V, float T, uint64_t seed,
  * (L_ce, L_tv, L_conf), grad_logits [B][gamma][V] (16-byte aligned), grad_conf [B][gamma], all
  * fp32.  workspace: dspark_draft_loss_workspace_bytes(B, gamma, V) bytes, 256-byte aligned
  * (contents need not be zero).  Limits: 1 <= gamma <= 16, 2 <= V <= 2^24, T finite and > 0.
+ * Masked entries, of the draft, the target or both, are -inf: their probability is 0, and so is their gradient
+ * but for a label's (L_ce is +inf there).  A row that is -inf everywhere has probabilities of 0 and nothing in
+ * common with any other row: ||p - q||_1 = 2, a constant, and c* = 0.  NaN or +inf logits make their request's
+ * losses, their row's gradient and its grad_conf NaN.
  * A label outside [0, V) makes every output of its request NaN and sets DSPARK_ERR_INVALID in
  * the workspace status.  Three launches on `stream`, four with grad_logits
  * (dspark_draft_loss_launches).

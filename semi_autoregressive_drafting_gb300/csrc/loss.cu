@@ -128,22 +128,22 @@ __global__ void __launch_bounds__(kLThr) loss_part_kernel(const float* __restric
       xd = fmaxf(xd, fmaxf(fmaxf(c.d[u].x, c.d[u].y), fmaxf(c.d[u].z, c.d[u].w)));
       xt = fmaxf(xt, fmaxf(fmaxf(c.t[u].x, c.t[u].y), fmaxf(c.t[u].z, c.t[u].w)));
     }
-    if (xd != -INFINITY) {  // (then xt is finite too: the same entries exist)
-      md = xd * s2;
-      mt = xt * s2;
+    md = xd * s2;
+    mt = xt * s2;
+    // (all entries masked: 2^-inf = 0 against a reference of 0, and NaN stays)
+    const float rd = xd == -INFINITY ? 0.f : md, rt = xt == -INFINITY ? 0.f : mt;
 #pragma unroll
-      for (int u = 0; u < kLPer; ++u) {
-        ld += ex2l(fmaf(c.d[u].x, s2, -md)) + ex2l(fmaf(c.d[u].y, s2, -md)) +
-              ex2l(fmaf(c.d[u].z, s2, -md)) + ex2l(fmaf(c.d[u].w, s2, -md));
-        lt += ex2l(fmaf(c.t[u].x, s2, -mt)) + ex2l(fmaf(c.t[u].y, s2, -mt)) +
-              ex2l(fmaf(c.t[u].z, s2, -mt)) + ex2l(fmaf(c.t[u].w, s2, -mt));
-      }
+    for (int u = 0; u < kLPer; ++u) {
+      ld += ex2l(fmaf(c.d[u].x, s2, -rd)) + ex2l(fmaf(c.d[u].y, s2, -rd)) +
+            ex2l(fmaf(c.d[u].z, s2, -rd)) + ex2l(fmaf(c.d[u].w, s2, -rd));
+      lt += ex2l(fmaf(c.t[u].x, s2, -rt)) + ex2l(fmaf(c.t[u].y, s2, -rt)) +
+            ex2l(fmaf(c.t[u].z, s2, -rt)) + ex2l(fmaf(c.t[u].w, s2, -rt));
     }
   } else {
     for (int v = v0 + (int)threadIdx.x; v < v1; v += kLThr) {
       const float yd = d[v] * s2, yt = t[v] * s2;
-      merge_l2(md, ld, yd, 1.f);
-      merge_l2(mt, lt, yt, 1.f);
+      if (yd != -INFINITY) merge_l2(md, ld, yd, 1.f);
+      if (yt != -INFINITY) merge_l2(mt, lt, yt, 1.f);
     }
   }
 #pragma unroll
@@ -201,7 +201,13 @@ __device__ __forceinline__ float2 row_norms_warp(const float4* part, long long r
   return make_float2(md + __log2f(ld), mt + __log2f(lt));
 }
 
-__device__ __forceinline__ float sgn(float x) { return x > 0.f ? 1.f : (x < 0.f ? -1.f : 0.f); }
+// What a row's exponents are taken against: its normaliser, 0 for a row that is -inf everywhere (its
+// probabilities are 0).
+__device__ __forceinline__ float2 references(float2 L) {
+  return make_float2(L.x == -INFINITY ? 0.f : L.x, L.y == -INFINITY ? 0.f : L.y);
+}
+
+__device__ __forceinline__ float sgn(float x) { return x > 0.f ? 1.f : (x < 0.f ? -1.f : x); }  // (0, or NaN)
 
 // ------------------------------------------------------------------ 2. |p - q| and s p sums
 // (the blocks take the chunks in reverse order, so that the first ones read the rows the
@@ -216,7 +222,7 @@ __global__ void __launch_bounds__(kLThr) loss_stat_kernel(const float* __restric
   const int v0 = ch * kLChunk, v1 = min(V, v0 + kLChunk);
   const float* d = zd + row * V;
   const float* t = zt + row * V;
-  const float2 L = row_norms_warp(ws.part, row, nchunk);
+  const float2 L = references(row_norms_warp(ws.part, row, nchunk));
   float l1 = 0.f, sp = 0.f;
   auto acc = [&](float a, float b) {
     const float p = ex2l(fmaf(a, s2, -L.x)), q = ex2l(fmaf(b, s2, -L.y));
@@ -264,7 +270,7 @@ __global__ void __launch_bounds__(kLThr, 3) loss_grad_kernel(
     for (int v = v0 + (int)threadIdx.x; v < v1; v += kLThr) g[v] = NAN;
     return;
   }
-  const float2 L = row_norms_warp(ws.part, row, nchunk);
+  const float2 L = references(row_norms_warp(ws.part, row, nchunk));
   float S = 0.f;  // sum s p over the row: lane-strided, then a butterfly (the same in every lane)
   for (int ch2 = lane; ch2 < nchunk; ch2 += 32) S += ws.stat[row * nchunk + ch2].y;
 #pragma unroll
@@ -305,11 +311,12 @@ __global__ void __launch_bounds__(kLThr) loss_final_kernel(
     const int x = lab[row];
     ok = x >= 0 && x < V;
     if (ok) {
-      const float2 L = row_norms(ws.part, row, nchunk);
+      const float2 N = row_norms(ws.part, row, nchunk), L = references(N);
       float l1 = 0.f;
       for (int c = 0; c < nchunk; ++c) l1 += ws.stat[row * nchunk + c].x;
+      if (N.x == -INFINITY || N.y == -INFINITY) l1 = 2.f;  // a row that is -inf everywhere
       const float w = __expf(-(float)lane / (float)G);
-      const float cstar = fminf(1.f, fmaxf(0.f, 1.f - 0.5f * l1));
+      const float cstar = acceptance(l1);
       const float l = conf[row];
       // ln c = -softplus(-l), ln(1 - c) = -softplus(l)
       const float sp1 = log1pf(__expf(-fabsf(l)));
@@ -333,7 +340,8 @@ __global__ void __launch_bounds__(kLThr) loss_final_kernel(
     ce = tv = cf = NAN;
   }
   if (lane == 0) {
-    if (loss) loss[b] = a_ce * ce + a_tv * tv + a_conf * cf;
+    // (a masked label's L_ce is +inf, and does not count where its weight is 0)
+    if (loss) loss[b] = (a_ce == 0.f && !isnan(ce) ? 0.f : a_ce * ce) + a_tv * tv + a_conf * cf;
     if (parts) {
       parts[3 * (size_t)b] = ce;
       parts[3 * (size_t)b + 1] = tv;
