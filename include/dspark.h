@@ -113,7 +113,8 @@ size_t dspark_workspace_bytes(int head, int B, int gamma, int V, int r, int d, i
  *            teacher-forcing tokens: step k+1 conditions on forced[b][k-1] ([P3] "Training
  *            DSpark"); tokens[] still receives each step's own sample.
  *   h, w     both NULL: c and S are not computed (c, S must then be NULL).
- *   target   NULL: cstar and l1 are not computed (cstar, l1 must then be NULL).
+ *   target   NULL: cstar and l1 are not computed (cstar, l1 must then be NULL).  Masked entries are -inf:
+ *            their probability is 0; a row that is -inf everywhere gives l1 2 and cstar 0, NaN logits NaN.
  *   outputs  tokens, lse: [B][gamma] (required).  c, S, cstar, l1: [B][gamma] fp32 or NULL.
  *            logits: [B][gamma][V] fp32 copy of z (debugging; NULL in production).
  * Device-side errors: an anchor or forced token outside [0, V) sets DSPARK_ERR_INVALID; that

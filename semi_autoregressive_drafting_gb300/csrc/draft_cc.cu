@@ -402,7 +402,11 @@ __device__ __forceinline__ float2 warp_merge_ml(const float2* part, int n, int l
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
     const float Mn = fmaxf(M, mb);  // the same in every lane
-    if (Mn == -INFINITY) continue;
+    if (Mn == -INFINITY) {  // masked entries alone: zeros, and NaN stays
+#pragma unroll
+      for (int j = 0; j < 8; ++j) L += q[j].y;
+      continue;
+    }
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum += q[j].y * __expf(q[j].x - Mn);
@@ -1309,8 +1313,10 @@ __global__ void __launch_bounds__(CW * 32 + 32 + (TCV ? 32 : 0), 1)
       csync<kCThreads>();
       for (int b = 0; b < B; ++b) {
         const float Ld = ms->Ld[b], Lt = ms->Lt[b];
-        float acc = 0.f;
-        for (int vl = tid; vl < SL; vl += kCThreads)
+        // (a row that is -inf everywhere: a distance of 2)
+        const bool empty = Ld == -INFINITY || Lt == -INFINITY;
+        float acc = empty && cta == 0 && tid == 0 ? 2.f : 0.f;
+        for (int vl = empty ? SL : tid; vl < SL; vl += kCThreads)
           acc += fabsf(__expf(ybuf[(size_t)b * SLM + vl] - Ld) -
                        __expf(tbuf[(size_t)(buf * NB + b) * SLM + vl] * p.invT - Lt));
         acc = warp_sum(acc);
@@ -1365,7 +1371,7 @@ __global__ void __launch_bounds__(CW * 32 + 32 + (TCV ? 32 : 0), 1)
         if (lane == 0) {
           const size_t o = (size_t)b * G + k;
           p.l1[o] = vb ? s : NAN;
-          p.cstar[o] = vb ? fminf(1.f, fmaxf(0.f, 1.f - 0.5f * s)) : NAN;
+          p.cstar[o] = vb ? acceptance(s) : NAN;
         }
       }
     }
@@ -1419,7 +1425,7 @@ __global__ void __launch_bounds__(CW * 32 + 32 + (TCV ? 32 : 0), 1)
         const size_t o = (size_t)b * G + G - 1;
         const bool vb = vtok[o] >= 0;
         p.l1[o] = vb ? s : NAN;
-        p.cstar[o] = vb ? fminf(1.f, fmaxf(0.f, 1.f - 0.5f * s)) : NAN;
+        p.cstar[o] = vb ? acceptance(s) : NAN;
       }
     }
     for (int i = tid; i < G * B * nCL; i += kCThreads) p.keys[i] = 0ull;

@@ -194,7 +194,11 @@ __device__ __forceinline__ float2 merge_ml(const float2* part, int n, int lane) 
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
     const float Mn = fmaxf(M, mb);  // the same in every lane
-    if (Mn == -INFINITY) continue;
+    if (Mn == -INFINITY) {  // masked entries alone: zeros, and NaN stays
+#pragma unroll
+      for (int j = 0; j < 8; ++j) L += q[j].y;
+      continue;
+    }
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum += q[j].y * __expf(q[j].x - Mn);
@@ -343,20 +347,19 @@ __global__ void __launch_bounds__(kTThr) target_part_kernel(const float* __restr
     float mx = -INFINITY;
 #pragma unroll
     for (int u = 0; u < kTChunk / 4 / kTThr; ++u) mx = fmaxf(mx, fmaxf(fmaxf(q[u].x, q[u].y), fmaxf(q[u].z, q[u].w)));
-    if (mx != -INFINITY) {
-      m = mx * s2;
+    m = mx * s2;
+    const float ref = mx == -INFINITY ? 0.f : m;  // (all entries masked: zeros, and NaN stays)
 #pragma unroll
-      for (int u = 0; u < kTChunk / 4 / kTThr; ++u)
-        l += ex2f(fmaf(q[u].x, s2, -m)) + ex2f(fmaf(q[u].y, s2, -m)) + ex2f(fmaf(q[u].z, s2, -m)) +
-             ex2f(fmaf(q[u].w, s2, -m));
-    }
+    for (int u = 0; u < kTChunk / 4 / kTThr; ++u)
+      l += ex2f(fmaf(q[u].x, s2, -ref)) + ex2f(fmaf(q[u].y, s2, -ref)) + ex2f(fmaf(q[u].z, s2, -ref)) +
+           ex2f(fmaf(q[u].w, s2, -ref));
   } else {
     for (int v = v0 + (int)threadIdx.x; v < v1; v += kTThr) {
       const float y = t[v] * s2;
       if (y > m) {
         l = l * ex2f(m - y) + 1.f;
         m = y;
-      } else {
+      } else if (y != -INFINITY) {  // (a masked entry adds nothing, also in front of the first other one)
         l += ex2f(y - m);
       }
     }
@@ -892,6 +895,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int j = 0; j < 20; ++j) sum += q[j].y * __expf(q[j].x - mb);
               M = mb;
               L = sum;
+            } else {  // masked entries alone: zeros, and NaN stays
+#pragma unroll
+              for (int j = 0; j < 20; ++j) L += q[j].y;
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) lse_merge(Mt, Lt, qt[j].x, qt[j].y);
@@ -913,7 +919,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* tr = tgp + ((size_t)b * G + kp) * V;
         float acc = 0.f;
         int vt = sl0;  // first entry left for the scalar tail
-        if (vec_t) {   // sl0 is a multiple of 128
+        if (Ld2 == -INFINITY || Lt2 == -INFINITY) {  // a row that is -inf everywhere: a distance of 2
+          acc = slc == 0 && lane == 0 ? 2.f : 0.f;
+          vt = sl1;
+        } else if (vec_t) {   // sl0 is a multiple of 128
           const int n4 = (sl1 - sl0) >> 2;
           const float4* y4 = (const float4*)(yr + sl0);
           const float4* t4 = (const float4*)(tr + sl0);
@@ -1203,7 +1212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float s = warp_sum_n(p.l1p + ((size_t)k * B + b) * nCTA, nslice, lane);
       if (lane == 0) {
         p.l1[o] = valid ? s : NAN;
-        p.cstar[o] = valid ? fminf(1.f, fmaxf(0.f, 1.f - 0.5f * s)) : NAN;
+        p.cstar[o] = valid ? acceptance(s) : NAN;
       }
     }
   }
@@ -1240,7 +1249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const size_t o = (size_t)b * G + G - 1;
           const bool vb = ((volatile int32_t*)p.tokens)[o] >= 0;
           p.l1[o] = vb ? s : NAN;
-          p.cstar[o] = vb ? fminf(1.f, fmaxf(0.f, 1.f - 0.5f * s)) : NAN;
+          p.cstar[o] = vb ? acceptance(s) : NAN;
         }
       }
     for (int i = et; i < G * B; i += kEpiThreads) p.keys[i] = 0ull;

@@ -28,8 +28,7 @@ def softmax(z, T=1.0):
     z = z.double() / T
     m = z.amax(-1, keepdim=True)
     e = (z - torch.where(m == -INF, 0.0, m)).exp()
-    s = e.sum(-1, keepdim=True)
-    return torch.where(s > 0, e / s, 0.0)
+    return torch.where(m == -INF, 0.0, e / e.sum(-1, keepdim=True))
 
 
 def distance(d, t, T=1.0):
