@@ -112,6 +112,8 @@ size_t dspark_workspace_bytes(int head, int B, int gamma, int V, int r, int d, i
  *   forced   NULL: step k+1 conditions on the sampled x_k.  Otherwise [B][gamma] int32
  *            teacher-forcing tokens: step k+1 conditions on forced[b][k-1] ([P3] "Training
  *            DSpark"); tokens[] still receives each step's own sample.
+ *   U        may hold masked entries, -inf: they are never drafted and add nothing to lse.  A row that is -inf
+ *            everywhere drafts nothing: its position has token -1 and NaN, and sets DSPARK_ERR_INVALID.
  *   h, w     both NULL: c and S are not computed (c, S must then be NULL).
  *   target   NULL: cstar and l1 are not computed (cstar, l1 must then be NULL).  Masked entries are -inf:
  *            their probability is 0; a row that is -inf everywhere gives l1 2 and cstar 0, NaN logits NaN.

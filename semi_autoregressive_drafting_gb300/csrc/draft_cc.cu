@@ -1286,10 +1286,11 @@ __global__ void __launch_bounds__(CW * 32 + 32 + (TCV ? 32 : 0), 1)
                      p.test_stuck == 1, p.test_stuck == 1 ? p.test_wait_ns : kWaitLimitNs);
       if (lane == 0 && ok) {
         const bool was_valid = ms->valid[b];
-        const int xk = was_valid ? (int)tagged_token(best) : -1;
+        // (a key without a score: a row of which nothing is left)
+        const int xk = was_valid && (best >> 32) != 0ull ? (int)tagged_token(best) : -1;
         const int nxt = p.forced ? p.forced[(size_t)b * G + ks] : xk;
         const bool nv = was_valid && nxt >= 0 && nxt < V;
-        if (was_valid && !nv && cta == 0) atomicMax(&hdr->status, kErrInvalid);
+        if (was_valid && (!nv || xk < 0) && cta == 0) atomicMax(&hdr->status, kErrInvalid);
         ms->cond[b] = nv ? nxt : 0;
         ms->valid[b] = nv;
         if (cta == b) p.tokens[(size_t)b * G + ks] = was_valid ? xk : -1;

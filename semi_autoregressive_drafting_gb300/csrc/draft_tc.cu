@@ -747,6 +747,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       wd[0] = r0.x; wd[1] = r0.y; wd[2] = r0.z; wd[3] = r0.w;
       wd[4] = r1.x; wd[5] = r1.y; wd[6] = r1.z; wd[7] = r1.w;
     }
+    auto store_y = [&]() {  // (the target's normalisers come from target_part_kernel)
+      float* yo = ybp + (size_t)b * V + v;  // y2 = z s2, read back by the second pass
+      if (FAST || (vec_t && full)) {
+        *(float4*)yo = make_float4(z[0] * s2, z[1] * s2, z[2] * s2, z[3] * s2);
+        *(float4*)(yo + 4) = make_float4(z[4] * s2, z[5] * s2, z[6] * s2, z[7] * s2);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (v + e < V) yo[e] = z[e] * s2;
+      }
+    };
     if (st.m == -INFINITY) {  // the row's first group: the normaliser's reference point, and
       // the running best seeded with the exact score of the group's largest entry (a real
       // score, so a lower bound of the row's best: without it every entry of the group would be
@@ -760,19 +771,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           es = e;
         }
       st.m = zs * s2;
-      if (zs != -INFINITY) {
-        uint32_t ws = wd[0];
-#pragma unroll
-        for (int e = 1; e < 8; ++e)
-          if (es == e) ws = wd[e];
-        const float sc = zs * s2 - gumbel_log2(ws);
-        if (sc > st.best || (sc == st.best && (uint32_t)(v + es) < st.tok)) {
-          st.best = sc;
-          st.tok = (uint32_t)(v + es);
-        }
-        *sb_own = st.best;
-        tb = fmaxf(tb, st.best);
+      if (st.m == -INFINITY) {  // all eight are masked: nothing to add, and the next group is the first
+        if (TGT) store_y();
+        return;
       }
+      uint32_t ws = wd[0];
+#pragma unroll
+      for (int e = 1; e < 8; ++e)
+        if (es == e) ws = wd[e];
+      const float sc = zs * s2 - gumbel_log2(ws);
+      if (sc > st.best || (sc == st.best && (uint32_t)(v + es) < st.tok)) {
+        st.best = sc;
+        st.tok = (uint32_t)(v + es);
+      }
+      *sb_own = st.best;
+      tb = fmaxf(tb, st.best);
       Cp = 1.002f * ex2f(st.m - tb);
     }
     const float2 s22 = make_float2(s2, s2);
@@ -843,17 +856,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     lsum = __fadd2_rn(lsum, gs);
-    if (TGT) {  // the target's normalisers come from target_part_kernel
-      float* yo = ybp + (size_t)b * V + v;  // y2 = z s2, read back by the second pass
-      if (FAST || (vec_t && full)) {
-        *(float4*)yo = make_float4(z[0] * s2, z[1] * s2, z[2] * s2, z[3] * s2);
-        *(float4*)(yo + 4) = make_float4(z[4] * s2, z[5] * s2, z[6] * s2, z[7] * s2);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (v + e < V) yo[e] = z[e] * s2;
-      }
-    }
+    if (TGT) store_y();
   };
 
   // Eq 8 of step kp over this block's slice, once every block has published step kp.
@@ -1197,8 +1200,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const size_t o = (size_t)b * G + k;
     bool valid = false;  // once false, false for every later position of the request
     const int x = cond_token(p, b, k, &valid);
-    if (!valid && lane == 0) atomicMax(&hdr->status, kErrInvalid);
     const int tok = valid ? (int)key_token(ld_acquire64(&p.keys[(size_t)k * B + b])) : -1;
+    valid = tok >= 0;  // (-1 too for a row of which nothing is left)
+    if (!valid && lane == 0) atomicMax(&hdr->status, kErrInvalid);
     const float2 ml = merge_ml(p.ml + ((size_t)k * B + b) * nCTA, nslice, lane);
     if (conf) {
       const float z7 = ((volatile float*)p.hdot)[o] + eq7_edot(p, x, lane);

@@ -63,3 +63,52 @@ def test_masked_targets(wl, share):
         assert (l1 - want)[~bad].abs().max() <= 1e-4
         assert (cs - (1 - want / 2).clamp(0, 1))[~bad].abs().max() <= 1e-4
         assert l1[0, 1] == 2 and cs[0, 1] == 0
+
+
+@pytest.mark.parametrize("wl", CASES, ids=name)
+@pytest.mark.parametrize("share", [0.5, 0.995])
+def test_masked_drafts(wl, share):
+    # the mask of U's rows, in whole groups too, and of the target's
+    wl = wl.with_(gamma=3, target_noise=1.0, seed=wl.V + 1)
+    t = inputs.generate(wl)
+    gen = torch.Generator().manual_seed(wl.B)
+    t["U"], _ = masked(t["U"], share, gen)
+    t["U"][0, 0, :wl.V // 2] = -INF
+    t["U"][0, 0, wl.V - 2] = 0.0
+    t["target"], _ = masked(t["target"], share, gen)
+    o = parity.oracle_draft(wl, t, want_z=True)
+    assert o.status == 0
+    forced = torch.from_numpy(o.tokens).cuda()
+    a, status = draft(wl, t, forced=forced, want_logits=True)
+    assert status == 0
+    parity.check_tokens_forced(a.tokens.cpu().numpy(), o)
+    parity.compare_floats(a, o)
+    b, status = draft(wl, t, forced=forced)
+    assert status == 0
+    parity.compare_floats(b, o, logits=False)
+    assert torch.equal(a.tokens, b.tokens)
+    assert torch.isfinite(t["U"].gather(2, a.tokens.cpu().long()[..., None]).float()).all()
+    free, status = draft(wl, t)
+    assert status == 0
+    parity.check_tokens_free(free.tokens.cpu().numpy(), o)
+
+
+@pytest.mark.parametrize("wl", CASES, ids=name)
+@pytest.mark.parametrize("at", [0, 2])
+def test_rows_of_u_that_nothing_is_left_of(wl, at):
+    # (position 2 is the block's last)
+    wl = wl.with_(gamma=3, target_noise=1.0, seed=wl.V + 2)
+    t = inputs.generate(wl)
+    whole, status = draft(wl, t)
+    assert status == 0
+    b = wl.B - 1
+    t["U"][b, at] = -INF
+    o, status = draft(wl, t)
+    assert status == 1
+    assert (o.tokens[b, at:] == -1).all()
+    for name_ in ("lse", "c", "S", "l1", "cstar"):
+        assert torch.isnan(getattr(o, name_)[b, at:]).all(), name_
+        assert torch.equal(getattr(o, name_)[b, :at], getattr(whole, name_)[b, :at]), name_
+    others = [i for i in range(wl.B) if i != b]
+    for name_ in ("tokens", "lse", "c", "S", "l1", "cstar"):
+        assert torch.equal(getattr(o, name_)[others], getattr(whole, name_)[others]), name_
