@@ -460,6 +460,8 @@ __global__ void __launch_bounds__(THR, THR != kThr ? 1 : GRAD ? kBlocksGrad : kB
         for (int v = max(v0, s0); v < min(v0 + 8, s1); ++v) {
           if (m == -2 || !allowed(mask, v))
             ((W*)o)[v] = (W)(m == -2 ? nan : fill);
+          else if (std::is_same<TI, TO>::value && !same)
+            ((W*)o)[v] = ((const W*)z)[v];   // (bits: through fp32 every bf16 NaN would become one)
           else if (!same)
             o[v] = from_f<TO>(to_f<TI>(z[v]));
         }

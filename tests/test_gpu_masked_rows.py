@@ -95,8 +95,11 @@ def loss_in_64_bits(d, t, lab, cf, T, alpha):
     # an entry next to the kink may have either sign
     near = (p - q).abs() <= 2e-4 * p
     tol = (alpha[0] * 5e-5 * p + alpha[1] * p * (1e-4 + 1e-4 + 2 * near + 2 * (near * p).sum(-1, keepdim=True))) / T
+    # and every entry by the roundings of its factors: the weight's exponential (2 + 1.2 steps of 2^-23 at
+    # |x| <= 1: 7 of 2^-24), 1 / T, their product, the difference p - [v == x], two products and a sum: 13 in all
+    tol = tol + 13 * 2.0 ** -24 * (alpha[0] * (p - hot).abs() + alpha[1] * p * (s - S).abs()) / T
     loss = (alpha[0] * ce if alpha[0] else 0.0) + alpha[1] * parts[:, 1] + alpha[2] * conf
-    return loss, parts, grad, tol + 2.0 ** -24 * alpha[0] / T, alpha[2] * w * (torch.sigmoid(c) - label)
+    return loss, parts, grad, tol, alpha[2] * w * (torch.sigmoid(c) - label)
 
 
 def check_loss(d, t, lab, cf, T=1.0, alpha=ALPHA):
@@ -112,7 +115,10 @@ def check_loss(d, t, lab, cf, T=1.0, alpha=ALPHA):
     some = torch.isfinite(loss)
     assert torch.equal(got[0][~some], loss[~some])
     assert not some.any() or (got[0] - loss)[some].abs().max() <= 1e-3 * G
-    assert ((got[2] - grad).abs() <= tol).all()
+    over = (got[2] - grad).abs() - tol
+    at = int(over.argmax())
+    assert (over <= 0).all(), (at % d.shape[-1], lab.flatten()[at // d.shape[-1]], got[2].flatten()[at],
+                               grad.flatten()[at], tol.flatten()[at])
     assert (got[3] - gconf).abs().max() <= 1e-4
     only = ds.draft_loss(*a, T=T, alpha=alpha, want_grads=False, workspace=ws)
     assert torch.equal(only[0].cpu().double(), got[0]) and torch.equal(only[1].cpu().double(), got[1])
