@@ -250,9 +250,9 @@ __device__ __forceinline__ uint32_t count_text(const Slice<COUNT>& sl, const int
   uint32_t most = 0u;
   const int tid = (int)threadIdx.x, nthr = (int)blockDim.x;
   auto one = [&](int i, int t) {
-    most = max(most, (uint32_t)(t + 1));
-    const int u = t - sl.s0;
-    if ((unsigned)u < (unsigned)sl.n) sl.add(u, i < P);
+    most = max(most, (uint32_t)t + 1u);   // (unsigned: any token is defined)
+    const uint32_t u = (uint32_t)t - (uint32_t)sl.s0;
+    if (u < (uint32_t)sl.n) sl.add((int)u, i < P);
   };
   const int head = min(L, (int)((16 - ((uintptr_t)h & 15)) & 15) >> 2);   // up to a 16-byte boundary
   const int n4 = (L - head) >> 2;
@@ -283,12 +283,12 @@ __device__ __forceinline__ uint32_t list_biases(const Slice<COUNT>& sl, const in
                                                 uint32_t* in) {
   uint32_t most = 0u;
   for (int i = (int)threadIdx.x;;) {
-    const int u = t - sl.s0;
-    const bool mine = (unsigned)u < (unsigned)sl.n;
-    most = max(most, (uint32_t)(t + 1));
+    const uint32_t u = (uint32_t)t - (uint32_t)sl.s0;
+    const bool mine = u < (uint32_t)sl.n;
+    most = max(most, (uint32_t)t + 1u);
     if (mine) {
-      sl.set(sl.biased, u);
-      sl.set(sl.touched, u);
+      sl.set(sl.biased, (int)u);
+      sl.set(sl.touched, (int)u);
     }
     if (i < nb) sl.bias[i] = 0.f;
     const uint32_t some = __ballot_sync(0xffffffffu, mine);
@@ -390,11 +390,11 @@ __global__ void __launch_bounds__(THR, THR != kThr ? 1 : GRAD ? kBlocksGrad : kB
       else
         most = max(most, count_text(sl, a.history + (long long)b * a.history_ld, L, P));
       if (tid < a.R - 1) {   // (R <= 32: the first warp)
-        const int t = s_drafted[tid], u = t - s0;
-        most = max(most, (uint32_t)(t + 1));
-        if ((unsigned)u < (unsigned)sl.n) {
-          sl.set(sl.drafted, u);
-          sl.set(sl.touched, u);
+        const uint32_t t = (uint32_t)s_drafted[tid], u = t - (uint32_t)s0;
+        most = max(most, t + 1u);
+        if (u < (uint32_t)sl.n) {
+          sl.set(sl.drafted, (int)u);
+          sl.set(sl.touched, (int)u);
         }
       }
     }
