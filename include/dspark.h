@@ -435,7 +435,8 @@ dspark_status dspark_bias_grad(int N, int V, int r, dspark_dtype gdt, const void
  *               NULL: none.  mask_rows [B][R] int32 gives each row's, -1 for none; NULL: row i of the mask for
  *               row i of the logits
  *   out         B R rows of type odt, out_ld apart, rounded once.  It may be the logits themselves (same
- *               type and stride): then only what changes is written.  Rows that no mask, penalty or bias
+ *               type and stride): then only what changes is written; it shares no memory with them otherwise
+ *               (two ranges of columns of one buffer are fine).  Rows that no mask, penalty or bias
  *               touches keep their bits when the types are equal
  * A row whose mask allows nothing is -inf everywhere.  A token outside [-1, V), in what is read, and a length
  * outside [0, H] or a prompt length outside [0, lengths[b]] make their request's rows NaN, a mask row outside

@@ -116,7 +116,12 @@ bool overlap(const void* a, dspark_dtype adt, int64_t ald, const void* b, dspark
   const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
   const uintptr_t a1 = a0 + (uintptr_t)((N - 1) * ald + V) * size_of(adt);
   const uintptr_t b1 = b0 + (uintptr_t)((N - 1) * bld + V) * size_of(bdt);
-  return a0 < b1 && b0 < a1;
+  if (a0 >= b1 || b0 >= a1) return false;
+  // rows of one distance may lie between one another: two ranges of columns of a buffer
+  const uintptr_t row = (uintptr_t)ald * size_of(adt), aw = (uintptr_t)V * size_of(adt), bw = (uintptr_t)V * size_of(bdt);
+  if (N == 1 || row != (uintptr_t)bld * size_of(bdt)) return true;
+  const uintptr_t at = (b0 + row - a0 % row) % row;   // where b's rows begin, from a's
+  return at < aw || at + bw > row;
 }
 // What the calls that process logits and their gradients share.
 dspark_status process_args(int B, int R, int V, int64_t ld, int64_t out_ld, dspark_dtype in_dt, const void* in,
