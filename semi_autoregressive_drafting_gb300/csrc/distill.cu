@@ -471,7 +471,7 @@ __device__ __forceinline__ void st_cluster_f(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// (a load each time it is asked for, so that a segment takes no 32 registers: six blocks per SM)
+// (a load each time it is asked for, so that a segment takes no 32 registers)
 __device__ __forceinline__ uint4 lds16(const uint4* p) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -480,7 +480,7 @@ __device__ __forceinline__ uint4 lds16(const uint4* p) {
   return v;
 }
 
-constexpr int kChipBlocks = 4;   // per SM
+constexpr int kChipBlocks = 4;   // per SM, that registers leave room for (shared memory: three of 64 KB)
 struct ChipSm {
   RowSm row;
   SeenSm seen;
@@ -762,10 +762,13 @@ cudaError_t gradient(int N, const T* logits, T* grad, DsArgs a, bool al_rows, cu
 }
 
 // How rows of nseg segments go to the chip: in clusters of C blocks of `segs` segments, of which the device holds
-// `clusters` at once.
+// `clusters` at once (0: no cluster holds them).  Bit c of `fits`: it holds clusters of c blocks too.
 struct ChipShape {
   int C, segs, clusters;
+  uint32_t fits;
+  bool asked;
 };
+int segments_each(int nseg, int C) { return (nseg + C - 1) / C; }
 size_t chip_smem(int C, int segs) { return (size_t)segs * 4096 + (size_t)C * segs * sizeof(float2); }
 cudaLaunchConfig_t chip_config(const ChipShape& h, int clusters, cudaLaunchAttribute* at, cudaStream_t stream) {
   at->id = cudaLaunchAttributeClusterDimension;
@@ -791,22 +794,26 @@ cudaError_t chip_shape(int nseg, ChipShape* shape) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lk(mu);
-  ChipShape best{0, 0, 0};
+  ChipShape best{};
   if (dev < kDevices) best = known[dev][nseg];
-  if (best.C == 0) {
+  if (!best.asked) {
     auto kernel = distill_chip_kernel<T>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    const int least = (nseg + kSegs - 1) / kSegs;
+    const int least = segments_each(nseg, kSegs);
     for (int C = least < kMostC ? least : kMostC; C <= kMostC && C <= nseg; ++C) {
-      ChipShape h{C, (nseg + C - 1) / C, 0};
+      ChipShape h{C, segments_each(nseg, C), 0, best.fits, false};
       cudaLaunchAttribute at{};
       const cudaLaunchConfig_t cfg = chip_config(h, 1, &at, nullptr);
-      e = cudaOccupancyMaxActiveClusters(&h.clusters, kernel, &cfg);
-      if (e != cudaSuccess) return e;
+      if (cudaOccupancyMaxActiveClusters(&h.clusters, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();   // a size that the device does not take
+        h.clusters = 0;
+      }
+      if (h.clusters > 0) best.fits = h.fits |= 1u << C;
       if (h.clusters > best.clusters) best = h;
     }
+    best.asked = true;
     if (dev < kDevices) known[dev][nseg] = best;
   }
   *shape = best;
@@ -816,8 +823,11 @@ cudaError_t chip_shape(int nseg, ChipShape* shape) {
 template <typename T>
 cudaError_t on_chip(int N, int nseg, const T* logits, T* grad, const DsArgs& a, ChipShape h, cudaStream_t stream) {
   // few rows: blocks for every SM (a row's results do not depend on how many share it)
-  const int most = nseg < kMostC ? nseg : kMostC, C = kFill / N < most ? kFill / N : most;
-  if (C > h.C) h = ChipShape{C, (nseg + C - 1) / C, 1};
+  for (int C = kMostC; C > h.C; --C) {
+    if ((long long)C * N > kFill || !((h.fits >> C) & 1u)) continue;
+    h.C = C;
+    h.segs = segments_each(nseg, C);
+  }
   cudaLaunchAttribute at{};
   const cudaLaunchConfig_t cfg = chip_config(h, N, &at, stream);
   return cudaLaunchKernelEx(&cfg, distill_chip_kernel<T>, logits, grad, a, h.C, h.segs);
