@@ -723,9 +723,12 @@ dspark_status dspark_process_logits(int B, int R, int V, dspark_dtype zdt, const
   const dspark_status s = process_args(B, R, V, ld, out_ld, zdt, logits, odt, out, history, history_ld, H, nb,
                                        bias_tokens, bias, mask, mask_ld, M, mask_rows);
   if (s != DSPARK_OK || B == 0) return s;
+  DevInfo di;
+  if (!dev_info(&di)) return fail(DSPARK_ERR_CUDA, "cannot query the current device");
   cudaError_t e = launch_process(0, B, R, V, zdt == DSPARK_BF16, logits, ld, odt == DSPARK_BF16, out, out_ld, nullptr,
                                  0, history, history_ld, H, lengths, prompt_lengths, drafted, repetition, presence,
-                                 frequency, nb, bias_tokens, bias, mask, mask_ld, M, mask_rows, (cudaStream_t)stream);
+                                 frequency, nb, bias_tokens, bias, mask, mask_ld, M, mask_rows, di.sms,
+                                 (cudaStream_t)stream);
   return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, "process logits launch");
 }
 
@@ -745,9 +748,11 @@ dspark_status dspark_process_logits_grad(int B, int R, int V, dspark_dtype gdt, 
   if (repetition && (overlap(logits, zdt, ld, out, zdt, out_ld, (int64_t)B * R, V) || (B > 0 && logits == out)))
     return fail(DSPARK_ERR_INVALID, "out overlaps the logits");
   if (B == 0) return DSPARK_OK;
+  DevInfo di;
+  if (!dev_info(&di)) return fail(DSPARK_ERR_CUDA, "cannot query the current device");
   cudaError_t e = launch_process(1, B, R, V, gdt == DSPARK_BF16, grad, grad_ld, zdt == DSPARK_BF16, out, out_ld,
                                  logits, ld, history, history_ld, H, lengths, prompt_lengths, drafted, repetition,
-                                 nullptr, nullptr, 0, nullptr, nullptr, mask, mask_ld, M, mask_rows,
+                                 nullptr, nullptr, 0, nullptr, nullptr, mask, mask_ld, M, mask_rows, di.sms,
                                  (cudaStream_t)stream);
   return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, "process logits gradient launch");
 }
@@ -775,9 +780,11 @@ dspark_status dspark_distill_loss(int N, int V, float T, dspark_dtype zdt, const
   // copies count as one that has run out.
   const char* f = std::getenv("DSPARK_TEST_STUCK_WAIT");
   const int stuck = f && !std::strcmp(f, "mbar");
+  DevInfo di;
+  if (!dev_info(&di)) return fail(DSPARK_ERR_CUDA, "cannot query the current device");
   cudaError_t e = launch_distill(N, V, T, zdt == DSPARK_BF16, logits, ld, K, teacher_ids, teacher_logp, weight,
                                  alpha_kl, alpha_l1, rest != 0, nullptr, loss, parts, norm, grad_logits, grad_ld, stuck,
-                                 workspace, (cudaStream_t)stream);
+                                 workspace, di.sms, (cudaStream_t)stream);
   return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, "distillation loss launch");
 }
 
@@ -793,9 +800,11 @@ dspark_status dspark_distill_grad(int N, int V, float T, dspark_dtype zdt, const
   if (N == 0) return DSPARK_OK;
   if (!norm || !grad_loss || !grad_logits)
     return fail(DSPARK_ERR_INVALID, "norm, grad_loss and grad_logits are required");
+  DevInfo di;
+  if (!dev_info(&di)) return fail(DSPARK_ERR_CUDA, "cannot query the current device");
   cudaError_t e = launch_distill(N, V, T, zdt == DSPARK_BF16, logits, ld, K, teacher_ids, teacher_logp, grad_loss,
                                  alpha_kl, alpha_l1, rest != 0, norm, nullptr, nullptr, nullptr, grad_logits, grad_ld, 0,
-                                 workspace, (cudaStream_t)stream);
+                                 workspace, di.sms, (cudaStream_t)stream);
   return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, "distillation gradient launch");
 }
 

@@ -713,8 +713,8 @@ __global__ void __launch_bounds__(kThr) distill_grad_kernel(const T* logits, T* 
 // 2000 x 8000 bf16 20 and 25, 448 x 151936 fp32 63 and 50).
 constexpr int kFewSegs = 16384;
 // Segments of a block's share of a row: 64 KB, three blocks per SM, and as many as its shared memory holds; blocks
-// of a cluster at most; blocks for every SM.
-constexpr int kSegs = 16, kMostSegs = 50, kMostC = 16, kFill = 152;
+// of a cluster at most.
+constexpr int kSegs = 16, kMostSegs = 50, kMostC = 16;
 constexpr int kMostSmem = kMostSegs * 4096 + kMostC * kMostSegs * (int)sizeof(float2);
 
 constexpr size_t al(size_t x) { return (x + 255) / 256 * 256; }
@@ -821,10 +821,11 @@ cudaError_t chip_shape(int nseg, ChipShape* shape) {
 }
 
 template <typename T>
-cudaError_t on_chip(int N, int nseg, const T* logits, T* grad, const DsArgs& a, ChipShape h, cudaStream_t stream) {
+cudaError_t on_chip(int N, int nseg, const T* logits, T* grad, const DsArgs& a, ChipShape h, int nsm,
+                    cudaStream_t stream) {
   // few rows: blocks for every SM (a row's results do not depend on how many share it)
   for (int C = kMostC; C > h.C; --C) {
-    if ((long long)C * N > kFill || !((h.fits >> C) & 1u)) continue;
+    if ((long long)C * N > nsm || !((h.fits >> C) & 1u)) continue;
     h.C = C;
     h.segs = segments_each(nseg, C);
   }
@@ -834,7 +835,7 @@ cudaError_t on_chip(int N, int nseg, const T* logits, T* grad, const DsArgs& a, 
 }
 
 template <typename T>
-cudaError_t run(int N, const T* logits, T* grad, const DsArgs& a, cudaStream_t stream) {
+cudaError_t run(int N, const T* logits, T* grad, const DsArgs& a, int nsm, cudaStream_t stream) {
   const bool al_rows = ((uintptr_t)logits % 16) == 0 && (a.ld * (long long)sizeof(T)) % 16 == 0;
   cudaError_t e;
   if (a.norm_in) {
@@ -846,7 +847,7 @@ cudaError_t run(int N, const T* logits, T* grad, const DsArgs& a, cudaStream_t s
       ChipShape shape;
       e = chip_shape<T>(nseg, &shape);
       if (e != cudaSuccess) return e;
-      if (shape.clusters > 0) return on_chip(N, nseg, logits, grad, a, shape, stream);
+      if (shape.clusters > 0) return on_chip(N, nseg, logits, grad, a, shape, nsm, stream);
     }
     e = forward(N, logits, a, al_rows, stream);
   }
@@ -863,7 +864,7 @@ size_t distill_workspace_bytes(int N, int V, int K) {
 cudaError_t launch_distill(int N, int V, float T, int bf16, const void* logits, long long ld, int K,
                            const int32_t* ids, const float* logq, const float* weight, float a_kl, float a_l1,
                            int rest, const float* norm_in, float* loss, float* parts, float* norm, void* grad,
-                           long long gld, int stuck, void* workspace, cudaStream_t stream) {
+                           long long gld, int stuck, void* workspace, int nsm, cudaStream_t stream) {
   const Ws s = layout(workspace, N, V, K);
   DsArgs a;
   a.V = V;
@@ -890,7 +891,8 @@ cudaError_t launch_distill(int N, int V, float T, int bf16, const void* logits, 
   a.coef = grad ? s.coef : nullptr;
   a.at = grad ? s.at : nullptr;
   using H = __nv_bfloat16;
-  return bf16 ? run<H>(N, (const H*)logits, (H*)grad, a, stream) : run<float>(N, (const float*)logits, (float*)grad, a, stream);
+  return bf16 ? run<H>(N, (const H*)logits, (H*)grad, a, nsm, stream)
+              : run<float>(N, (const float*)logits, (float*)grad, a, nsm, stream);
 }
 
 }  // namespace dspark

@@ -55,12 +55,12 @@ cudaError_t launch_process(int grad, int B, int R, int V, int i_bf16, const void
                            const int32_t* drafted, const float* repetition, const float* presence,
                            const float* frequency, int nb, const int32_t* bias_tokens, const float* bias,
                            const uint32_t* mask, long long mask_ld, int M, const int32_t* mask_rows,
-                           cudaStream_t stream);
+                           int nsm, cudaStream_t stream);
 size_t distill_workspace_bytes(int N, int V, int K);
 // norm_in: the gradient alone, from an earlier call's normalisers (then loss, parts and norm are NULL).
 cudaError_t launch_distill(int N, int V, float T, int bf16, const void* logits, long long ld, int K,
                            const int32_t* ids, const float* logq, const float* weight, float a_kl, float a_l1,
                            int rest, const float* norm_in, float* loss, float* parts, float* norm, void* grad,
-                           long long gld, int stuck, void* workspace, cudaStream_t stream);
+                           long long gld, int stuck, void* workspace, int nsm, cudaStream_t stream);
 
 }  // namespace dspark

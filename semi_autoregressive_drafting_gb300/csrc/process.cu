@@ -39,7 +39,7 @@ constexpr int kSlice = 8192, kSliceOne = 16384;   // with several rows, with one
 // Where a text may have this many tokens for each entry that a block copies, its blocks have more threads and larger
 // slices, which read it fewer times (8 requests with texts of up to 131072: 22 us, with small blocks 51).
 constexpr int kLong = 3, kThrLong = 1024, kSliceLong = 16384;
-constexpr int kFill = 152, kLeast = 512;   // SMs to fill; slices are multiples of this
+constexpr int kLeast = 512;                // slices are multiples of this
 constexpr int kRound = 8192;               // what a block takes besides its copies, in entries
 constexpr int kChunk = 256;                // entries that a warp looks through for touched ones, in the gradient
 constexpr int kListed = 128;               // touched entries of a unit that a warp lists at a time
@@ -618,34 +618,34 @@ cudaError_t launch(int B, const TI* in, TO* out, const TO* raw, PrArgs a, int S,
 }
 
 template <typename TI, typename TO, bool GRAD, int COUNT>
-cudaError_t run_count(int B, const TI* in, TO* out, const TO* raw, const PrArgs& a, cudaStream_t stream) {
-  const int S = slice_of(B, a.V, !GRAD && a.R == 1 ? kSliceOne : kSlice, 2 * kFill);
+cudaError_t run_count(int B, const TI* in, TO* out, const TO* raw, const PrArgs& a, int nsm, cudaStream_t stream) {
+  const int S = slice_of(B, a.V, !GRAD && a.R == 1 ? kSliceOne : kSlice, 2 * nsm);
   if (a.H / a.R >= kLong * (long long)(S < a.V ? S : a.V))
-    return launch<TI, TO, GRAD, COUNT, kThrLong>(B, in, out, raw, a, slice_of(B, a.V, kSliceLong, kFill), stream);
+    return launch<TI, TO, GRAD, COUNT, kThrLong>(B, in, out, raw, a, slice_of(B, a.V, kSliceLong, nsm), stream);
   return launch<TI, TO, GRAD, COUNT, kThr>(B, in, out, raw, a,
-                                           even_slice(B, a.V, S, kFill * (GRAD ? kBlocksGrad : kBlocks)), stream);
+                                           even_slice(B, a.V, S, nsm * (GRAD ? kBlocksGrad : kBlocks)), stream);
 }
 
 template <typename TI, typename TO, bool GRAD>
-cudaError_t run(int B, const TI* in, TO* out, const TO* raw, PrArgs a, cudaStream_t stream) {
+cudaError_t run(int B, const TI* in, TO* out, const TO* raw, PrArgs a, int nsm, cudaStream_t stream) {
   if constexpr (GRAD) {
     a.nb = 0;
-    return run_count<TI, TO, GRAD, kNoCount>(B, in, out, raw, a, stream);
+    return run_count<TI, TO, GRAD, kNoCount>(B, in, out, raw, a, nsm, stream);
   } else {
-    return a.H + a.R <= 65535 ? run_count<TI, TO, GRAD, kCount16>(B, in, out, raw, a, stream)
-                              : run_count<TI, TO, GRAD, kCount32>(B, in, out, raw, a, stream);
+    return a.H + a.R <= 65535 ? run_count<TI, TO, GRAD, kCount16>(B, in, out, raw, a, nsm, stream)
+                              : run_count<TI, TO, GRAD, kCount32>(B, in, out, raw, a, nsm, stream);
   }
 }
 
 template <bool GRAD>
 cudaError_t run_types(int B, int i_bf16, const void* in, int o_bf16, void* out, const void* raw, const PrArgs& a,
-                      cudaStream_t stream) {
+                      int nsm, cudaStream_t stream) {
   using H = __nv_bfloat16;
   if (i_bf16)
-    return o_bf16 ? run<H, H, GRAD>(B, (const H*)in, (H*)out, (const H*)raw, a, stream)
-                  : run<H, float, GRAD>(B, (const H*)in, (float*)out, (const float*)raw, a, stream);
-  return o_bf16 ? run<float, H, GRAD>(B, (const float*)in, (H*)out, (const H*)raw, a, stream)
-                : run<float, float, GRAD>(B, (const float*)in, (float*)out, (const float*)raw, a, stream);
+    return o_bf16 ? run<H, H, GRAD>(B, (const H*)in, (H*)out, (const H*)raw, a, nsm, stream)
+                  : run<H, float, GRAD>(B, (const H*)in, (float*)out, (const float*)raw, a, nsm, stream);
+  return o_bf16 ? run<float, H, GRAD>(B, (const float*)in, (H*)out, (const H*)raw, a, nsm, stream)
+                : run<float, float, GRAD>(B, (const float*)in, (float*)out, (const float*)raw, a, nsm, stream);
 }
 
 }  // namespace
@@ -656,7 +656,7 @@ cudaError_t launch_process(int grad, int B, int R, int V, int i_bf16, const void
                            const int32_t* drafted, const float* repetition, const float* presence,
                            const float* frequency, int nb, const int32_t* bias_tokens, const float* bias,
                            const uint32_t* mask, long long mask_ld, int M, const int32_t* mask_rows,
-                           cudaStream_t stream) {
+                           int nsm, cudaStream_t stream) {
   PrArgs a;
   a.R = R;
   a.V = V;
@@ -680,8 +680,8 @@ cudaError_t launch_process(int grad, int B, int R, int V, int i_bf16, const void
   a.bias = bias;
   a.mask = mask;
   a.mask_rows = mask_rows;
-  return grad ? run_types<true>(B, i_bf16, in, o_bf16, out, raw, a, stream)
-              : run_types<false>(B, i_bf16, in, o_bf16, out, raw, a, stream);
+  return grad ? run_types<true>(B, i_bf16, in, o_bf16, out, raw, a, nsm, stream)
+              : run_types<false>(B, i_bf16, in, o_bf16, out, raw, a, nsm, stream);
 }
 
 }  // namespace dspark
