@@ -487,8 +487,8 @@ dspark_status dspark_process_logits_grad(int B, int R, int V, dspark_dtype gdt, 
  *               stride)
  *   workspace   dspark_distill_workspace_bytes(N, V, K) bytes, 256-byte aligned, zeroed once before the first
  *               call; it serves smaller calls too
- * Masked logits are -inf: p = 0.  A teacher's token that the student masks makes KL +inf; the gradient is
- * the formula's.  A row that is -inf everywhere has p = 0 throughout and norm (-inf, 0, -inf, 0).  NaN or
+ * Masked logits are -inf: p = 0.  A teacher's token that the student masks makes KL +inf, however small its q;
+ * elsewhere a q below e^-87 counts as 0.  The gradient is the formula's.  A row that is -inf everywhere has p = 0 throughout and norm (-inf, 0, -inf, 0).  NaN or
  * +inf logits make their row's outputs NaN (but the maxima).  Sums in fp32 in a fixed order (a row has the same
  * bits in calls of any N), and the outcomes in pairs of fp32 numbers where one would round away what the sums
  * hold.  For rows of up to 3.2 MB one launch with grad_logits (their logits are read once), and for the loss

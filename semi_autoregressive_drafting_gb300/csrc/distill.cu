@@ -380,7 +380,8 @@ __device__ __forceinline__ void row_loss(const Outcomes& y, const RowSm& sm, con
     const int j = i * 32 + lane;
     if (j >= a.K || !in_vocabulary(sm.id[j], a.V)) continue;
     const Two q = sm.q[j], lp = sm.z[j] == -INFINITY ? never : minus(scaled(sm.z[j], y.mall, inv), ls);
-    kl += q.hi != 0.f ? q.hi * ((sm.lq[j] - lp.hi) - lp.lo) : 0.f;
+    // (below e^-87 q counts as 0, but a token that the student rules out is no less ruled out for that)
+    kl += q.hi != 0.f ? q.hi * ((sm.lq[j] - lp.hi) - lp.lo) : sm.lq[j] > -INFINITY && lp.hi == -INFINITY ? INFINITY : 0.f;
     l1 += fabsf((y.p[i] - q.hi) - q.lo);
   }
 #pragma unroll
