@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(512) tv_label_kernel(int V, float invT, const 
   __shared__ float sm[4][16];
   const size_t base = (size_t)blockIdx.x * V;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
-  float md = -INFINITY, ld = 0.f, mt = -INFINITY, lt = 0.f;
+  float md = kNoMax, ld = 0.f, mt = kNoMax, lt = 0.f;
   for (int v = tid; v < V; v += blockDim.x) {
     lse_push(md, ld, dl[base + v] * invT);
     lse_push(mt, lt, tl[base + v] * invT);

@@ -129,6 +129,9 @@ __device__ __forceinline__ float key_score(unsigned long long key) {
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
 }
 
+// The maximum that a running (max, sum-exp) begins with, below every finite entry that counts and not -inf: a
+// masked entry, -inf, then adds exp(-inf) = 0 in front of the first other one too, where -inf - -inf would be NaN.
+constexpr float kNoMax = -3.402823466e38f;
 // Running state of one (request, vocab subset): Gumbel-max winner and online log-sum-exp.
 struct RowState {
   float best;     // winning perturbed score
@@ -138,14 +141,14 @@ struct RowState {
 __device__ __forceinline__ void rs_init(RowState& s) {
   s.best = -INFINITY;
   s.tok = 0xFFFFFFFFu;
-  s.m = -INFINITY;
+  s.m = kNoMax;
   s.l = 0.f;
 }
 __device__ __forceinline__ void lse_push(float& m, float& l, float y) {
   if (y > m) {
     l = l * __expf(m - y) + 1.f;
     m = y;
-  } else if (y != -INFINITY) {  // (a masked entry adds nothing, also in front of the first other one)
+  } else {
     l += __expf(y - m);
   }
 }

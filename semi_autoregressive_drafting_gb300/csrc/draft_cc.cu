@@ -402,11 +402,7 @@ __device__ __forceinline__ float2 warp_merge_ml(const float2* part, int n, int l
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
     const float Mn = fmaxf(M, mb);  // the same in every lane
-    if (Mn == -INFINITY) {  // masked entries alone: zeros, and NaN stays
-#pragma unroll
-      for (int j = 0; j < 8; ++j) L += q[j].y;
-      continue;
-    }
+    if (Mn == -INFINITY) continue;
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum += q[j].y * __expf(q[j].x - Mn);
@@ -452,9 +448,9 @@ __device__ __forceinline__ void fill_noise(float* gbuf, int SLM, int SL, int v0,
 __device__ __forceinline__ void slot_init(Slot& s) {
   s.best = -INFINITY;
   s.tok = 0xFFFFFFFFu;
-  s.m = -INFINITY;
+  s.m = kNoMax;
   s.l = 0.f;
-  s.mt = -INFINITY;
+  s.mt = kNoMax;
   s.lt = 0.f;
 }
 // Row dot-product accumulation for one 16-byte W2 chunk against this lane's K-chunk of e.

@@ -143,7 +143,7 @@ __device__ __forceinline__ float ld_u(const void* p, size_t i, int bf16) {
 __device__ __forceinline__ void tslot_init(TSlot& s) {
   s.best = -INFINITY;
   s.tok = 0xFFFFFFFFu;
-  s.m = -INFINITY;
+  s.m = kNoMax;
   s.l = 0.f;
   s.mt = -INFINITY;
   s.lt = 0.f;
@@ -194,11 +194,7 @@ __device__ __forceinline__ float2 merge_ml(const float2* part, int n, int lane) 
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
     const float Mn = fmaxf(M, mb);  // the same in every lane
-    if (Mn == -INFINITY) {  // masked entries alone: zeros, and NaN stays
-#pragma unroll
-      for (int j = 0; j < 8; ++j) L += q[j].y;
-      continue;
-    }
+    if (Mn == -INFINITY) continue;
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum += q[j].y * __expf(q[j].x - Mn);
@@ -334,7 +330,7 @@ __global__ void __launch_bounds__(kTThr) target_part_kernel(const float* __restr
   const int b = (int)(row / G), k = (int)(row % G);
   const float* t = tgt + row * V;
   const int v0 = ch * kTChunk, v1 = min(V, v0 + kTChunk);
-  float m = -INFINITY, l = 0.f;  // log2 units here
+  float m = kNoMax, l = 0.f;  // log2 units here
   if ((V & 3) == 0) {  // 16-byte aligned rows: all sixteen loads of a thread at once
     const float4* t4 = (const float4*)(t + v0);
     const int n4 = (v1 - v0) >> 2;
@@ -347,19 +343,18 @@ __global__ void __launch_bounds__(kTThr) target_part_kernel(const float* __restr
     float mx = -INFINITY;
 #pragma unroll
     for (int u = 0; u < kTChunk / 4 / kTThr; ++u) mx = fmaxf(mx, fmaxf(fmaxf(q[u].x, q[u].y), fmaxf(q[u].z, q[u].w)));
-    m = mx * s2;
-    const float ref = mx == -INFINITY ? 0.f : m;  // (all entries masked: zeros, and NaN stays)
+    m = fmaxf(mx * s2, kNoMax);  // (all entries masked: zeros, and NaN stays)
 #pragma unroll
     for (int u = 0; u < kTChunk / 4 / kTThr; ++u)
-      l += ex2f(fmaf(q[u].x, s2, -ref)) + ex2f(fmaf(q[u].y, s2, -ref)) + ex2f(fmaf(q[u].z, s2, -ref)) +
-           ex2f(fmaf(q[u].w, s2, -ref));
+      l += ex2f(fmaf(q[u].x, s2, -m)) + ex2f(fmaf(q[u].y, s2, -m)) + ex2f(fmaf(q[u].z, s2, -m)) +
+           ex2f(fmaf(q[u].w, s2, -m));
   } else {
     for (int v = v0 + (int)threadIdx.x; v < v1; v += kTThr) {
       const float y = t[v] * s2;
       if (y > m) {
         l = l * ex2f(m - y) + 1.f;
         m = y;
-      } else if (y != -INFINITY) {  // (a masked entry adds nothing, also in front of the first other one)
+      } else {
         l += ex2f(y - m);
       }
     }
@@ -747,18 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       wd[0] = r0.x; wd[1] = r0.y; wd[2] = r0.z; wd[3] = r0.w;
       wd[4] = r1.x; wd[5] = r1.y; wd[6] = r1.z; wd[7] = r1.w;
     }
-    auto store_y = [&]() {  // (the target's normalisers come from target_part_kernel)
-      float* yo = ybp + (size_t)b * V + v;  // y2 = z s2, read back by the second pass
-      if (FAST || (vec_t && full)) {
-        *(float4*)yo = make_float4(z[0] * s2, z[1] * s2, z[2] * s2, z[3] * s2);
-        *(float4*)(yo + 4) = make_float4(z[4] * s2, z[5] * s2, z[6] * s2, z[7] * s2);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (v + e < V) yo[e] = z[e] * s2;
-      }
-    };
-    if (st.m == -INFINITY) {  // the row's first group: the normaliser's reference point, and
+    if (st.m == kNoMax) {  // the row's first group: the normaliser's reference point, and
       // the running best seeded with the exact score of the group's largest entry (a real
       // score, so a lower bound of the row's best: without it every entry of the group would be
       // a candidate).  That entry is tested again below and changes nothing.
@@ -770,22 +754,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           zs = z[e];
           es = e;
         }
-      st.m = zs * s2;
-      if (st.m == -INFINITY) {  // all eight are masked: nothing to add, and the next group is the first
-        if (TGT) store_y();
-        return;
-      }
-      uint32_t ws = wd[0];
+      // (all eight masked: they add 2^-inf = 0, and the next group is the first)
+      st.m = fmaxf(zs * s2, kNoMax);
+      if (zs != -INFINITY) {
+        uint32_t ws = wd[0];
 #pragma unroll
-      for (int e = 1; e < 8; ++e)
-        if (es == e) ws = wd[e];
-      const float sc = zs * s2 - gumbel_log2(ws);
-      if (sc > st.best || (sc == st.best && (uint32_t)(v + es) < st.tok)) {
-        st.best = sc;
-        st.tok = (uint32_t)(v + es);
+        for (int e = 1; e < 8; ++e)
+          if (es == e) ws = wd[e];
+        const float sc = zs * s2 - gumbel_log2(ws);
+        if (sc > st.best || (sc == st.best && (uint32_t)(v + es) < st.tok)) {
+          st.best = sc;
+          st.tok = (uint32_t)(v + es);
+        }
+        *sb_own = st.best;
+        tb = fmaxf(tb, st.best);
       }
-      *sb_own = st.best;
-      tb = fmaxf(tb, st.best);
       Cp = 1.002f * ex2f(st.m - tb);
     }
     const float2 s22 = make_float2(s2, s2);
@@ -856,7 +839,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     lsum = __fadd2_rn(lsum, gs);
-    if (TGT) store_y();
+    if (TGT) {  // the target's normalisers come from target_part_kernel
+      float* yo = ybp + (size_t)b * V + v;  // y2 = z s2, read back by the second pass
+      if (FAST || (vec_t && full)) {
+        *(float4*)yo = make_float4(z[0] * s2, z[1] * s2, z[2] * s2, z[3] * s2);
+        *(float4*)(yo + 4) = make_float4(z[4] * s2, z[5] * s2, z[6] * s2, z[7] * s2);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (v + e < V) yo[e] = z[e] * s2;
+      }
+    }
   };
 
   // Eq 8 of step kp over this block's slice, once every block has published step kp.
@@ -898,9 +891,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int j = 0; j < 20; ++j) sum += q[j].y * __expf(q[j].x - mb);
               M = mb;
               L = sum;
-            } else {  // masked entries alone: zeros, and NaN stays
-#pragma unroll
-              for (int j = 0; j < 20; ++j) L += q[j].y;
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) lse_merge(Mt, Lt, qt[j].x, qt[j].y);

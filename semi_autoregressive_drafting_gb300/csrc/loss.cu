@@ -39,6 +39,16 @@ __device__ __forceinline__ float ex2l(float x) {
   return y;
 }
 
+// an entry y into (m, l = sum 2^(y - m)), which begins with (kNoMax, 0)
+__device__ __forceinline__ void push_l2(float& m, float& l, float y) {
+  if (y > m) {
+    l = l * ex2l(m - y) + 1.f;
+    m = y;
+  } else {
+    l += ex2l(y - m);
+  }
+}
+
 __device__ __forceinline__ void merge_l2(float& m, float& l, float m2, float l2) {
   if (l2 == 0.f) return;
   if (l == 0.f) {
@@ -118,7 +128,7 @@ __global__ void __launch_bounds__(kLThr) loss_part_kernel(const float* __restric
   const int v0 = ch * kLChunk, v1 = min(V, v0 + kLChunk);
   const float* d = zd + row * V;
   const float* t = zt + row * V;
-  float md = -INFINITY, ld = 0.f, mt = -INFINITY, lt = 0.f;
+  float md = kNoMax, ld = 0.f, mt = kNoMax, lt = 0.f;
   if ((V & 3) == 0) {
     Chunk c;
     load_chunk<false>(c, d + v0, t + v0, (v1 - v0) >> 2);
@@ -128,22 +138,30 @@ __global__ void __launch_bounds__(kLThr) loss_part_kernel(const float* __restric
       xd = fmaxf(xd, fmaxf(fmaxf(c.d[u].x, c.d[u].y), fmaxf(c.d[u].z, c.d[u].w)));
       xt = fmaxf(xt, fmaxf(fmaxf(c.t[u].x, c.t[u].y), fmaxf(c.t[u].z, c.t[u].w)));
     }
-    md = xd * s2;
-    mt = xt * s2;
-    // (all entries masked: 2^-inf = 0 against a reference of 0, and NaN stays)
-    const float rd = xd == -INFINITY ? 0.f : md, rt = xt == -INFINITY ? 0.f : mt;
+    if (xd != -INFINITY || xt != -INFINITY) {
+      md = fmaxf(xd * s2, kNoMax);
+      mt = fmaxf(xt * s2, kNoMax);
 #pragma unroll
-    for (int u = 0; u < kLPer; ++u) {
-      ld += ex2l(fmaf(c.d[u].x, s2, -rd)) + ex2l(fmaf(c.d[u].y, s2, -rd)) +
-            ex2l(fmaf(c.d[u].z, s2, -rd)) + ex2l(fmaf(c.d[u].w, s2, -rd));
-      lt += ex2l(fmaf(c.t[u].x, s2, -rt)) + ex2l(fmaf(c.t[u].y, s2, -rt)) +
-            ex2l(fmaf(c.t[u].z, s2, -rt)) + ex2l(fmaf(c.t[u].w, s2, -rt));
+      for (int u = 0; u < kLPer; ++u) {
+        ld += ex2l(fmaf(c.d[u].x, s2, -md)) + ex2l(fmaf(c.d[u].y, s2, -md)) +
+              ex2l(fmaf(c.d[u].z, s2, -md)) + ex2l(fmaf(c.d[u].w, s2, -md));
+        lt += ex2l(fmaf(c.t[u].x, s2, -mt)) + ex2l(fmaf(c.t[u].y, s2, -mt)) +
+              ex2l(fmaf(c.t[u].z, s2, -mt)) + ex2l(fmaf(c.t[u].w, s2, -mt));
+      }
+    } else {  // nothing but masked entries, or NaN
+#pragma unroll
+      for (int u = 0; u < kLPer; ++u) {
+        ld += (c.d[u].x + c.d[u].y) + (c.d[u].z + c.d[u].w);
+        lt += (c.t[u].x + c.t[u].y) + (c.t[u].z + c.t[u].w);
+      }
+      ld = isnan(ld) ? ld : 0.f;
+      lt = isnan(lt) ? lt : 0.f;
     }
   } else {
     for (int v = v0 + (int)threadIdx.x; v < v1; v += kLThr) {
       const float yd = d[v] * s2, yt = t[v] * s2;
-      if (yd != -INFINITY) merge_l2(md, ld, yd, 1.f);
-      if (yt != -INFINITY) merge_l2(mt, lt, yt, 1.f);
+      push_l2(md, ld, yd);
+      push_l2(mt, lt, yt);
     }
   }
 #pragma unroll
@@ -207,7 +225,7 @@ __device__ __forceinline__ float2 references(float2 L) {
   return make_float2(L.x == -INFINITY ? 0.f : L.x, L.y == -INFINITY ? 0.f : L.y);
 }
 
-__device__ __forceinline__ float sgn(float x) { return x > 0.f ? 1.f : (x < 0.f ? -1.f : x); }  // (0, or NaN)
+__device__ __forceinline__ float sgn(float x) { return x > 0.f ? 1.f : (x < 0.f ? -1.f : 0.f); }
 
 // ------------------------------------------------------------------ 2. |p - q| and s p sums
 // (the blocks take the chunks in reverse order, so that the first ones read the rows the
@@ -275,6 +293,7 @@ __global__ void __launch_bounds__(kLThr, 3) loss_grad_kernel(
   for (int ch2 = lane; ch2 < nchunk; ch2 += 32) S += ws.stat[row * nchunk + ch2].y;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
+  if (!isfinite(L.x) || !isfinite(L.y)) S = NAN;  // NaN or +inf in either row
   const int k0 = (int)(row % G);  // position k - 1
   const float wT = __expf(-(float)k0 / (float)G) * invT;
   auto gv = [&](float a, float b, int v) {
