@@ -213,7 +213,8 @@ dspark_status dspark_prefix_schedule(int B, int gamma, const float* S, const dou
  * Masked entries are -inf, in rows of the draft and of the target: their probability is 0, so a token that
  * the target masks is neither accepted nor drawn.  Where the target's row to draw from is -inf everywhere there is
  * nothing to draw: n_accepted = n as usual, out_tokens[n] = -1, and the status stays DSPARK_OK.  A draft row
- * that is -inf everywhere is rejected, and its correction drawn from q_j.
+ * that is -inf everywhere is rejected, and its correction drawn from q_j.  A row with a NaN is taken for one that is
+ * -inf everywhere.
  * Limits: 1 <= gamma <= 16, 2 <= V <= 2^24, T finite and > 0.  Three launches on `stream`.
  * A drafted token outside [0, V) gives that request n_accepted = -1 and out_tokens -1, and sets
  * DSPARK_ERR_INVALID in the workspace status (read with dspark_get_status).

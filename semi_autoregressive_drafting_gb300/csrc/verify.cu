@@ -123,6 +123,10 @@ __global__ void __launch_bounds__(kThr) verify_part_kernel(const float* __restri
         a1 += ex2v(fmaf(q[u].z, s2, -m)) + ex2v(fmaf(q[u].w, s2, -m));
       }
       l = a0 + a1;
+    } else {  // nothing but masked entries, or NaN, which stays
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) l += (q[u].x + q[u].y) + (q[u].z + q[u].w);
+      l = isnan(l) ? l : 0.f;
     }
   } else {
     for (int v = v0 + (int)threadIdx.x; v < v1; v += kThr) {

@@ -36,3 +36,25 @@ def test_rows_that_nothing_is_left_of(V, oracle_mod):
     # the workspace is ready for the next call
     again = ds.verify(zd.cuda(), zt.cuda(), tok.cuda(), seed=3, workspace=ws)
     assert torch.equal(again[0].cpu(), n) and torch.equal(again[1].cpu(), out)
+
+
+@pytest.mark.parametrize("V", [4096, 4001, 40000])
+def test_rows_with_nan(V):
+    # NaN is met wherever it stands, also where a mask leaves nothing else of a thread's entries
+    B, G = 5, 3
+    t = inputs.verify_inputs(B, G, V, seed=V + 1, target_noise=0.0, tokens="argmax")
+    zd, zt, tok = t["draft_logits"], t["target_logits"], t["draft_tokens"]
+    nan = float("nan")
+    zt[0, 1, V // 2] = nan
+    keep = zt[1, 2, int(tok[1, 2])].clone()
+    zt[1, 2] = -INF
+    zt[1, 2, int(tok[1, 2])], zt[1, 2, (int(tok[1, 2]) + 1501) % V] = keep, nan
+    zt[2, G] = -INF
+    zt[2, G, 7] = nan
+    zd[3, 0, V - 1] = nan
+    zt[4] = nan
+    n, out = (x.cpu() for x in ds.verify(zd.cuda(), zt.cuda(), tok.cuda(), seed=3))
+    assert n.tolist() == [1, 2, G, 0, 0]
+    for b in (0, 1, 2, 4):
+        assert (out[b, int(n[b]):] == -1).all() and (out[b, :int(n[b])] == tok[b, :int(n[b])]).all()
+    assert out[3, 0] >= 0 and (out[3, 1:] == -1).all()
