@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kThr) verify_part_kernel(const float* __restri
   const int ch = (int)(blk % nchunk);
   const float* z = row < nd_rows ? zd + row * V : zt + (row - nd_rows) * V;
   const int v0 = ch * kChunk, v1 = min(V, v0 + kChunk);
-  float m = -INFINITY, l = 0.f;
+  float m = kNoMax, l = 0.f;
   if ((V & 3) == 0) {  // rows are 16-byte aligned: the chunk's sixteen loads per thread at once
     const float4* z4 = (const float4*)(z + v0);
     const int n4 = (v1 - v0) >> 2;
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThr) verify_part_kernel(const float* __restri
       if (y > m) {
         l = l * ex2v(m - y) + 1.f;
         m = y;
-      } else if (y != -INFINITY) {  // (a masked entry adds nothing, also in front of the first other one)
+      } else {  // (a masked entry adds 2^-inf = 0, also in front of the first other one)
         l += ex2v(y - m);
       }
     }
