@@ -21,7 +21,7 @@
 // of shared memory hold rows, for 11 us each, of which the loads take 3, the sums 2, the exchange and the outcomes
 // 4 and the gradient 2.5 (resident clusters that load the next row behind the gradient: 838; blocks of half the
 // size, twice as many: 1010).  448 x 151936 fp32: 116 us (4.7 TB/s).  The gradient alone: 540 and 84 us (6.95 and 6.5
-// TB/s); the loss alone, 499 x 50021 fp32: 28 us, two launches.  The teacher's part is hidden behind the loads.
+// TB/s); the loss alone, 499 x 50021 fp32: 29 us, two launches.  The teacher's part is hidden behind the loads.
 #include "common.cuh"
 #include "kernels.h"
 #include "rows.cuh"

@@ -21,6 +21,8 @@
 //   4. loss_final_kernel: one warp per request, one lane per position: c*, the three terms, the
 //      confidence gradient, and the per-request sums.
 // Each launch reads the rows once: three reads of every logit row and one gradient write.
+// Masked entries are -inf, in either row: the running maxima begin at kNoMax, so that 2^(-inf - max) = 0 without a
+// test per entry, and a row that is -inf everywhere is told by its normaliser, -inf.
 #include "common.cuh"
 #include "kernels.h"
 

@@ -33,11 +33,11 @@ constexpr int kThr = 256;                  // threads of a block
 // logits, the touched ones), which the other blocks' copies and a larger slice hide; slices much larger leave few
 // blocks, and five blocks leave a thread too few registers to copy and list.  512 x 1 rows: 128 us with slices of
 // 8192, 117 with 16384; 64 x 8 rows: 98 with 4096, 93 with 8192, 114 with 12288, 151 with five blocks.  The gradient,
-// 512 x 7 rows: 690 us with four blocks, 631 with five, 727 with six.
+// 512 x 7 rows of 262144 bf16: 690 us with four blocks, 631 with five, 727 with six.
 constexpr int kBlocks = 4, kBlocksGrad = 5;
 constexpr int kSlice = 8192, kSliceOne = 16384;   // with several rows, with one
 // Where a text may have this many tokens for each entry that a block copies, its blocks have more threads and larger
-// slices, which read it fewer times (8 requests with texts of up to 131072: 22 us, with small blocks 51).
+// slices, which read it fewer times (8 requests of 262144 bf16 with texts of up to 131072: 25 us, with small blocks 51).
 constexpr int kLong = 3, kThrLong = 1024, kSliceLong = 16384;
 constexpr int kLeast = 512;                // slices are multiples of this
 constexpr int kRound = 8192;               // what a block takes besides its copies, in entries
