@@ -21,6 +21,8 @@
  *     workspace and read back with dspark_get_status().
  *   - dtypes: `wdt` applies to the weights (W1, W2, w, Wj), `udt` to the activations (U, h).
  *     DSPARK_BF16 arrays hold raw bfloat16; fp32 accumulation everywhere.
+ *   - Masked logits are -inf: their probability is 0.  Beside entries that are not masked the type's lowest
+ *     number serves too; each call says what a row gives that is -inf everywhere.
  *   - Limits: 1 <= gamma <= 16, 2 <= V <= 2^24, r and d multiples of 8 (d may be 0 when the
  *     confidence head is not used), 8 <= r <= 512, T finite and > 0.
  *

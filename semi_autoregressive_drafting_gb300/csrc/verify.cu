@@ -115,7 +115,8 @@ __global__ void __launch_bounds__(kThr) verify_part_kernel(const float* __restri
 #pragma unroll
     for (int u = 0; u < kPer; ++u) mx = fmaxf(mx, fmaxf(fmaxf(q[u].x, q[u].y), fmaxf(q[u].z, q[u].w)));
     if (mx != -INFINITY) {
-      m = mx * s2;  // the scale is positive and rounding monotone: the max of z s2
+      // the scale is positive and rounding monotone: the max of z s2 (-inf where the type's lowest number masks)
+      m = fmaxf(mx * s2, kNoMax);
       float a0 = 0.f, a1 = 0.f;
 #pragma unroll
       for (int u = 0; u < kPer; ++u) {
